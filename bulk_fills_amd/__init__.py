@@ -33,6 +33,7 @@ except ImportError:  # the C library still loads on its own
 lib = C.CDLL(LIB_PATH)
 
 TK_OK, TK_EINVAL, TK_ERANGE, TK_ENOMEM, TK_EHIP = 0, 1, 2, 3, 4
+TK_RESIDUAL_F32, TK_PARAMS_F32 = 1, 2  # flags of the row operators
 
 _u32, _u64, _i32, _i64, _f32 = C.c_uint32, C.c_uint64, C.c_int32, C.c_int64, C.c_float
 _p = C.c_void_p
@@ -84,6 +85,18 @@ SIGNATURES = {
     "tk_fill_constant_u32": [_u32, _u64, _p, _p],
     "tk_fill_normal_f64_no_alloc": [_u32, _u64, _u64, _p, _p],
 }
+for _t in ("f32", "f16", "bf16"):
+    SIGNATURES.update({
+        f"tk_dropout_add_{_t}": [_u32, _u64, _u64, _u64, _f32, _u32, _p, _u64, _p, _p, _u64, _p, _u64, _p],
+        f"tk_dropout_add_backward_{_t}": [_u32, _u64, _u64, _u64, _f32, _u32, _p, _u64, _p, _u64, _p, _p, _u64, _p],
+        f"tk_layer_norm_{_t}": [_u64, _u64, _f32, _u32, _p, _u64, _p, _p, _p, _u64, _p, _p, _p],
+        f"tk_layer_norm_backward_{_t}": [_u64, _u64, _u32, _p, _u64, _p, _u64, _p, _p, _p, _p, _u64, _p, _p, _p, _u64, _p],
+        f"tk_dropout_add_layer_norm_{_t}": [_u32, _u64, _u64, _u64, _f32, _f32, _u32, _p, _u64, _p, _p, _u64, _p, _p, _p,
+                                            _u64, _p, _u64, _p, _p, _p],
+        f"tk_dropout_add_layer_norm_backward_{_t}": [_u32, _u64, _u64, _u64, _f32, _u32, _p, _u64, _p, _u64, _p, _u64, _p,
+                                                     _p, _p, _p, _u64, _p, _u64, _p, _p, _p, _p, _u64, _p],
+    })
+SIGNATURES["tk_backward_workspace_bytes"] = [_u64, _u64, _p]
 for _name, _args in SIGNATURES.items():
     _fn = getattr(lib, _name)
     _fn.argtypes = _args
@@ -223,6 +236,181 @@ def tk_dropout_backward_f32(key, start_draw, n, p, dy, dx, stream=None):
     _check(lib.tk_dropout_backward_f32(key, start_draw, n, p, _buf(dy, 4, n, "tk_dropout_backward_f32"),
                                        _buf(dx, 4, n, "tk_dropout_backward_f32"), _stream(stream, dx)),
            "tk_dropout_backward_f32")
+
+
+def tk_backward_workspace_bytes(rows, cols):
+    """Device bytes that the row operators' backward calls need for their column sums."""
+    v = C.c_uint64()
+    _check(lib.tk_backward_workspace_bytes(rows, cols, C.byref(v)), "tk_backward_workspace_bytes")
+    return v.value
+
+
+class _Args:
+    """Checks and marshals one row operator's buffers.  A matrix is a tensor of rows x cols (any
+    shape that flattens to it, the last dimension contiguous), whose row distance is taken where
+    the call gives None for its ld; or a raw address (ld None: cols)."""
+
+    __slots__ = ("where", "rows", "cols", "dtype", "residual", "params", "device")
+
+    def __init__(self, where, rows, cols, dtype, flags):
+        self.where, self.rows, self.cols, self.dtype = where, rows, cols, dtype
+        self.residual = torch.float32 if flags & TK_RESIDUAL_F32 else dtype
+        self.params = torch.float32 if flags & TK_PARAMS_F32 else dtype
+        self.device = None
+
+    def _tensor(self, x, dtype):
+        if x.dtype is not dtype:
+            raise ValueError(f"{self.where}: a buffer's type is {x.dtype}, not {dtype}")
+        index = x.get_device()  # -1 on the host
+        if index != self.device:
+            if index < 0:
+                raise ValueError(f"{self.where}: buffer must live on a HIP device")
+            if index != torch.cuda.current_device():
+                # the library launches on the calling thread's current device
+                raise ValueError(f"{self.where}: buffer is on {x.device}, the current device is "
+                                 f"cuda:{torch.cuda.current_device()}")
+            self.device = index
+        return x.data_ptr()
+
+    def matrix(self, x, ld, dtype):
+        """(address, ld) of a matrix argument."""
+        if x is None:
+            return None, 0
+        if isinstance(x, int):
+            return x, self.cols if ld is None else ld
+        ptr = self._tensor(x, dtype)
+        if x.is_contiguous():
+            own = self.cols
+            fits = x.numel() == self.rows * self.cols and (ld is None or ld == own or self.rows <= 1)
+        else:
+            own = x.stride(-2) if x.dim() > 1 else self.cols
+            fits = tuple(x.shape) == (self.rows, self.cols) and (self.cols == 1 or x.stride(1) == 1)
+            if self.rows <= 1:  # one row has no distance to a next
+                own = self.cols
+            fits = fits and own >= self.cols and (ld is None or ld == own or self.rows <= 1)
+        if not fits:
+            raise ValueError(f"{self.where}: need a {self.rows} x {self.cols} matrix with contiguous rows that do not "
+                             f"overlap (and its own row distance as ld, or None), got shape {tuple(x.shape)}, strides "
+                             f"{x.stride()}, ld {ld}")
+        return ptr, own if ld is None else ld
+
+    def vector(self, x, n, dtype):
+        if x is None or isinstance(x, int):
+            return x
+        if x.numel() != n or not x.is_contiguous():
+            raise ValueError(f"{self.where}: need a contiguous vector of {n} elements, got shape {tuple(x.shape)}")
+        return self._tensor(x, dtype)
+
+    def raw_stream(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def workspace(self, x, stream, needed):
+        """(address, bytes, what keeps it alive).  None allocates it with torch, in the order of
+        the current stream: for a call on another stream the caller passes one."""
+        if x is None:
+            n = tk_backward_workspace_bytes(self.rows, self.cols) if needed else 0
+            if n == 0:
+                return None, 0, None
+            if stream is not None and self.raw_stream(stream) != self.raw_stream(None):
+                raise ValueError(f"{self.where}: a call on a stream that is not the current one needs a workspace")
+            x = torch.empty(n, dtype=torch.uint8, device="cuda")
+            return x.data_ptr(), n, x
+        if not x.is_contiguous():
+            raise ValueError(f"{self.where}: the workspace must be contiguous")
+        return self._tensor(x, x.dtype), x.numel() * x.element_size(), x
+
+
+def _row_operators(suffix, dtype):
+    """The row operators for one element type, under the names of their C entry points."""
+    add_fwd, add_bwd = getattr(lib, "tk_dropout_add_" + suffix), getattr(lib, "tk_dropout_add_backward_" + suffix)
+    norm_fwd, norm_bwd = getattr(lib, "tk_layer_norm_" + suffix), getattr(lib, "tk_layer_norm_backward_" + suffix)
+    both_fwd = getattr(lib, "tk_dropout_add_layer_norm_" + suffix)
+    both_bwd = getattr(lib, "tk_dropout_add_layer_norm_backward_" + suffix)
+
+    def dropout_add(key, start_draw, rows, cols, p, flags, x, ldx, bias, residual, ldr, y, ldy, stream=None):
+        where = "tk_dropout_add_" + suffix
+        a = _Args(where, rows, cols, dtype, flags)
+        px, ldx = a.matrix(x, ldx, dtype)
+        pr, ldr = a.matrix(residual, ldr, a.residual)
+        py, ldy = a.matrix(y, ldy, a.residual)
+        pb = a.vector(bias, cols, a.params)
+        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, a.raw_stream(stream)), where)
+
+    def dropout_add_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dx, lddx, dbias, workspace=None, stream=None):
+        where = "tk_dropout_add_backward_" + suffix
+        a = _Args(where, rows, cols, dtype, flags)
+        pdy, lddy = a.matrix(dy, lddy, a.residual)
+        pdx, lddx = a.matrix(dx, lddx, dtype)
+        pb = a.vector(dbias, cols, a.params)
+        ws, n, keep = a.workspace(workspace, stream, dbias is not None)
+        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, a.raw_stream(stream)), where)
+
+    def layer_norm(rows, cols, eps, flags, x, ldx, gamma, beta, y, ldy, mean=None, rstd=None, stream=None):
+        where = "tk_layer_norm_" + suffix
+        a = _Args(where, rows, cols, dtype, flags)
+        px, ldx = a.matrix(x, ldx, a.residual)
+        py, ldy = a.matrix(y, ldy, dtype)
+        pg, pb = a.vector(gamma, cols, a.params), a.vector(beta, cols, a.params)
+        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
+        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, a.raw_stream(stream)), where)
+
+    def layer_norm_backward(rows, cols, flags, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta,
+                            workspace=None, stream=None):
+        where = "tk_layer_norm_backward_" + suffix
+        a = _Args(where, rows, cols, dtype, flags)
+        pdy, lddy = a.matrix(dy, lddy, dtype)
+        px, ldx = a.matrix(x, ldx, a.residual)
+        pdx, lddx = a.matrix(dx, lddx, a.residual)
+        pg, pdg, pdb = (a.vector(v, cols, a.params) for v in (gamma, dgamma, dbeta))
+        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
+        ws, n, keep = a.workspace(workspace, stream, True)
+        _check(norm_bwd(rows, cols, flags, pdy, lddy, px, ldx, pg, pm, ps, pdx, lddx, pdg, pdb, ws, n,
+                        a.raw_stream(stream)), where)
+
+    def dropout_add_layer_norm(key, start_draw, rows, cols, p, eps, flags, x, ldx, bias, residual, ldr, gamma, beta, sum,
+                               lds, y, ldy, mean=None, rstd=None, stream=None):
+        where = "tk_dropout_add_layer_norm_" + suffix
+        a = _Args(where, rows, cols, dtype, flags)
+        px, ldx = a.matrix(x, ldx, dtype)
+        pr, ldr = a.matrix(residual, ldr, a.residual)
+        pv, lds = a.matrix(sum, lds, a.residual)
+        py, ldy = a.matrix(y, ldy, dtype)
+        pb, pg, pt = (a.vector(v, cols, a.params) for v in (bias, gamma, beta))
+        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
+        _check(both_fwd(key, start_draw, rows, cols, p, eps, flags, px, ldx, pb, pr, ldr, pg, pt, pv, lds, py, ldy, pm, ps,
+                        a.raw_stream(stream)), where)
+
+    def dropout_add_layer_norm_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, gamma, mean,
+                                        rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace=None, stream=None):
+        where = "tk_dropout_add_layer_norm_backward_" + suffix
+        a = _Args(where, rows, cols, dtype, flags)
+        pdy, lddy = a.matrix(dy, lddy, dtype)
+        pds, ldds = a.matrix(dsum, ldds, a.residual)
+        pv, lds = a.matrix(sum, lds, a.residual)
+        pdx, lddx = a.matrix(dx, lddx, dtype)
+        pdr, lddr = a.matrix(dresidual, lddr, a.residual)
+        pg, pdg, pdb, pdt = (a.vector(v, cols, a.params) for v in (gamma, dgamma, dbeta, dbias))
+        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
+        ws, n, keep = a.workspace(workspace, stream, True)
+        _check(both_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pds, ldds, pv, lds, pg, pm, ps, pdx, lddx, pdr,
+                        lddr, pdg, pdb, pdt, ws, n, a.raw_stream(stream)), where)
+
+    out = {}
+    for f in (dropout_add, dropout_add_backward, layer_norm, layer_norm_backward, dropout_add_layer_norm,
+              dropout_add_layer_norm_backward):
+        f.__name__ = f.__qualname__ = f"tk_{f.__name__}_{suffix}"
+        f.__doc__ = (f"{f.__name__}: see include/tk.h.  Matrices are rows x cols tensors (their ld may be None) or raw "
+                     "addresses" + (", and a workspace of None is allocated." if "backward" in f.__name__ else "."))
+        out[f.__name__] = f
+    return out
+
+
+if torch is not None:
+    globals().update(_row_operators("f32", torch.float32))
+    globals().update(_row_operators("f16", torch.float16))
+    globals().update(_row_operators("bf16", torch.bfloat16))
 
 
 class Alias:

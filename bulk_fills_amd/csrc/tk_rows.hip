@@ -1,0 +1,439 @@
+// tk_rows.hip -- entry points of the row operators: argument checks, how a backward call is
+// cut, and the kernel that adds up the partial column sums.
+#include <math.h>
+
+#include "tk_internal.h"
+#include "tk_rows_args.h"
+
+namespace tk {
+
+// ---------------------------------------------------------------------------------------
+// The end of the column sums: line k of the partial sums into element type float or the
+// parameters', one column a lane, the lines in a fixed order
+// ---------------------------------------------------------------------------------------
+struct FinishArgs {
+  const float *partial;
+  void *out[3];  // null: not wanted
+  uint64_t lines;
+  uint32_t cols;
+  int kind;  // 0 float, 1 binary16, 2 bfloat16
+};
+
+__global__ __launch_bounds__(256) void k_finish(FinishArgs a) {
+  __shared__ float part[4][64];
+  void *out = a.out[blockIdx.y];
+  if (!out) return;
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  const float *p = a.partial + (uint64_t)blockIdx.y * a.lines * a.cols + c;
+  float s = 0.0f;
+  if (c < a.cols)
+    for (uint64_t l = wave; l < a.lines; l += 4) s += p[l * a.cols];
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < a.cols) {
+    s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if (a.kind == 0) ((float *)out)[c] = s;
+    else if (a.kind == 1) ((_Float16 *)out)[c] = (_Float16)s;
+    else ((__bf16 *)out)[c] = (__bf16)s;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// How a backward call is cut
+// ---------------------------------------------------------------------------------------
+constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 40;
+constexpr uint64_t kRowsInRegisters = 16384;  // columns that k_norm_bwd's largest shape holds
+
+// Strips of 64 lanes' chunks by ranges of rows: about eight work-groups a compute unit, of at
+// least eight rows each.
+static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
+  BwdPlan p{};
+  p.strips = (cols + 64 * chunk - 1) / (64 * chunk);
+  uint64_t lines = (2048 + p.strips - 1) / p.strips;
+  if (lines > (rows + 7) / 8) lines = (rows + 7) / 8;
+  p.rows_per_block = (rows + lines - 1) / lines;
+  p.lines = (rows + p.rows_per_block - 1) / p.rows_per_block;
+  return p;
+}
+
+static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
+  if (cols > kRowsInRegisters) return strips_plan(chunk, rows, cols);
+  BwdPlan p{};
+  p.tpr = cols <= 128 ? 16 : cols <= 1024 ? 64 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
+  p.ept = cols <= 512 || (cols > 1024 && cols <= 2048) ? 8 : 16;
+  const uint64_t per = p.tpr < 256 ? 256 / p.tpr : 1, sets = (rows + per - 1) / per;
+  const uint64_t most = p.tpr <= 256 ? 1024 : 512;
+  p.lines = sets < most ? sets : most;
+  return p;
+}
+
+static uint64_t bytes_of(const BwdPlan &p, uint64_t cols) { return 12 * p.lines * cols; }
+
+// The larger of both chunk sizes and both kinds of call, so that one size serves every type.
+static uint64_t workspace_bytes(uint64_t rows, uint64_t cols) {
+  if (rows == 0 || cols == 0) return 0;
+  uint64_t b = 0;
+  for (int chunk = 4; chunk <= 8; chunk += 4) {
+    const uint64_t s = bytes_of(strips_plan(chunk, rows, cols), cols), n = bytes_of(norm_plan(chunk, rows, cols), cols);
+    b = s > b ? s : b;
+    b = n > b ? n : b;
+  }
+  return b + (cols > kRowsInRegisters ? 8 * rows : 0);
+}
+
+// ---------------------------------------------------------------------------------------
+// Argument checks
+// ---------------------------------------------------------------------------------------
+struct Region {
+  uintptr_t at;
+  uint64_t rows, pitch, width;  // bytes
+  int size;                     // element bytes
+  bool out, matrix;
+};
+
+// Whether two arguments share bytes in a way a call may not have: an output matrix may be an
+// input matrix; matrices of one pitch are told apart by their place within it.
+static bool clash(const Region &a, const Region &b) {
+  if (!a.out && !b.out) return false;
+  const uintptr_t ea = a.at + (a.rows - 1) * a.pitch + a.width, eb = b.at + (b.rows - 1) * b.pitch + b.width;
+  if (ea <= b.at || eb <= a.at) return false;
+  if (a.matrix && b.matrix) {
+    if (a.at == b.at && a.size == b.size && (a.pitch == b.pitch || a.rows == 1)) return a.out && b.out;
+    if (a.pitch == b.pitch && a.rows > 1) {
+      const uint64_t d = b.at >= a.at ? (b.at - a.at) % a.pitch : (a.pitch - (a.at - b.at) % a.pitch) % a.pitch;
+      return d < a.width || d + b.width > a.pitch;
+    }
+  }
+  return true;
+}
+
+enum RowType { kF32, kF16, kBF16 };
+
+struct Checker {
+  RowType type;
+  uint64_t rows, cols;
+  uint32_t flags;
+  Region r[14];
+  int n = 0;
+  bool ok = true, range = true;
+  int t() const { return type == kF32 ? 4 : 2; }
+  int res() const { return flags & TK_RESIDUAL_F32 ? 4 : t(); }
+  int par() const { return flags & TK_PARAMS_F32 ? 4 : t(); }
+  void add(const void *p, uint64_t count, uint64_t ld, uint64_t width, int size, bool out, bool matrix) {
+    if ((uintptr_t)p % size) ok = false;
+    r[n++] = Region{(uintptr_t)p, count, ld * size, width * size, size, out, matrix};
+  }
+  void matrix(const void *p, uint64_t ld, int size, bool out, bool needed) {
+    if (!p) {
+      ok = ok && !needed;
+      return;
+    }
+    if (ld < cols) ok = false;
+    if (ld >= kMaxLd) range = false;
+    else add(p, rows, ld, cols, size, out, true);
+  }
+  void vector(const void *p, uint64_t count, int size, bool out, bool needed) {
+    if (!p) ok = ok && !needed;
+    else add(p, 1, count, count, size, out, false);
+  }
+  // Checks every pair; the caller has added all of a call's arguments.
+  tk_status done() const {
+    if (!ok) return TK_EINVAL;
+    if (!range) return TK_ERANGE;
+    for (int i = 0; i < n; ++i) {
+      // a matrix must end within the address space (47 bits on this platform)
+      const unsigned __int128 end = (unsigned __int128)r[i].at + (unsigned __int128)(r[i].rows - 1) * r[i].pitch + r[i].width;
+      if (end >> 57) return TK_ERANGE;
+    }
+    for (int i = 0; i < n; ++i)
+      for (int j = i + 1; j < n; ++j)
+        if (clash(r[i], r[j])) return TK_EINVAL;
+    return TK_OK;
+  }
+};
+
+static tk_status check_scalars(uint64_t start, uint64_t rows, uint64_t cols, float p, float eps, uint32_t flags) {
+  if (!(p >= 0.0f && p < 1.0f) || !(eps >= 0.0f && eps < INFINITY)) return TK_EINVAL;
+  if (flags & ~(TK_RESIDUAL_F32 | TK_PARAMS_F32)) return TK_EINVAL;
+  if (rows >= kMaxDim || cols >= kMaxDim) return TK_ERANGE;
+  if (p > 0.0f && (start > (1ull << 32) || rows * cols > (1ull << 32) - start)) return TK_ERANGE;
+  return TK_OK;
+}
+
+static Drop drop_of(uint32_t key, uint64_t start, float p) {
+  Drop d{};
+  d.on = p > 0.0f;
+  d.hk = host_lowbias32(key);
+  d.start = (uint32_t)start;
+  d.threshold = (uint32_t)ceilf(p * 0x1p23f);  // the product is exact
+  d.q = 1.0f - p;
+  d.rq = 1.0f / d.q;
+  return d;
+}
+
+static RowTable table_of(RowType t, uint32_t flags) {
+  const bool r32 = flags & TK_RESIDUAL_F32;
+  switch (t) {
+    case kF16: return r32 ? rows_f16_r32() : rows_f16();
+    case kBF16: return r32 ? rows_bf16_r32() : rows_bf16();
+    default: return rows_f32();
+  }
+}
+
+static bool params_f32(RowType t, uint32_t flags) { return t == kF32 || (flags & TK_PARAMS_F32); }
+
+static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
+                        void *c, hipStream_t stream) {
+  FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
+  hipLaunchKernelGGL(k_finish, dim3((uint32_t)((cols + 63) / 64), 3), dim3(256), 0, stream, f);
+  return launch_status();
+}
+
+// Whether a workspace of `have` bytes serves.
+static bool serves(const void *workspace, uint64_t have, uint64_t need) {
+  return need == 0 || (workspace && ((uintptr_t)workspace & 3u) == 0 && have >= need);
+}
+
+// ---------------------------------------------------------------------------------------
+// Dropout-add
+// ---------------------------------------------------------------------------------------
+// The element-wise launches.  A contiguous call without a bias is one long row; a call of 2^31
+// chunks or more is cut.
+static tk_status run_add(void (*launch)(const AddArgs &, hipStream_t), int chunk, AddArgs a, uint64_t rows, uint64_t cols,
+                         int in_size, int out_size, hipStream_t stream) {
+  const bool flat = !a.bias && (rows == 1 || (a.ldx == cols && a.ldy == cols && (!a.residual || a.ldr == cols)));
+  const uint64_t most = 1ull << 30;  // chunks of a launch
+  if (flat) {
+    const uint64_t n = rows * cols, piece = most * chunk;
+    for (uint64_t k = 0; k < n; k += piece) {
+      AddArgs b = a;
+      const uint64_t m = n - k < piece ? n - k : piece;
+      b.x = (const char *)a.x + k * in_size;
+      if (a.residual) b.residual = (const char *)a.residual + k * out_size;
+      b.y = (char *)a.y + k * out_size;
+      b.drop.start = a.drop.start + (uint32_t)k;
+      b.chunks = (uint32_t)((m + chunk - 1) / chunk);
+      b.chunks_per_row = b.chunks;
+      b.div_mul = 0;  // every chunk is in row 0
+      b.div_shift = 0;
+      b.cols64 = m;
+      launch(b, stream);
+      const tk_status st = launch_status();
+      if (st != TK_OK) return st;
+    }
+    return TK_OK;
+  }
+  const uint64_t per_row = (cols + chunk - 1) / chunk;
+  const uint64_t rows_each = most / per_row ? most / per_row : 1;
+  a.chunks_per_row = (uint32_t)per_row;
+  a.cols64 = cols;
+  // n / d for n < 2^31: n ceil(2^(31 + l) / d) >> (31 + l), l = ceil(log2 d)
+  int l = 0;
+  while ((1ull << l) < per_row) ++l;
+  a.div_shift = l - 1;
+  a.div_mul = (uint32_t)(((1ull << (31 + l)) + per_row - 1) / per_row);
+  for (uint64_t r = 0; r < rows; r += rows_each) {
+    AddArgs b = a;
+    b.row0 = r;
+    b.chunks = (uint32_t)((rows - r < rows_each ? rows - r : rows_each) * per_row);
+    launch(b, stream);
+    const tk_status st = launch_status();
+    if (st != TK_OK) return st;
+  }
+  return TK_OK;
+}
+
+static tk_status dropout_add(RowType t, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p, uint32_t flags,
+                             const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr, void *y,
+                             uint64_t ldy, hipStream_t stream) {
+  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
+  if (st != TK_OK || rows == 0 || cols == 0) return st;
+  Checker c{t, rows, cols, flags};
+  c.matrix(x, ldx, c.t(), false, true);
+  c.vector(bias, cols, c.par(), false, false);
+  c.matrix(residual, ldr, c.res(), false, false);
+  c.matrix(y, ldy, c.res(), true, true);
+  if ((st = c.done()) != TK_OK) return st;
+  AddArgs a{};
+  a.x = x; a.ldx = ldx; a.bias = bias; a.residual = residual; a.ldr = ldr; a.y = y; a.ldy = ldy;
+  a.params_f32 = params_f32(t, flags);
+  a.drop = drop_of(key, start, p);
+  const RowTable k = table_of(t, flags);
+  return run_add(k.add_fwd, k.chunk, a, rows, cols, c.t(), c.res(), stream);
+}
+
+static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p,
+                                      uint32_t flags, const void *dy, uint64_t lddy, void *dx, uint64_t lddx, void *dbias,
+                                      void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
+  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
+  if (st != TK_OK || cols == 0) return st;
+  Checker c{t, rows, cols, flags};
+  if (rows == 0) {
+    c.vector(dbias, cols, c.par(), true, false);
+    if ((st = c.done()) != TK_OK || !dbias) return st;
+    return finish(t, flags, nullptr, 0, cols, dbias, nullptr, nullptr, stream);
+  }
+  c.matrix(dy, lddy, c.res(), false, true);
+  c.matrix(dx, lddx, c.t(), true, true);
+  c.vector(dbias, cols, c.par(), true, false);
+  const uint64_t need = dbias ? workspace_bytes(rows, cols) : 0;
+  if (!serves(workspace, workspace_bytes_, need)) return TK_EINVAL;
+  if (need) c.vector(workspace, need / 4, 4, true, true);
+  if ((st = c.done()) != TK_OK) return st;
+  const RowTable k = table_of(t, flags);
+  if (!dbias) {
+    AddArgs a{};
+    a.x = dy; a.ldx = lddy; a.y = dx; a.ldy = lddx;
+    a.drop = drop_of(key, start, p);
+    return run_add(k.add_bwd, k.chunk, a, rows, cols, c.res(), c.t(), stream);
+  }
+  const BwdPlan plan = strips_plan(k.chunk, rows, cols);
+  BwdArgs a{};
+  a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
+  a.rows = rows; a.cols = (uint32_t)cols; a.rows_per_block = plan.rows_per_block;
+  a.partial = (float *)workspace;
+  a.params_f32 = params_f32(t, flags);
+  a.drop = drop_of(key, start, p);
+  k.add_bwd_sums(a, plan, stream);
+  if ((st = launch_status()) != TK_OK) return st;
+  return finish(t, flags, a.partial, plan.lines, cols, dbias, nullptr, nullptr, stream);
+}
+
+// ---------------------------------------------------------------------------------------
+// Layer norm, alone and after dropout-add
+// ---------------------------------------------------------------------------------------
+// `fused`: x is needed and the norm's input is residual + drop(x + bias); else the norm's input
+// comes as `residual`.
+static tk_status norm_forward(RowType t, bool fused, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p,
+                              float eps, uint32_t flags, const void *x, uint64_t ldx, const void *bias, const void *residual,
+                              uint64_t ldr, const void *gamma, const void *beta, void *sum, uint64_t lds, void *y,
+                              uint64_t ldy, float *mean, float *rstd, hipStream_t stream) {
+  tk_status st = check_scalars(start, rows, cols, p, eps, flags);
+  if (st != TK_OK || rows == 0 || cols == 0) return st;
+  Checker c{t, rows, cols, flags};
+  if (fused) c.matrix(x, ldx, c.t(), false, true);
+  c.vector(bias, cols, c.par(), false, false);
+  c.matrix(residual, ldr, c.res(), false, !fused);
+  c.vector(gamma, cols, c.par(), false, false);
+  c.vector(beta, cols, c.par(), false, false);
+  c.matrix(sum, lds, c.res(), true, false);
+  c.matrix(y, ldy, c.t(), true, true);
+  c.vector(mean, rows, 4, true, false);
+  c.vector(rstd, rows, 4, true, false);
+  if ((st = c.done()) != TK_OK) return st;
+  FwdArgs a{};
+  a.x = x; a.ldx = ldx; a.bias = bias; a.residual = residual; a.ldr = ldr; a.gamma = gamma; a.beta = beta;
+  a.sum = sum; a.lds = lds; a.y = y; a.ldy = ldy; a.mean = mean; a.rstd = rstd;
+  a.rows = rows; a.cols = (uint32_t)cols; a.eps = eps;
+  a.params_f32 = params_f32(t, flags);
+  a.drop = drop_of(key, start, p);
+  table_of(t, flags).norm_fwd(a, stream);
+  return launch_status();
+}
+
+static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p,
+                               uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds,
+                               const void *sum, uint64_t lds, const void *gamma, const float *mean, const float *rstd,
+                               void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma, void *dbeta,
+                               void *dbias, void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
+  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
+  if (st != TK_OK || cols == 0) return st;
+  Checker c{t, rows, cols, flags};
+  const bool sums = dgamma || dbeta || dbias;
+  if (rows == 0) {
+    c.vector(dgamma, cols, c.par(), true, false);
+    c.vector(dbeta, cols, c.par(), true, false);
+    c.vector(dbias, cols, c.par(), true, false);
+    if ((st = c.done()) != TK_OK || !sums) return st;
+    return finish(t, flags, nullptr, 0, cols, dgamma, dbeta, dbias, stream);
+  }
+  c.matrix(dy, lddy, c.t(), false, true);
+  c.matrix(dsum, ldds, c.res(), false, false);
+  c.matrix(sum, lds, c.res(), false, true);
+  c.vector(gamma, cols, c.par(), false, false);
+  c.vector(mean, rows, 4, false, true);
+  c.vector(rstd, rows, 4, false, true);
+  if (fused) c.matrix(dx, lddx, c.t(), true, true);
+  c.matrix(dresidual, lddr, c.res(), true, !fused);
+  c.vector(dgamma, cols, c.par(), true, false);
+  c.vector(dbeta, cols, c.par(), true, false);
+  c.vector(dbias, cols, c.par(), true, false);
+  const uint64_t need = sums || cols > kRowsInRegisters ? workspace_bytes(rows, cols) : 0;
+  if (!serves(workspace, workspace_bytes_, need)) return TK_EINVAL;
+  if (need) c.vector(workspace, need / 4, 4, true, true);
+  if ((st = c.done()) != TK_OK) return st;
+  const RowTable k = table_of(t, flags);
+  const BwdPlan plan = norm_plan(k.chunk, rows, cols);
+  BwdArgs a{};
+  a.dy = dy; a.lddy = lddy; a.dsum = dsum; a.ldds = ldds; a.sum = sum; a.lds = lds;
+  a.gamma = gamma; a.mean = mean; a.rstd = rstd;
+  a.dx = dx; a.lddx = lddx; a.dresidual = dresidual; a.lddr = lddr;
+  a.rows = rows; a.cols = (uint32_t)cols; a.rows_per_block = plan.rows_per_block;
+  a.partial = sums ? (float *)workspace : nullptr;
+  a.stats = plan.tpr ? nullptr : (float *)((char *)workspace + need - 8 * rows);
+  a.params_f32 = params_f32(t, flags);
+  a.drop = drop_of(key, start, p);
+  k.norm_bwd(a, plan, dbias != nullptr, stream);
+  if ((st = launch_status()) != TK_OK || !sums) return st;
+  return finish(t, flags, a.partial, plan.lines, cols, dgamma, dbeta, dbias, stream);
+}
+
+}  // namespace tk
+
+extern "C" {
+
+tk_status tk_backward_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t *bytes) {
+  if (!bytes) return TK_EINVAL;
+  if (rows >= tk::kMaxDim || cols >= tk::kMaxDim) return TK_ERANGE;
+  *bytes = tk::workspace_bytes(rows, cols);
+  return TK_OK;
+}
+
+#define TK_ROW_OPERATORS(SUFFIX, TYPE)                                                                                   \
+  tk_status tk_dropout_add_##SUFFIX(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,            \
+                                    uint32_t flags, const void *x, uint64_t ldx, const void *bias, const void *residual, \
+                                    uint64_t ldr, void *y, uint64_t ldy, hipStream_t stream) {                           \
+    return tk::dropout_add(TYPE, key, start_draw, rows, cols, p, flags, x, ldx, bias, residual, ldr, y, ldy, stream);    \
+  }                                                                                                                      \
+  tk_status tk_dropout_add_backward_##SUFFIX(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,   \
+                                             uint32_t flags, const void *dy, uint64_t lddy, void *dx, uint64_t lddx,     \
+                                             void *dbias, void *workspace, uint64_t workspace_bytes,                     \
+                                             hipStream_t stream) {                                                       \
+    return tk::dropout_add_backward(TYPE, key, start_draw, rows, cols, p, flags, dy, lddy, dx, lddx, dbias, workspace,   \
+                                    workspace_bytes, stream);                                                            \
+  }                                                                                                                      \
+  tk_status tk_layer_norm_##SUFFIX(uint64_t rows, uint64_t cols, float eps, uint32_t flags, const void *x, uint64_t ldx, \
+                                   const void *gamma, const void *beta, void *y, uint64_t ldy, float *mean, float *rstd, \
+                                   hipStream_t stream) {                                                                 \
+    return tk::norm_forward(TYPE, false, 0, 0, rows, cols, 0.0f, eps, flags, nullptr, 0, nullptr, x, ldx, gamma, beta,   \
+                            nullptr, 0, y, ldy, mean, rstd, stream);                                                     \
+  }                                                                                                                      \
+  tk_status tk_layer_norm_backward_##SUFFIX(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy, uint64_t lddy, \
+                                            const void *x, uint64_t ldx, const void *gamma, const float *mean,           \
+                                            const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta,       \
+                                            void *workspace, uint64_t workspace_bytes, hipStream_t stream) {             \
+    return tk::norm_backward(TYPE, false, 0, 0, rows, cols, 0.0f, flags, dy, lddy, nullptr, 0, x, ldx, gamma, mean,      \
+                             rstd, nullptr, 0, dx, lddx, dgamma, dbeta, nullptr, workspace, workspace_bytes, stream);    \
+  }                                                                                                                      \
+  tk_status tk_dropout_add_layer_norm_##SUFFIX(                                                                          \
+      uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float eps, uint32_t flags,               \
+      const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr, const void *gamma,              \
+      const void *beta, void *sum, uint64_t lds, void *y, uint64_t ldy, float *mean, float *rstd, hipStream_t stream) {  \
+    return tk::norm_forward(TYPE, true, key, start_draw, rows, cols, p, eps, flags, x, ldx, bias, residual, ldr, gamma,  \
+                            beta, sum, lds, y, ldy, mean, rstd, stream);                                                 \
+  }                                                                                                                      \
+  tk_status tk_dropout_add_layer_norm_backward_##SUFFIX(                                                                 \
+      uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, uint32_t flags, const void *dy,          \
+      uint64_t lddy, const void *dsum, uint64_t ldds, const void *sum, uint64_t lds, const void *gamma,                  \
+      const float *mean, const float *rstd, void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma,       \
+      void *dbeta, void *dbias, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {                         \
+    return tk::norm_backward(TYPE, true, key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, gamma,   \
+                             mean, rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace, workspace_bytes,    \
+                             stream);                                                                                    \
+  }
+
+TK_ROW_OPERATORS(f32, tk::kF32)
+TK_ROW_OPERATORS(f16, tk::kF16)
+TK_ROW_OPERATORS(bf16, tk::kBF16)
+
+}  // extern "C"

@@ -1,0 +1,77 @@
+// tk_rows_args.h -- arguments of the row operators' kernels, and the table of launches that
+// each pair of types gives the entry points (tk_rows.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace tk {
+
+struct Drop {
+  bool on;             // p > 0
+  uint32_t hk;         // hash of the key
+  uint32_t start;      // counter of element (0, 0)
+  uint32_t threshold;  // kept where the word's low 23 bits reach ceil(p 2^23): u >= p, exactly
+  float q, rq;         // 1 - p, and its reciprocal rounded to float
+};
+
+// Forward of the layer norm (x null: its input is `residual`) and of the fused operator.
+struct FwdArgs {
+  const void *x, *bias, *residual, *gamma, *beta;
+  void *sum, *y;
+  float *mean, *rstd;
+  uint64_t rows, ldx, ldr, lds, ldy;
+  uint32_t cols;
+  float eps;
+  bool params_f32;
+  Drop drop;
+};
+
+// Backward of either (dx null: the layer norm alone, whose dx is `dresidual` here), and of
+// dropout-add with a bias (dy is then of the residual stream's type, sum null).
+struct BwdArgs {
+  const void *dy, *dsum, *sum, *gamma;
+  const float *mean, *rstd;
+  void *dx, *dresidual;
+  float *partial;  // lines of partial column sums: dgamma's, dbeta's, then dbias's; null: no sums wanted
+  float *stats;    // mean(g), mean(g h) of every row (wide rows)
+  uint64_t rows, lddy, ldds, lds, lddx, lddr, rows_per_block;
+  uint32_t cols;
+  bool params_f32;
+  Drop drop;
+};
+
+struct AddArgs {
+  const void *x, *bias, *residual;
+  void *y;
+  uint64_t row0, ldx, ldr, ldy, cols64;
+  uint32_t chunks, chunks_per_row, div_mul;
+  int div_shift;
+  bool params_f32;
+  Drop drop;
+};
+
+// How a backward call is cut: `lines` lines of partial sums; tpr threads a row with ept
+// elements each, or tpr = 0 and strips of columns.
+struct BwdPlan {
+  int tpr, ept;
+  uint64_t lines, strips, rows_per_block;
+};
+
+struct RowTable {
+  int chunk;
+  void (*norm_fwd)(const FwdArgs &, hipStream_t);
+  void (*norm_bwd)(const BwdArgs &, const BwdPlan &, bool bias, hipStream_t);
+  void (*add_bwd_sums)(const BwdArgs &, const BwdPlan &, hipStream_t);
+  void (*add_fwd)(const AddArgs &, hipStream_t);
+  void (*add_bwd)(const AddArgs &, hipStream_t);
+};
+
+// One for each pair of types (activations, residual stream).
+RowTable rows_f32();
+RowTable rows_f16();
+RowTable rows_f16_r32();
+RowTable rows_bf16();
+RowTable rows_bf16_r32();
+
+}  // namespace tk

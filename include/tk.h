@@ -171,6 +171,118 @@ tk_status tk_dropout_f32(uint32_t key, uint64_t start_draw, uint64_t n, float p,
 tk_status tk_dropout_backward_f32(uint32_t key, uint64_t start_draw, uint64_t n, float p, const float *dy,
                                   float *dx, hipStream_t stream);
 
+/* ---- Row operators: dropout-add and layer norm ---------------------------------------
+ * The dropout of a transformer block at its place: after a bias, before the residual, and
+ * with the layer norm that reads the sum.  Every operator works on a rows x cols matrix of
+ * float (_f32), binary16 (_f16) or bfloat16 (_bf16) elements and computes in float, rounding
+ * each output once.  With z = x + bias and drop(v) at (r, c) = v / (1 - p) where the f32
+ * uniform of word start_draw + r * cols + c is at least p, else +0.0 (Phobos, §dropout: the
+ * decision of tk_dropout_f32 with the flat index as its counter, so a fill cut at any row
+ * equals the whole and the backward pass redraws the mask):
+ *   tk_dropout_add             y = residual + drop(z)
+ *     _backward                dx = drop(dy);  dbias = column sums of dx.  (residual's
+ *                              gradient is dy itself.)
+ *   tk_layer_norm              y = h gamma + beta, h = (x - mean) rstd, with the row's mean and
+ *                              rstd = 1 / sqrt(variance + eps), variance = mean of (x - mean)^2
+ *     _backward                g = dy gamma:  dx = rstd (g - mean(g) - h mean(g h)),
+ *                              dgamma = column sums of dy h, dbeta = column sums of dy
+ *   tk_dropout_add_layer_norm  sum = residual + drop(z);  y = layer norm of that sum (before
+ *                              sum's own rounding)
+ *     _backward                dresidual = dsum + dx of the layer norm at `sum`;
+ *                              dx = drop(dresidual);  dbias = column sums of dx;  dgamma, dbeta
+ * The quotient is the IEEE division in the _f32 operators (as in tk_dropout_f32); the 16-bit
+ * ones multiply by 1 / (1 - p) rounded to float, which their own rounding covers.  p == 0
+ * keeps every element and takes no draws (no limit on the counters then).
+ *   flags: TK_RESIDUAL_F32  the residual stream is float: residual, dropout-add's y and dy,
+ *                           sum, dsum, dresidual, and tk_layer_norm's x and dx
+ *          TK_PARAMS_F32    bias, gamma, beta and their gradients are float
+ *          (both change nothing for _f32; other bits: TK_EINVAL)
+ *   Nullable: bias, residual, beta and gamma (0, 0, 0 and 1 in their place), dsum (0), and the
+ *          outputs sum, mean, rstd, dgamma, dbeta, dbias and the fused backward's dresidual.
+ *   ld*:   elements from a matrix's row to its next, at least cols.  Elements between the rows
+ *          are neither read nor written.  mean and rstd are `rows` floats; the backward takes
+ *          those that the forward wrote.  Any element-aligned address is accepted.
+ *   In place: an output matrix may be an input matrix (same address, ld and element type).
+ *          Otherwise no output may share bytes with any other argument; slices of one buffer
+ *          with one row pitch are told apart exactly, other matrices by their whole extent.
+ *   p must lie in [0, 1) and eps be finite and >= 0, else TK_EINVAL.  rows and cols are below
+ *          2^31 and ld below 2^40, else TK_ERANGE; start_draw + rows * cols <= 2^32 where
+ *          p > 0, else TK_ERANGE.  rows == 0 or cols == 0 is TK_OK: the forward calls and dx
+ *          have nothing to write, gradients over rows == 0 are written as zeros.
+ *   workspace: the backward calls that give dgamma, dbeta or dbias, and those of the layer
+ *          norms at more than 16384 columns, need device memory of at least the size that
+ *          tk_backward_workspace_bytes names (64-bit count in *bytes; TK_ERANGE as above),
+ *          4-byte aligned, else TK_EINVAL.  It holds nothing between calls; calls that may
+ *          overlap in time (other streams, graphs replayed together) need one each.
+ * NaN and infinity follow the formulas; a dropped element is +0.0 whatever it was.  Column
+ * sums are taken in a fixed order: equal arguments give equal bits, run after run.          */
+#define TK_RESIDUAL_F32 1u
+#define TK_PARAMS_F32 2u
+tk_status tk_backward_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t *bytes);
+
+tk_status tk_dropout_add_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, uint32_t flags,
+        const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr, void *y, uint64_t ldy,
+        hipStream_t stream);
+tk_status tk_dropout_add_backward_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,
+        uint32_t flags, const void *dy, uint64_t lddy, void *dx, uint64_t lddx, void *dbias, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_layer_norm_f32(uint64_t rows, uint64_t cols, float eps, uint32_t flags, const void *x, uint64_t ldx,
+        const void *gamma, const void *beta, void *y, uint64_t ldy, float *mean, float *rstd, hipStream_t stream);
+tk_status tk_layer_norm_backward_f32(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy, uint64_t lddy,
+        const void *x, uint64_t ldx, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,
+        void *dgamma, void *dbeta, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,
+        float eps, uint32_t flags, const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr,
+        const void *gamma, const void *beta, void *sum, uint64_t lds, void *y, uint64_t ldy, float *mean, float *rstd,
+        hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_backward_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols,
+        float p, uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds, const void *sum,
+        uint64_t lds, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,
+        void *dresidual, uint64_t lddr, void *dgamma, void *dbeta, void *dbias, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+
+tk_status tk_dropout_add_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, uint32_t flags,
+        const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr, void *y, uint64_t ldy,
+        hipStream_t stream);
+tk_status tk_dropout_add_backward_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,
+        uint32_t flags, const void *dy, uint64_t lddy, void *dx, uint64_t lddx, void *dbias, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_layer_norm_f16(uint64_t rows, uint64_t cols, float eps, uint32_t flags, const void *x, uint64_t ldx,
+        const void *gamma, const void *beta, void *y, uint64_t ldy, float *mean, float *rstd, hipStream_t stream);
+tk_status tk_layer_norm_backward_f16(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy, uint64_t lddy,
+        const void *x, uint64_t ldx, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,
+        void *dgamma, void *dbeta, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,
+        float eps, uint32_t flags, const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr,
+        const void *gamma, const void *beta, void *sum, uint64_t lds, void *y, uint64_t ldy, float *mean, float *rstd,
+        hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_backward_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols,
+        float p, uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds, const void *sum,
+        uint64_t lds, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,
+        void *dresidual, uint64_t lddr, void *dgamma, void *dbeta, void *dbias, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+
+tk_status tk_dropout_add_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, uint32_t flags,
+        const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr, void *y, uint64_t ldy,
+        hipStream_t stream);
+tk_status tk_dropout_add_backward_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,
+        uint32_t flags, const void *dy, uint64_t lddy, void *dx, uint64_t lddx, void *dbias, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_layer_norm_bf16(uint64_t rows, uint64_t cols, float eps, uint32_t flags, const void *x, uint64_t ldx,
+        const void *gamma, const void *beta, void *y, uint64_t ldy, float *mean, float *rstd, hipStream_t stream);
+tk_status tk_layer_norm_backward_bf16(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy, uint64_t lddy,
+        const void *x, uint64_t ldx, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,
+        void *dgamma, void *dbeta, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p,
+        float eps, uint32_t flags, const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr,
+        const void *gamma, const void *beta, void *sum, uint64_t lds, void *y, uint64_t ldy, float *mean, float *rstd,
+        hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_backward_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols,
+        float p, uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds, const void *sum,
+        uint64_t lds, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,
+        void *dresidual, uint64_t lddr, void *dgamma, void *dbeta, void *dbias, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+
 /* ---- Weighted choice through an alias table -----------------------------------------
  * tandem-sycl, "Design", §Fills: the choice fill maps each 64-bit draw through an alias
  * table.  tk_alias_create builds the table on the host from n >= 1 finite, non-negative
