@@ -19,19 +19,24 @@ struct FinishArgs {
   int kind;  // 0 float, 1 binary16, 2 bfloat16
 };
 
-__global__ __launch_bounds__(256) void k_finish(FinishArgs a) {
-  __shared__ float part[4][64];
+__global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
+  constexpr int kWaves = 16;
+  __shared__ float part[kWaves][64];
   void *out = a.out[blockIdx.y];
   if (!out) return;
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
   const float *p = a.partial + (uint64_t)blockIdx.y * a.lines * a.cols + c;
   float s = 0.0f;
-  if (c < a.cols)
-    for (uint64_t l = wave; l < a.lines; l += 4) s += p[l * a.cols];
+  if (c < a.cols) {
+#pragma unroll 8
+    for (uint64_t l = wave; l < a.lines; l += kWaves) s += p[l * a.cols];
+  }
   part[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < a.cols) {
-    s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) s += part[w][lane];
     if (a.kind == 0) ((float *)out)[c] = s;
     else if (a.kind == 1) ((_Float16 *)out)[c] = (_Float16)s;
     else ((__bf16 *)out)[c] = (__bf16)s;
@@ -59,10 +64,11 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
 static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
   if (cols > kRowsInRegisters) return strips_plan(chunk, rows, cols);
   BwdPlan p{};
-  p.tpr = cols <= 128 ? 16 : cols <= 1024 ? 64 : cols <= 4096 ? 256 : cols <= 8192 ? 512 : 1024;
-  p.ept = cols <= 512 || (cols > 1024 && cols <= 2048) ? 8 : 16;
-  const uint64_t per = p.tpr < 256 ? 256 / p.tpr : 1, sets = (rows + per - 1) / per;
-  const uint64_t most = p.tpr <= 256 ? 1024 : 512;
+  p.tpr = cols <= 128 ? 16 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+  p.ept = cols <= 8192 ? 8 : 16;
+  const uint64_t blk = cols < (uint64_t)chunk ? 256 : cols <= 4096 ? 512 : 1024;
+  const uint64_t per = blk / p.tpr, sets = (rows + per - 1) / per;
+  const uint64_t most = blk == 1024 ? 256 : 512;
   p.lines = sets < most ? sets : most;
   return p;
 }
@@ -185,7 +191,7 @@ static bool params_f32(RowType t, uint32_t flags) { return t == kF32 || (flags &
 static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
                         void *c, hipStream_t stream) {
   FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
-  hipLaunchKernelGGL(k_finish, dim3((uint32_t)((cols + 63) / 64), 3), dim3(256), 0, stream, f);
+  hipLaunchKernelGGL(k_finish, dim3((uint32_t)((cols + 63) / 64), c ? 3 : b ? 2 : 1), dim3(1024), 0, stream, f);
   return launch_status();
 }
 
@@ -199,15 +205,16 @@ static bool serves(const void *workspace, uint64_t have, uint64_t need) {
 // ---------------------------------------------------------------------------------------
 // The element-wise launches.  A contiguous call without a bias is one long row; a call of 2^31
 // chunks or more is cut.
-static tk_status run_add(void (*launch)(const AddArgs &, hipStream_t), int chunk, AddArgs a, uint64_t rows, uint64_t cols,
+static tk_status run_add(void (*launch)(const AddArgs &, int, hipStream_t), int chunk, AddArgs a, uint64_t rows, uint64_t cols,
                          int in_size, int out_size, hipStream_t stream) {
   const bool flat = !a.bias && (rows == 1 || (a.ldx == cols && a.ldy == cols && (!a.residual || a.ldr == cols)));
+  if ((flat ? rows * cols : cols) < (uint64_t)chunk) chunk = 1;  // no row holds a whole chunk
   const uint64_t most = 1ull << 30;  // chunks of a launch
   if (flat) {
     const uint64_t n = rows * cols, piece = most * chunk;
-    for (uint64_t k = 0; k < n; k += piece) {
+    for (uint64_t k = 0, m; k < n; k += m) {
       AddArgs b = a;
-      const uint64_t m = n - k < piece ? n - k : piece;
+      m = n - k < piece + chunk ? n - k : piece;  // no piece is shorter than a chunk
       b.x = (const char *)a.x + k * in_size;
       if (a.residual) b.residual = (const char *)a.residual + k * out_size;
       b.y = (char *)a.y + k * out_size;
@@ -217,7 +224,7 @@ static tk_status run_add(void (*launch)(const AddArgs &, hipStream_t), int chunk
       b.div_mul = 0;  // every chunk is in row 0
       b.div_shift = 0;
       b.cols64 = m;
-      launch(b, stream);
+      launch(b, chunk, stream);
       const tk_status st = launch_status();
       if (st != TK_OK) return st;
     }
@@ -236,7 +243,7 @@ static tk_status run_add(void (*launch)(const AddArgs &, hipStream_t), int chunk
     AddArgs b = a;
     b.row0 = r;
     b.chunks = (uint32_t)((rows - r < rows_each ? rows - r : rows_each) * per_row);
-    launch(b, stream);
+    launch(b, chunk, stream);
     const tk_status st = launch_status();
     if (st != TK_OK) return st;
   }

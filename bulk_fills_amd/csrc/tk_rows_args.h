@@ -63,8 +63,8 @@ struct RowTable {
   void (*norm_fwd)(const FwdArgs &, hipStream_t);
   void (*norm_bwd)(const BwdArgs &, const BwdPlan &, bool bias, hipStream_t);
   void (*add_bwd_sums)(const BwdArgs &, const BwdPlan &, hipStream_t);
-  void (*add_fwd)(const AddArgs &, hipStream_t);
-  void (*add_bwd)(const AddArgs &, hipStream_t);
+  void (*add_fwd)(const AddArgs &, int chunk, hipStream_t);
+  void (*add_bwd)(const AddArgs &, int chunk, hipStream_t);
 };
 
 // One for each pair of types (activations, residual stream).
