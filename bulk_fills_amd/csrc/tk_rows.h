@@ -35,10 +35,16 @@ __device__ __forceinline__ N chunk_at(N c, N cols) {
   return c + CH <= cols ? c : cols - CH;
 }
 
-// Data that is read once, past the caches.
-template <int CH, class T>
-__device__ __forceinline__ Chunk<T, CH> load_once(const T *p) {
-  return __builtin_nontemporal_load((const Chunk<T, CH> *)p);
+// kOnce: past the caches.  Calls that read up to kCachedReads use ordinary loads: what a call of
+// that size reads was often written just before and still lies in the 256 MB last-level cache.
+// MI355X, calls in a row over three sets of buffers, ordinary against non-temporal loads:
+// layer norm bf16 16384x1024 (reads 34 MB) 12.3 against 13.9 us, 262144x128 (67 MB) 21.6
+// against 24.9, dropout-add's backward 8192x4096 (67 MB) 25.6 against 30.4; dropout-add
+// 8192x4096 (134 MB) 38.4 against 36.8, layer norm 16384x8192 with a float stream (537 MB)
+// 143 against 131, the fused backward 8192x8192 (403 MB) 137 against 131.
+template <bool kOnce, int CH, class T>
+__device__ __forceinline__ Chunk<T, CH> load_chunk(const T *p) {
+  return kOnce ? __builtin_nontemporal_load((const Chunk<T, CH> *)p) : *(const Chunk<T, CH> *)p;
 }
 
 // The elements of a loaded chunk as floats, of which the first nv count; the rest become 0.
@@ -53,18 +59,6 @@ __device__ __forceinline__ void unpack(const Chunk<T, CH> &t, int nv, float *v) 
       if (down & step)
 #pragma unroll
         for (int e = 0; e < CH; ++e) v[e] = e + step < CH ? v[e + step] : 0.0f;
-  }
-}
-
-// Holds a chunk in its loaded form up to here: what is unpacked from it afterwards is unpacked
-// again, so that two uses of a chunk on both sides of a row's sum do not keep its floats alive.
-template <class C>
-__device__ __forceinline__ void stay_packed(C &c) {
-  if constexpr (sizeof(C) >= 8) {
-    typedef uint32_t words __attribute__((ext_vector_type(sizeof(C) / 4)));
-    words w = __builtin_bit_cast(words, c);
-    __asm__ volatile("" : "+v"(w));
-    c = __builtin_bit_cast(C, w);
   }
 }
 
@@ -100,12 +94,41 @@ __device__ __forceinline__ void load_param(const void *p, bool f32, uint32_t c, 
 // ---- dropout ---------------------------------------------------------------------------
 // Kept values over 1 - p: the IEEE quotient for float, and a product with the reciprocal for
 // the 16-bit types, whose 2^-23 relative error is far below their own rounding (2^-11, 2^-8).
+//
+// The words of a chunk whose first counter c is a multiple of CH share most of the hash's first
+// step: with k = c ^ hk ^ ((c ^ hk) >> 16), the argument of the first product for counter c + j
+// is k ^ j (j < CH changes no higher bit), and (k ^ j) K = k K + the sum over the bits b of j of
+// +-2^b K, + where k's bit b is clear.  One product and CH - 1 additions instead of CH products,
+// which take four cycles each: 14 instead of 18 cycles an element in all.
+constexpr uint32_t kHashMul1 = 0x7FEB352Du, kHashMul2 = 0x846CA68Bu;  // tk_hash32's
+
+template <bool kDivide>
+__device__ __forceinline__ float drop_one(const Drop &d, uint32_t word, float v) {
+  const bool keep = (word & 0x7FFFFFu) >= d.threshold;
+  return keep ? (kDivide ? __fdiv_rn(v, d.q) : v * d.rq) : 0.0f;
+}
+
 template <bool kDivide, int CH>
 __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) {
+  if (CH > 1 && (c & (CH - 1)) == 0) {
+    uint32_t k = c ^ d.hk;
+    k ^= k >> 16;
+    uint32_t x[CH];
+    x[0] = k * kHashMul1;
 #pragma unroll
-  for (int e = 0; e < CH; ++e) {
-    const bool keep = (tk_word(d.hk, c + e) & 0x7FFFFFu) >= d.threshold;
-    v[e] = keep ? (kDivide ? __fdiv_rn(v[e], d.q) : v[e] * d.rq) : 0.0f;
+    for (int b = 1; b < CH; b <<= 1) {
+      const uint32_t step = k & b ? 0u - b * kHashMul1 : b * kHashMul1;
+#pragma unroll
+      for (int e = 0; e < b; ++e) x[b + e] = x[e] + step;
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+      const uint32_t y = (x[e] ^ (x[e] >> 15)) * kHashMul2;
+      v[e] = drop_one<kDivide>(d, y ^ (y >> 16), v[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < CH; ++e) v[e] = drop_one<kDivide>(d, tk_word(d.hk, c + e), v[e]);
   }
 }
 
@@ -113,6 +136,18 @@ __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) 
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float x) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), kCtrl, 0xF, 0xF, true));
+}
+
+// Sums over pairs of lanes 16 and 32 apart: the row swaps of gfx950.
+__device__ __forceinline__ float swap_sum16(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float swap_sum32(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
 // The sum over each group of kLanes lanes (a power of two), the same bits in all of them:
@@ -123,54 +158,68 @@ __device__ __forceinline__ float lanes_sum(float x) {
   if (kLanes >= 4) x += dpp<0x4E>(x);    // quad_perm 2,3,0,1
   if (kLanes >= 8) x += dpp<0x141>(x);   // row_half_mirror
   if (kLanes >= 16) x += dpp<0x140>(x);  // row_mirror
-  if (kLanes == 64) {
-    const uint32_t u = __float_as_uint(x);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const uint32_t w = __float_as_uint(x);
-    const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-    x = __uint_as_float(b[0]) + __uint_as_float(b[1]);
-  }
+  if (kLanes >= 32) x = swap_sum16(x);
+  if (kLanes >= 64) x = swap_sum32(x);
   return x;
 }
 
-// kN sums over the kTpr threads of a row.  Rows of up to a wave stay in registers; wider ones
-// go through `slot` (kN floats a wave of the work-group), which must not be written again before
-// another barrier has passed: every lane reads one wave's sums and the lanes add them up.
-template <int kTpr, int kN>
-__device__ __forceinline__ void row_sums(float (&x)[kN], float (*slot)[kN]) {
-#pragma unroll
-  for (int k = 0; k < kN; ++k) x[k] = lanes_sum<(kTpr < 64 ? kTpr : 64)>(x[k]);
-  if constexpr (kTpr > 64) {
-    constexpr uint32_t kWaves = kTpr / 64;
-    const uint32_t wave = threadIdx.x >> 6, from = threadIdx.x / kTpr * kWaves + threadIdx.x % kWaves;
-    if ((threadIdx.x & 63) == 0)
-#pragma unroll
-      for (int k = 0; k < kN; ++k) slot[wave][k] = x[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kN; ++k) x[k] = lanes_sum<kWaves>(slot[from][k]);
-  }
+// The sum over a wave's groups of kLanes lanes, lane by lane of a group.
+template <int kLanes>
+__device__ __forceinline__ float groups_sum(float x) {
+  if (kLanes <= 8) x += dpp<0x128>(x);  // row_ror:8
+  if (kLanes <= 16) x = swap_sum16(x);
+  if (kLanes <= 32) x = swap_sum32(x);
+  return x;
 }
 
-// The row group of a thread: on the scalar unit where a wave has one row, and with it the
-// addresses of its rows.
-template <int kTpr>
-__device__ __forceinline__ uint32_t row_group() {
-  const uint32_t g = threadIdx.x / kTpr;
-  return kTpr >= 64 ? (uint32_t)__builtin_amdgcn_readfirstlane(g) : g;
+// How a work-group's threads take rows: kLanes (8, 16 or 32) lanes to a row, or with kLanes =
+// 64 as many whole waves (1 to 16) as the row needs, `waves`.  Whole waves keep the row and
+// its addresses on the scalar unit.
+template <int kLanes>
+struct Team {
+  uint32_t group, t, threads, groups;  // this thread's row group and place in it; a group's threads; groups
+  __device__ __forceinline__ explicit Team(uint32_t waves) {
+    if constexpr (kLanes < 64) {
+      group = threadIdx.x / kLanes;
+      t = threadIdx.x % kLanes;
+      threads = kLanes;
+    } else {
+      group = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / waves;
+      threads = waves * 64;
+      t = threadIdx.x - group * threads;
+    }
+    groups = blockDim.x / threads;
+  }
+};
+
+// kN sums over a row.  Rows of up to a wave stay in registers; wider ones go through `slot` (kN
+// floats a wave of the work-group), which must not be written again before another barrier has
+// passed: every lane reads one wave's sums and the lanes add them up.
+template <int kLanes, int kN>
+__device__ __forceinline__ void row_sums(float (&x)[kN], float (*slot)[kN], uint32_t group, uint32_t waves) {
+#pragma unroll
+  for (int k = 0; k < kN; ++k) x[k] = lanes_sum<kLanes>(x[k]);
+  if (kLanes == 64 && waves > 1) {
+    const uint32_t lane = threadIdx.x & 15;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < kN; ++k) slot[threadIdx.x >> 6][k] = x[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kN; ++k) x[k] = lanes_sum<16>(lane < waves ? slot[group * waves + lane][k] : 0.0f);
+  }
 }
 
 // ---- forward ---------------------------------------------------------------------------
 // A chunk of a row's inputs as loaded.
-template <class T, class R, bool kX, int CH>
+template <class T, class R, bool kX, bool kOnce, int CH>
 struct FwdIn {
   Chunk<T, CH> x;
   Chunk<R, CH> r;
   __device__ __forceinline__ void load(const FwdArgs &a, uint64_t row, uint32_t c) {
     const uint32_t at = chunk_at<CH>(c, a.cols);
-    if constexpr (kX) x = load_once<CH>((const T *)a.x + row * a.ldx + at);
-    if (!kX || a.residual) r = load_once<CH>((const R *)a.residual + row * a.ldr + at);
+    if constexpr (kX) x = load_chunk<kOnce, CH>((const T *)a.x + row * a.ldx + at);
+    if (!kX || a.residual) r = load_chunk<kOnce, CH>((const R *)a.residual + row * a.ldr + at);
   }
   // The norm's input: residual + drop(x + bias); 0 past the row's end.
   __device__ __forceinline__ void value(const FwdArgs &a, uint64_t row, uint32_t c, const float *bias, float *v) const {
@@ -193,77 +242,93 @@ struct FwdIn {
   }
 };
 
-template <class T, class R, int CH>
-__device__ __forceinline__ void norm_out(const FwdArgs &a, uint64_t row, uint32_t c, float mean, float rstd,
-                                         const float *gamma, const float *beta, const float *v) {
+// y from the distances d of a chunk's elements to the row's mean.
+template <class T, int CH>
+__device__ __forceinline__ void norm_out(const FwdArgs &a, uint64_t row, uint32_t c, float rstd, const float *gamma,
+                                         const float *beta, const float *d) {
   const int nv = (int)(a.cols - c);
   if (nv <= 0) return;
-  if (a.sum) store_chunk<CH>((R *)a.sum + row * a.lds + c, nv, v);
   float y[CH];
 #pragma unroll
-  for (int e = 0; e < CH; ++e) y[e] = __builtin_fmaf((v[e] - mean) * rstd, gamma[e], beta[e]);
+  for (int e = 0; e < CH; ++e) y[e] = __builtin_fmaf(d[e] * rstd, gamma[e], beta[e]);
   store_chunk<CH>((T *)a.y + row * a.ldy + c, nv, y);
 }
 
-__device__ __forceinline__ float rstd_of(float m2, uint32_t cols, float eps) {
-  return 1.0f / sqrtf(m2 / (float)cols + eps);
+// 1 / sqrt(x) to within two units of the last place: the hardware's v_rsq_f32 (one unit), with
+// the argument scaled into its range where it might be subnormal (eps = 0).
+__device__ __forceinline__ float rsqrt_any(float x) {
+  return x < 0x1p-96f ? __builtin_amdgcn_rsqf(x * 0x1p96f) * 0x1p48f : __builtin_amdgcn_rsqf(x);
 }
 
 // The row stays in registers between the two sums (the mean, then the squared distances from
 // it: no cancellation) and the output: one read and one write of the data.  A work-group takes
 // every gridDim.x-th set of rows, keeps the parameters in registers, and loads its next rows
 // before it works on the present ones.
-template <class T, class R, bool kX, int CH, int kTpr, int V, int kBlk>
-__global__ __launch_bounds__(kBlk) void k_norm_fwd(FwdArgs a) {
-  constexpr int kRows = kBlk / kTpr;
-  __shared__ float slot[2][kBlk / 64][1];
-  const uint32_t t = threadIdx.x % kTpr;
-  const uint64_t step = (uint64_t)gridDim.x * kRows;
-  uint64_t row = (uint64_t)blockIdx.x * kRows + row_group<kTpr>();
-  float bias[V][CH], gamma[V][CH], beta[V][CH];
-  FwdIn<T, R, kX, CH> next[V];
+template <class T, class R, bool kX, bool kOnce, int CH, int kLanes, int V, bool kKeep>
+__global__ __launch_bounds__(kLanes < 64 ? 256 : 1024) void k_norm_fwd(FwdArgs a) {
+  __shared__ float slot[2][16][1];
+  Team<kLanes> team(a.waves);
+  const uint64_t step = (uint64_t)gridDim.x * team.groups;
+  uint64_t base = (uint64_t)blockIdx.x * team.groups, row = base + team.group;
+  float bias[kKeep ? V : 1][CH], gamma[kKeep ? V : 1][CH], beta[kKeep ? V : 1][CH];
+  FwdIn<T, R, kX, kOnce, CH> next[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const uint32_t c = (j * kTpr + t) * CH;
+    const uint32_t c = (j * team.threads + team.t) * CH;
     if (row < a.rows) next[j].load(a, row, c);
-    if (kX) load_param<CH, T>(a.bias, a.params_f32, c, a.cols, 0.0f, bias[j]);
-    load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, gamma[j]);
-    load_param<CH, T>(a.beta, a.params_f32, c, a.cols, 0.0f, beta[j]);
+    if constexpr (kKeep) {
+      if (kX) load_param<CH, T>(a.bias, a.params_f32, c, a.cols, 0.0f, bias[j]);
+      load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, gamma[j]);
+      load_param<CH, T>(a.beta, a.params_f32, c, a.cols, 0.0f, beta[j]);
+    }
   }
+  const float inv = 1.0f / (float)a.cols;
   // every wave of a work-group runs the same rounds: the sums have barriers
-  for (uint64_t base = (uint64_t)blockIdx.x * kRows; base < a.rows; base += step, row += step) {
+  for (; base < a.rows; base += step, row += step) {
+    if (V * CH > 8) __asm__ volatile("" : "+v"(team.t));  // addresses are made anew each round, not kept
     float v[V][CH], s[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      next[j].value(a, row, (j * kTpr + t) * CH, bias[j], v[j]);
+      const uint32_t c = (j * team.threads + team.t) * CH;
+      if (kX && !kKeep) load_param<CH, T>(a.bias, a.params_f32, c, a.cols, 0.0f, bias[0]);
+      next[j].value(a, row, c, bias[kKeep ? j : 0], v[j]);
 #pragma unroll
       for (int e = 0; e < CH; ++e) s[0] += v[j][e];
+      if (!kKeep) __builtin_amdgcn_sched_barrier(0);  // one chunk's temporaries at a time
     }
     if (row + step < a.rows)
 #pragma unroll
-      for (int j = 0; j < V; ++j) next[j].load(a, row + step, (j * kTpr + t) * CH);
-    row_sums<kTpr>(s, slot[0]);
-    const float mean = s[0] / (float)a.cols;
+      for (int j = 0; j < V; ++j) next[j].load(a, row + step, (j * team.threads + team.t) * CH);
+    row_sums<kLanes>(s, slot[0], team.group, a.waves);
+    const float mean = s[0] * inv;
     float m2[1] = {0.0f};
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int nv = (int)(a.cols - (j * kTpr + t) * CH);
+      const uint32_t c = (j * team.threads + team.t) * CH;
+      const int nv = (int)(a.cols - c);
+      if (a.sum && nv > 0 && row < a.rows) store_chunk<CH>((R *)a.sum + row * a.lds + c, nv, v[j]);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) v[j][e] -= mean;
       if (nv < CH)  // past the end: no distance from the mean
 #pragma unroll
-        for (int e = 0; e < CH; ++e) v[j][e] = e < nv ? v[j][e] : mean;
+        for (int e = 0; e < CH; ++e) v[j][e] = e < nv ? v[j][e] : 0.0f;
 #pragma unroll
-      for (int e = 0; e < CH; ++e) {
-        const float d = v[j][e] - mean;
-        m2[0] = __builtin_fmaf(d, d, m2[0]);
-      }
+      for (int e = 0; e < CH; ++e) m2[0] = __builtin_fmaf(v[j][e], v[j][e], m2[0]);
     }
-    row_sums<kTpr>(m2, slot[1]);
-    const float rstd = rstd_of(m2[0], a.cols, a.eps);
+    row_sums<kLanes>(m2, slot[1], team.group, a.waves);
+    const float rstd = rsqrt_any(__builtin_fmaf(m2[0], inv, a.eps));
     if (row < a.rows) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        norm_out<T, R, CH>(a, row, (j * kTpr + t) * CH, mean, rstd, gamma[j], beta[j], v[j]);
-      if (t == 0) {
+      for (int j = 0; j < V; ++j) {
+        const uint32_t c = (j * team.threads + team.t) * CH;
+        if constexpr (!kKeep) {
+          load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, gamma[0]);
+          load_param<CH, T>(a.beta, a.params_f32, c, a.cols, 0.0f, beta[0]);
+        }
+        norm_out<T, CH>(a, row, c, rstd, gamma[kKeep ? j : 0], beta[kKeep ? j : 0], v[j]);
+        if (!kKeep) __builtin_amdgcn_sched_barrier(0);
+      }
+      if (team.t == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
       }
@@ -279,9 +344,10 @@ template <class T, class R, bool kX>
 __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
   constexpr int CH = kChunk<T, R>, kTpr = 1024;
   __shared__ float slot[2][kTpr / 64][1];
+  const float inv = 1.0f / (float)a.cols;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const auto chunk = [&](uint32_t c, float *v) {
-      FwdIn<T, R, kX, CH> in;
+      FwdIn<T, R, kX, false, CH> in;
       float bias[CH];
       in.load(a, row, c);
       if (kX) load_param<CH, T>(a.bias, a.params_f32, c, a.cols, 0.0f, bias);
@@ -294,8 +360,8 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
 #pragma unroll
       for (int e = 0; e < CH; ++e) s[0] += e < nv ? v[e] : 0.0f;
     }
-    row_sums<kTpr>(s, slot[0]);
-    const float mean = s[0] / (float)a.cols;
+    row_sums<64>(s, slot[0], 0, kTpr / 64);
+    const float mean = s[0] * inv;
     float m2[1] = {0.0f};
     for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
       chunk(c, v);
@@ -306,14 +372,17 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
         m2[0] = __builtin_fmaf(d, d, m2[0]);
       }
     }
-    row_sums<kTpr>(m2, slot[1]);
-    const float rstd = rstd_of(m2[0], a.cols, a.eps);
+    row_sums<64>(m2, slot[1], 0, kTpr / 64);
+    const float rstd = rsqrt_any(__builtin_fmaf(m2[0], inv, a.eps));
     for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
       float gamma[CH], beta[CH];
       chunk(c, v);
       load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, gamma);
       load_param<CH, T>(a.beta, a.params_f32, c, a.cols, 0.0f, beta);
-      norm_out<T, R, CH>(a, row, c, mean, rstd, gamma, beta, v);
+      if (a.sum) store_chunk<CH>((R *)a.sum + row * a.lds + c, (int)(a.cols - c), v);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) v[e] -= mean;
+      norm_out<T, CH>(a, row, c, rstd, gamma, beta, v);
     }
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -323,21 +392,22 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
 }
 
 // ---- backward --------------------------------------------------------------------------
-// Layer norm's gradient for one element: rstd (g - mean(g) - h mean(g h)).
-__device__ __forceinline__ float norm_grad(float g, float h, float rstd, float mg, float mgh) {
-  return rstd * __builtin_fmaf(-h, mgh, g - mg);
+// Layer norm's gradient for one element, rstd (g - mean(g) - h mean(g h)), with
+// a = -rstd mean(g) and b = -rstd mean(g h).
+__device__ __forceinline__ float norm_grad(float g, float h, float rstd, float a, float b) {
+  return __builtin_fmaf(h, b, __builtin_fmaf(g, rstd, a));
 }
 
 // A chunk of a row's inputs as loaded.  dy is of type D: T, or R for dropout-add's gradient.
-template <class T, class R, class D, bool kNorm, int CH>
+template <class T, class R, class D, bool kNorm, bool kOnce, int CH>
 struct BwdIn {
   Chunk<D, CH> dy;
   Chunk<R, CH> sum, dsum;
   __device__ __forceinline__ void load(const BwdArgs &a, uint64_t row, uint32_t c) {
     const uint32_t at = chunk_at<CH>(c, a.cols);
-    dy = load_once<CH>((const D *)a.dy + row * a.lddy + at);
-    if (kNorm) sum = load_once<CH>((const R *)a.sum + row * a.lds + at);
-    if (a.dsum) dsum = load_once<CH>((const R *)a.dsum + row * a.ldds + at);
+    dy = load_chunk<kOnce, CH>((const D *)a.dy + row * a.lddy + at);
+    if (kNorm) sum = load_chunk<kOnce, CH>((const R *)a.sum + row * a.lds + at);
+    if (a.dsum) dsum = load_chunk<kOnce, CH>((const R *)a.dsum + row * a.ldds + at);
   }
   // h of every element
   __device__ __forceinline__ void normed(int nv, float mean, float rstd, float *h) const {
@@ -367,19 +437,19 @@ struct BwdIn {
 // takes every gridDim.x-th set of rows and keeps the column sums of its own rows in registers;
 // at the end its groups' sums are added up through LDS and written to the workspace, one line
 // of partial sums per work-group, which k_finish adds up in order.
-template <class T, class R, bool kX, bool kBias, int CH, int kTpr, int V, int kBlk>
-__global__ __launch_bounds__(kBlk) void k_norm_bwd(BwdArgs a) {
-  constexpr int kRows = kBlk / kTpr, kSums = kBias ? 3 : 2;
-  __shared__ float slot[2][kBlk / 64][2];
-  const uint32_t t = threadIdx.x % kTpr, group = row_group<kTpr>();
-  const uint64_t step = (uint64_t)gridDim.x * kRows;
-  uint64_t row = (uint64_t)blockIdx.x * kRows + group;
+template <class T, class R, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
+__global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
+  constexpr int kSums = kBias ? 3 : 2;
+  __shared__ float slot[2][16][2];
+  const Team<kLanes> team(a.waves);
+  const uint64_t step = (uint64_t)gridDim.x * team.groups;
+  uint64_t base = (uint64_t)blockIdx.x * team.groups, row = base + team.group;
   const float inv = 1.0f / (float)a.cols;
   float acc[kSums][V][CH], gamma[V][CH], mean = 0.0f, rstd = 0.0f;
-  BwdIn<T, R, T, true, CH> next[V];
+  BwdIn<T, R, T, true, kOnce, CH> next[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const uint32_t c = (j * kTpr + t) * CH;
+    const uint32_t c = (j * team.threads + team.t) * CH;
     if (row < a.rows) next[j].load(a, row, c);
     load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, gamma[j]);
 #pragma unroll
@@ -392,80 +462,84 @@ __global__ __launch_bounds__(kBlk) void k_norm_bwd(BwdArgs a) {
     rstd = a.rstd[row];
   }
   int par = 0;  // the slot in use: one barrier a round keeps the other one safe to write
-  for (uint64_t base = (uint64_t)blockIdx.x * kRows; base < a.rows; base += step, row += step, par ^= 1) {
+  for (; base < a.rows; base += step, row += step, par ^= 1) {
     const bool here = row < a.rows;
     const float m = mean, rs = rstd;
-    BwdIn<T, R, T, true, CH> in[V];
+    BwdIn<T, R, T, true, kOnce, CH> in[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) in[j] = next[j];
     if (row + step < a.rows) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) next[j].load(a, row + step, (j * kTpr + t) * CH);
+      for (int j = 0; j < V; ++j) next[j].load(a, row + step, (j * team.threads + team.t) * CH);
       mean = a.mean[row + step];
       rstd = a.rstd[row + step];
     }
-    float s[2] = {0.0f, 0.0f};
+    float g[V][CH], h[V][CH], s[2] = {0.0f, 0.0f};
     if (here) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const int nv = (int)(a.cols - (j * kTpr + t) * CH);
-        float g[CH], h[CH];
-        unpack<CH, T>(in[j].dy, nv, g);
-        in[j].normed(nv, m, rs, h);
+        const int nv = (int)(a.cols - (j * team.threads + team.t) * CH);
+        unpack<CH, T>(in[j].dy, nv, g[j]);
+        in[j].normed(nv, m, rs, h[j]);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
-          acc[0][j][e] = __builtin_fmaf(g[e], h[e], acc[0][j][e]);
-          acc[1][j][e] += g[e];
-          const float w = g[e] * gamma[j][e];
-          s[0] += w;
-          s[1] = __builtin_fmaf(w, h[e], s[1]);
+          acc[0][j][e] = __builtin_fmaf(g[j][e], h[j][e], acc[0][j][e]);
+          acc[1][j][e] += g[j][e];
+          g[j][e] *= gamma[j][e];
+          s[0] += g[j][e];
+          s[1] = __builtin_fmaf(g[j][e], h[j][e], s[1]);
         }
       }
     }
-    row_sums<kTpr>(s, slot[par]);
+    row_sums<kLanes>(s, slot[par], team.group, a.waves);
+    const float ka = -rs * (s[0] * inv), kb = -rs * (s[1] * inv);
     if (here) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const uint32_t c = (j * kTpr + t) * CH;
-        const int nv = (int)(a.cols - c);
-        float g[CH], h[CH];
-        stay_packed(in[j].dy);
-        stay_packed(in[j].sum);
-        unpack<CH, T>(in[j].dy, nv, g);
-        in[j].normed(nv, m, rs, h);
+        const uint32_t c = (j * team.threads + team.t) * CH;
 #pragma unroll
-        for (int e = 0; e < CH; ++e) g[e] = norm_grad(g[e] * gamma[j][e], h[e], rs, s[0] * inv, s[1] * inv);
-        in[j].template out<kX>(a, row, c, g);
+        for (int e = 0; e < CH; ++e) g[j][e] = norm_grad(g[j][e], h[j][e], rs, ka, kb);
+        in[j].template out<kX>(a, row, c, g[j]);
         if constexpr (kBias) {
 #pragma unroll
-          for (int e = 0; e < CH; ++e) acc[2][j][e] += g[e];
+          for (int e = 0; e < CH; ++e) acc[2][j][e] += g[j][e];
         }
       }
     }
   }
   if (!a.partial) return;
-  constexpr int kCols = kTpr * V * CH;
-  __shared__ float tile[kRows > 1 ? kRows : 1][kRows > 1 ? kCols : 1];
+  // The groups' sums of the same columns: first over the groups of a wave, in registers, then
+  // over the waves, one vector at a time through (dynamic) LDS.
+  constexpr uint32_t kWaveCols = (kLanes < 64 ? kLanes : 64) * V * CH;
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = kLanes < 64 ? 1 : a.waves;
+  const uint32_t groups = (blockDim.x >> 6) / waves;
+  extern __shared__ float tile[];
 #pragma unroll
   for (int k = 0; k < kSums; ++k) {
     float *line = a.partial + ((uint64_t)k * gridDim.x + blockIdx.x) * a.cols;
-    if constexpr (kRows > 1) {
-      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < V; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < CH; ++e) tile[group][(j * kTpr + t) * CH + e] = acc[k][j][e];
+      for (int e = 0; e < CH; ++e) acc[k][j][e] = groups_sum<kLanes>(acc[k][j][e]);
+    if (groups > 1) {
+      if (k) __syncthreads();
+      if (lane < kLanes)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int e = 0; e < CH; ++e)
+            tile[wave / waves * (waves * kWaveCols) + (j * team.threads + team.t) * CH + e] = acc[k][j][e];
       __syncthreads();
-      for (uint32_t c = threadIdx.x; c < kCols && c < a.cols; c += kBlk) {
+      for (uint32_t c = threadIdx.x; c < a.cols; c += blockDim.x) {
         float s = 0.0f;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) s += tile[r][c];
+#pragma unroll 8
+        for (uint32_t r = 0; r < groups; ++r) s += tile[r * (waves * kWaveCols) + c];
         line[c] = s;
       }
-    } else {
+    } else if (lane < kLanes) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const uint32_t c = (j * kTpr + t) * CH;
+        const uint32_t c = (j * team.threads + team.t) * CH;
         const int nv = (int)(a.cols - c);
 #pragma unroll
         for (int e = 0; e < CH; ++e)
@@ -475,8 +549,8 @@ __global__ __launch_bounds__(kBlk) void k_norm_bwd(BwdArgs a) {
   }
 }
 
-// Rows wider than k_norm_bwd's registers hold with their column sums: first mean(g) and
-// mean(g h) of every row, then k_cols_bwd over columns.
+// Rows wider than k_norm_bwd's registers hold with their column sums: first norm_grad's two
+// numbers for every row, then k_cols_bwd over columns.
 template <class T, class R>
 __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
   constexpr int CH = kChunk<T, R>, kTpr = 1024;
@@ -500,10 +574,10 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
         s[1] = __builtin_fmaf(x, (h[e] - mean) * rstd, s[1]);
       }
     }
-    row_sums<kTpr>(s, slot[par]);
+    row_sums<64>(s, slot[par], 0, kTpr / 64);
     if (threadIdx.x == 0) {
-      a.stats[2 * row] = s[0] / (float)a.cols;
-      a.stats[2 * row + 1] = s[1] / (float)a.cols;
+      a.stats[2 * row] = -rstd * (s[0] / (float)a.cols);
+      a.stats[2 * row + 1] = -rstd * (s[1] / (float)a.cols);
     }
   }
 }
@@ -511,11 +585,11 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
 // A strip of 64 lanes' chunks by a range of rows, four waves taking every fourth row: each
 // lane keeps the sums of its own columns.  kNorm: layer norm's gradient with the row's means
 // from k_row_stats; else dy (of the residual stream's type) is the sum's gradient itself.
-template <class T, class R, bool kNorm, bool kX, bool kBias, int CH>
+template <class T, class R, bool kNorm, bool kX, bool kBias, bool kOnce, int CH>
 __global__ __launch_bounds__(256) void k_cols_bwd(BwdArgs a) {
   constexpr int kSums = (kNorm ? 2 : 0) + (kBias ? 1 : 0);
   typedef typename std::conditional<kNorm, T, R>::type D;
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t lane = threadIdx.x & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t c = (blockIdx.x * 64 + lane) * CH;
   const int nv = (int)(a.cols - c);
   const uint64_t r0 = (uint64_t)blockIdx.y * a.rows_per_block;
@@ -528,21 +602,23 @@ __global__ __launch_bounds__(256) void k_cols_bwd(BwdArgs a) {
   if (nv > 0) {
     float w[CH];
     if (kNorm) load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, w);
-#pragma unroll 2
-    for (uint64_t row = r0 + wave; row < r1; row += 4) {
-      BwdIn<T, R, D, kNorm, CH> in;
-      in.load(a, row, c);
+    BwdIn<T, R, D, kNorm, kOnce, CH> next;
+    uint64_t row = r0 + wave;
+    if (row < r1) next.load(a, row, c);
+    for (; row < r1; row += 4) {
+      const BwdIn<T, R, D, kNorm, kOnce, CH> in = next;
+      if (row + 4 < r1) next.load(a, row + 4, c);
       float v[CH];
       unpack<CH, D>(in.dy, nv, v);
       if constexpr (kNorm) {
-        const float rstd = a.rstd[row], mg = a.stats[2 * row], mgh = a.stats[2 * row + 1];
+        const float rstd = a.rstd[row], ka = a.stats[2 * row], kb = a.stats[2 * row + 1];
         float h[CH];
         in.normed(nv, a.mean[row], rstd, h);
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
           acc[0][e] = __builtin_fmaf(v[e], h[e], acc[0][e]);
           acc[1][e] += v[e];
-          v[e] = norm_grad(v[e] * w[e], h[e], rstd, mg, mgh);
+          v[e] = norm_grad(v[e] * w[e], h[e], rstd, ka, kb);
         }
       }
       in.template out<kX>(a, row, c, v);
@@ -572,126 +648,172 @@ __global__ __launch_bounds__(256) void k_cols_bwd(BwdArgs a) {
 }
 
 // ---- dropout-add, element by element ---------------------------------------------------
-// Chunk n of the call lies in row n / chunks_per_row (a product with the rounded-up
-// reciprocal: exact below 2^31 chunks, which a launch stays under).
-template <class TI, class TO, bool kDivide, int CH, class TP>
-__global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
-  const uint32_t n = blockIdx.x * 256u + threadIdx.x;
-  if (n >= a.chunks) return;
-  const uint32_t r = a.div_shift < 0 ? n : __umulhi(n, a.div_mul) >> a.div_shift;
-  const uint64_t c = (uint64_t)(n - r * a.chunks_per_row) * CH, row = a.row0 + r, at = chunk_at<CH>(c, a.cols64);
-  const int nv = a.cols64 - c < CH ? (int)(a.cols64 - c) : CH;
-  const Chunk<TI, CH> x = load_once<CH>((const TI *)a.x + row * a.ldx + at);
+// Chunk n of the call lies in row n / chunks_per_row.  A work-group's first row is found on the
+// scalar unit and its lanes' rows from there, a few rows further: one product a matrix.  The
+// quotient is a product with the rounded-up reciprocal: exact below 2^31 chunks, which a launch
+// stays under.
+__device__ __forceinline__ uint32_t row_of(const AddArgs &a, uint32_t n) {
+  return a.div_shift < 0 ? n : __umulhi(n, a.div_mul) >> a.div_shift;
+}
+
+template <class TI, class TO, bool kOnce, int CH>
+struct AddChunk {
+  uint64_t row0, c;
+  uint32_t dr;
+  Chunk<TI, CH> x;
   Chunk<TO, CH> d;
-  if (a.residual) d = load_once<CH>((const TO *)a.residual + row * a.ldr + at);
+  __device__ __forceinline__ uint64_t at(uint64_t ld, uint64_t column) const {
+    return row0 * ld + ((uint64_t)dr * (uint32_t)ld + column);
+  }
+  __device__ __forceinline__ void load(const AddArgs &a, uint32_t first) {
+    const uint32_t r0 = row_of(a, first), n = first - r0 * a.chunks_per_row + threadIdx.x;  // from that row's start
+    row0 = a.row0 + r0;
+    dr = row_of(a, n);
+    c = (uint64_t)(n - dr * a.chunks_per_row) * CH;
+    if (first + threadIdx.x >= a.chunks) return;
+    const uint64_t from = chunk_at<CH>(c, a.cols64);
+    x = load_chunk<kOnce, CH>((const TI *)a.x + at(a.ldx, from));
+    if (a.residual) d = load_chunk<kOnce, CH>((const TO *)a.residual + at(a.ldr, from));
+  }
+};
+
+template <class TI, class TO, bool kDivide, bool kOnce, int CH, class TP>
+__global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
+  const uint32_t first = blockIdx.x * 256u;
+  AddChunk<TI, TO, kOnce, CH> p;
+  p.load(a, first);
+  if (first + threadIdx.x >= a.chunks) return;
+  const int nv = a.cols64 - p.c < CH ? (int)(a.cols64 - p.c) : CH;
   float v[CH];
+  unpack<CH, TI>(p.x, nv, v);
   if (a.bias) {
     float b[CH];
-    load_param<CH, TP>(a.bias, a.params_f32, (uint32_t)c, (uint32_t)a.cols64, 0.0f, b);
-    unpack<CH, TI>(x, nv, v);
+    load_param<CH, TP>(a.bias, a.params_f32, (uint32_t)p.c, (uint32_t)a.cols64, 0.0f, b);
 #pragma unroll
     for (int e = 0; e < CH; ++e) v[e] += b[e];
-  } else {
-    unpack<CH, TI>(x, nv, v);
   }
-  if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)(row * a.cols64 + c), v);
+  if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)p.at(a.cols64, p.c), v);
   if (a.residual) {
-    float u[CH];
-    unpack<CH, TO>(d, nv, u);
+    float t[CH];
+    unpack<CH, TO>(p.d, nv, t);
 #pragma unroll
-    for (int e = 0; e < CH; ++e) v[e] += u[e];
+    for (int e = 0; e < CH; ++e) v[e] += t[e];
   }
-  store_chunk<CH>((TO *)a.y + row * a.ldy + c, nv, v);
+  store_chunk<CH>((TO *)a.y + p.at(a.ldy, p.c), nv, v);
 }
 
 // ---- launches --------------------------------------------------------------------------
-// Work-groups over sets of rows; the kernels loop beyond (a launch holds fewer than 2^32 threads).
+// Work-groups over sets of rows; the kernels loop beyond.
 static inline uint32_t row_grid(uint64_t sets, uint32_t most) { return (uint32_t)(sets < most ? sets : most); }
 
-#ifndef TK_FWD_GRID
-#define TK_FWD_GRID 1024
-#endif
-template <class T, class R, bool kX, int CH, int kTpr, int V, int kBlk>
-static void launch_fwd(const FwdArgs &a, hipStream_t s) {
-  constexpr int kRows = kBlk / kTpr;
-  hipLaunchKernelGGL((k_norm_fwd<T, R, kX, CH, kTpr, V, kBlk>), dim3(row_grid((a.rows + kRows - 1) / kRows, TK_FWD_GRID)),
-                     dim3(kBlk), 0, s, a);
+// About 20 waves a compute unit, each set of rows prefetched: layer norm bf16 32768x2048 takes
+// 61, 49, 46, 45, 48 and 55 us with 8, 12, 16, 20, 24 and 32 waves, and 71 us with a work-group
+// for each row and no prefetch; the fused forward 8192x4096 49 to 53 us, and 62.
+constexpr uint32_t kFwdWaves = 20;
+
+template <class T, class R, bool kX, bool kOnce, int CH, int kLanes, int V, bool kKeep = true>
+static void launch_fwd(FwdArgs a, hipStream_t s) {
+  constexpr uint32_t kCols = kLanes * V * CH;
+  a.waves = kLanes < 64 ? 1 : (a.cols + kCols - 1) / kCols;
+  const uint32_t waves = a.waves >= 4 ? a.waves : 4 / a.waves * a.waves;  // of a work-group
+  const uint32_t rows = kLanes < 64 ? 64 * waves / kLanes : waves / a.waves;
+  const uint32_t most = 256 * (waves < kFwdWaves ? kFwdWaves / waves : 1);
+  hipLaunchKernelGGL((k_norm_fwd<T, R, kX, kOnce, CH, kLanes, V, kKeep>), dim3(row_grid((a.rows + rows - 1) / rows, most)),
+                     dim3(64 * waves), 0, s, a);
 }
 
-template <class T, class R, bool kX>
+// Lanes to a row by its width, eight elements a lane.  Beyond ten waves a row (5120 columns) a
+// lane takes sixteen, so that several rows share a compute unit (layer norm bf16 8192x8192: 46
+// against 53 us; f16 4095x5001 at ten waves of eight elements 38 against 41), and beyond
+// sixteen waves of those thirty-two, with the parameters read again for every row.
+template <class T, class R, bool kX, bool kOnce>
 static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   constexpr int CH = kChunk<T, R>, K = 8 / CH;
-  if (a.cols < CH) launch_fwd<T, R, kX, 1, 16, 1, 256>(a, s);
-  else if (a.cols <= 128) launch_fwd<T, R, kX, CH, 16, K, 256>(a, s);
-  else if (a.cols <= 512) launch_fwd<T, R, kX, CH, 64, K, 256>(a, s);
-  else if (a.cols <= 1024) launch_fwd<T, R, kX, CH, 64, 2 * K, 256>(a, s);
-  else if (a.cols <= 2048) launch_fwd<T, R, kX, CH, 256, K, 256>(a, s);
-  else if (a.cols <= 4096) launch_fwd<T, R, kX, CH, 512, K, 512>(a, s);
-  else if (a.cols <= 8192) launch_fwd<T, R, kX, CH, 1024, K, 1024>(a, s);
-  else if (a.cols <= 16384) launch_fwd<T, R, kX, CH, 1024, 2 * K, 1024>(a, s);
+  if (a.cols < CH) launch_fwd<T, R, kX, kOnce, 1, 8, 1>(a, s);
+  else if (a.cols <= 64) launch_fwd<T, R, kX, kOnce, CH, 8, K>(a, s);
+  else if (a.cols <= 128) launch_fwd<T, R, kX, kOnce, CH, 16, K>(a, s);
+  else if (a.cols <= 256) launch_fwd<T, R, kX, kOnce, CH, 32, K>(a, s);
+  else if (a.cols <= 5120) launch_fwd<T, R, kX, kOnce, CH, 64, K>(a, s);
+  else if (a.cols <= 16384) launch_fwd<T, R, kX, kOnce, CH, 64, 2 * K>(a, s);
+  else if (a.cols <= 32768) launch_fwd<T, R, kX, kOnce, CH, 64, 4 * K, false>(a, s);
   else hipLaunchKernelGGL((k_norm_fwd_wide<T, R, kX>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
+}
+
+template <class T, class R, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
+static void launch_bwd(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
+  const uint32_t lds = p.waves > (int)a.waves ? (uint32_t)p.waves * kLanes * V * CH * 4 : 0;
+  hipLaunchKernelGGL((k_norm_bwd<T, R, kX, kBias, kOnce, CH, kLanes, V>), dim3((uint32_t)p.lines), dim3(64 * p.waves), lds, s,
+                     a);
+}
+
+template <class T, class R, bool kX, bool kBias, bool kOnce>
+static void norm_bwd_as(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
+  constexpr int CH = kChunk<T, R>, K = 8 / CH;
+  if (a.cols < CH) launch_bwd<T, R, kX, kBias, kOnce, 1, 8, 1>(a, p, s);
+  else if (p.lanes == 8) launch_bwd<T, R, kX, kBias, kOnce, CH, 8, K>(a, p, s);
+  else if (p.lanes == 16) launch_bwd<T, R, kX, kBias, kOnce, CH, 16, K>(a, p, s);
+  else if (p.lanes == 32) launch_bwd<T, R, kX, kBias, kOnce, CH, 32, K>(a, p, s);
+  else launch_bwd<T, R, kX, kBias, kOnce, CH, 64, K>(a, p, s);
+}
+
+template <class T, class R, bool kNorm, bool kX, bool kBias, bool kOnce>
+static void cols_bwd_as(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
+  const dim3 g((uint32_t)p.strips, (uint32_t)p.lines);
+  if (!kNorm && a.cols < kChunk<T, R>)
+    hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kOnce, kNorm ? kChunk<T, R> : 1>), g, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kOnce, kChunk<T, R>>), g, dim3(256), 0, s, a);
 }
 
 template <class T, class R, bool kX, bool kBias>
 static void norm_bwd_of(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
-  constexpr int CH = kChunk<T, R>, K = 8 / CH;
-  const dim3 g((uint32_t)p.lines);
-#define TK_BWD(CHUNK, TPR, V, BLK) \
-  hipLaunchKernelGGL((k_norm_bwd<T, R, kX, kBias, CHUNK, TPR, V, BLK>), g, dim3(BLK), 0, s, a)
-  if (a.cols < CH) TK_BWD(1, 16, 1, 256);
-  else if (p.tpr == 16) TK_BWD(CH, 16, K, 512);
-  else if (p.tpr == 64) TK_BWD(CH, 64, K, 512);
-  else if (p.tpr == 128) TK_BWD(CH, 128, K, 512);
-  else if (p.tpr == 256) TK_BWD(CH, 256, K, 512);
-  else if (p.tpr == 512) TK_BWD(CH, 512, K, 512);
-  else if (p.ept == 8) TK_BWD(CH, 1024, K, 1024);
-  else TK_BWD(CH, 1024, 2 * K, 1024);
-#undef TK_BWD
+  if (p.lanes == 0) {  // wide rows
+    hipLaunchKernelGGL((k_row_stats<T, R>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
+    if (a.once) cols_bwd_as<T, R, true, kX, kBias, true>(a, p, s);
+    else cols_bwd_as<T, R, true, kX, kBias, false>(a, p, s);
+  } else if (a.once) {
+    norm_bwd_as<T, R, kX, kBias, true>(a, p, s);
+  } else {
+    norm_bwd_as<T, R, kX, kBias, false>(a, p, s);
+  }
 }
 
-template <class T, class R, bool kNorm, bool kX, bool kBias>
-static void cols_bwd_of(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
-  const dim3 g((uint32_t)p.strips, (uint32_t)p.lines);
-  if (!kNorm && a.cols < kChunk<T, R>)
-    hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kNorm ? kChunk<T, R> : 1>), g, dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kChunk<T, R>>), g, dim3(256), 0, s, a);
-}
-
-template <class TI, class TO, bool kDivide, class TP>
-static void drop_add_of(const AddArgs &a, int chunk, hipStream_t s) {
+template <class TI, class TO, bool kDivide, class TP, bool kOnce>
+static void drop_add_as(const AddArgs &a, int chunk, hipStream_t s) {
   const dim3 g((a.chunks + 255) / 256);
-  if (chunk == 1) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, 1, TP>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
+  if (chunk == 1) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, 1, TP>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
+}
+
+template <class TI, class TO, class TP>
+static void drop_add_of(const AddArgs &a, int chunk, hipStream_t s) {
+  constexpr bool kDivide = std::is_same<TP, float>::value;
+  if (a.once) drop_add_as<TI, TO, kDivide, TP, true>(a, chunk, s);
+  else drop_add_as<TI, TO, kDivide, TP, false>(a, chunk, s);
 }
 
 template <class T, class R>
 struct RowKernels {
   static void norm_fwd(const FwdArgs &a, hipStream_t s) {
-    if (a.x) norm_fwd_of<T, R, true>(a, s);
-    else norm_fwd_of<T, R, false>(a, s);
+    if (a.x) {
+      if (a.once) norm_fwd_of<T, R, true, true>(a, s);
+      else norm_fwd_of<T, R, true, false>(a, s);
+    } else {
+      if (a.once) norm_fwd_of<T, R, false, true>(a, s);
+      else norm_fwd_of<T, R, false, false>(a, s);
+    }
   }
   static void norm_bwd(const BwdArgs &a, const BwdPlan &p, bool bias, hipStream_t s) {
-    if (p.tpr == 0) {  // wide rows
-      hipLaunchKernelGGL((k_row_stats<T, R>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
-      if (!a.dx) cols_bwd_of<T, R, true, false, false>(a, p, s);
-      else if (!bias) cols_bwd_of<T, R, true, true, false>(a, p, s);
-      else cols_bwd_of<T, R, true, true, true>(a, p, s);
-      return;
-    }
     if (!a.dx) norm_bwd_of<T, R, false, false>(a, p, s);
     else if (!bias) norm_bwd_of<T, R, true, false>(a, p, s);
     else norm_bwd_of<T, R, true, true>(a, p, s);
   }
   static void add_bwd_sums(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
-    cols_bwd_of<T, R, false, true, true>(a, p, s);
+    if (a.once) cols_bwd_as<T, R, false, true, true, true>(a, p, s);
+    else cols_bwd_as<T, R, false, true, true, false>(a, p, s);
   }
-  static void add_fwd(const AddArgs &a, int chunk, hipStream_t s) {
-    drop_add_of<T, R, std::is_same<T, float>::value, T>(a, chunk, s);
-  }
-  static void add_bwd(const AddArgs &a, int chunk, hipStream_t s) {
-    drop_add_of<R, T, std::is_same<T, float>::value, T>(a, chunk, s);
-  }
+  static void add_fwd(const AddArgs &a, int chunk, hipStream_t s) { drop_add_of<T, R, T>(a, chunk, s); }
+  static void add_bwd(const AddArgs &a, int chunk, hipStream_t s) { drop_add_of<R, T, T>(a, chunk, s); }
   static RowTable table() { return {kChunk<T, R>, norm_fwd, norm_bwd, add_bwd_sums, add_fwd, add_bwd}; }
 };
 

@@ -46,8 +46,9 @@ __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
 // ---------------------------------------------------------------------------------------
 // How a backward call is cut
 // ---------------------------------------------------------------------------------------
-constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 40;
-constexpr uint64_t kRowsInRegisters = 16384;  // columns that k_norm_bwd's largest shape holds
+constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 31;
+constexpr uint64_t kRowsInRegisters = 8192;      // columns that k_norm_bwd holds
+constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through the caches (tk_rows.h)
 
 // Strips of 64 lanes' chunks by ranges of rows: about eight work-groups a compute unit, of at
 // least eight rows each.
@@ -61,15 +62,19 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
   return p;
 }
 
+// Layer norm's: one work-group of up to 16 waves to a compute unit, as many rows at a time as
+// it has waves for, so that there are few lines of partial sums (fused backward bf16 8192x4096:
+// 68 us with two rows of eight waves to a work-group, 79 with one row and twice the lines).
+// Beyond 8192 columns the column sums do not fit the registers beside a row: two kernels and a
+// second read of dy and sum are faster (4096x16384: 166 against 286 us).
 static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
   if (cols > kRowsInRegisters) return strips_plan(chunk, rows, cols);
   BwdPlan p{};
-  p.tpr = cols <= 128 ? 16 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
-  p.ept = cols <= 8192 ? 8 : 16;
-  const uint64_t blk = cols < (uint64_t)chunk ? 256 : cols <= 4096 ? 512 : 1024;
-  const uint64_t per = blk / p.tpr, sets = (rows + per - 1) / per;
-  const uint64_t most = blk == 1024 ? 256 : 512;
-  p.lines = sets < most ? sets : most;
+  p.lanes = cols <= 64 ? 8 : cols <= 128 ? 16 : cols <= 256 ? 32 : 64;
+  p.row_waves = p.lanes < 64 ? 1 : (int)((cols + 511) / 512);
+  p.waves = 16 / p.row_waves * p.row_waves;
+  const uint64_t per = p.lanes < 64 ? 64 * p.waves / p.lanes : p.waves / p.row_waves, sets = (rows + per - 1) / per;
+  p.lines = sets < 256 ? sets : 256;
   return p;
 }
 
@@ -265,6 +270,7 @@ static tk_status dropout_add(RowType t, uint32_t key, uint64_t start, uint64_t r
   a.x = x; a.ldx = ldx; a.bias = bias; a.residual = residual; a.ldr = ldr; a.y = y; a.ldy = ldy;
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
+  a.once = rows * cols * (c.t() + (residual ? c.res() : 0)) > kCachedReads;
   const RowTable k = table_of(t, flags);
   return run_add(k.add_fwd, k.chunk, a, rows, cols, c.t(), c.res(), stream);
 }
@@ -292,6 +298,7 @@ static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, u
     AddArgs a{};
     a.x = dy; a.ldx = lddy; a.y = dx; a.ldy = lddx;
     a.drop = drop_of(key, start, p);
+    a.once = rows * cols * c.res() > kCachedReads;
     return run_add(k.add_bwd, k.chunk, a, rows, cols, c.res(), c.t(), stream);
   }
   const BwdPlan plan = strips_plan(k.chunk, rows, cols);
@@ -301,6 +308,7 @@ static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, u
   a.partial = (float *)workspace;
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
+  a.once = rows * cols * c.res() > kCachedReads;
   k.add_bwd_sums(a, plan, stream);
   if ((st = launch_status()) != TK_OK) return st;
   return finish(t, flags, a.partial, plan.lines, cols, dbias, nullptr, nullptr, stream);
@@ -334,6 +342,7 @@ static tk_status norm_forward(RowType t, bool fused, uint32_t key, uint64_t star
   a.rows = rows; a.cols = (uint32_t)cols; a.eps = eps;
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
+  a.once = rows * cols * ((fused ? c.t() : 0) + (residual ? c.res() : 0)) > kCachedReads;
   table_of(t, flags).norm_fwd(a, stream);
   return launch_status();
 }
@@ -375,11 +384,12 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   a.dy = dy; a.lddy = lddy; a.dsum = dsum; a.ldds = ldds; a.sum = sum; a.lds = lds;
   a.gamma = gamma; a.mean = mean; a.rstd = rstd;
   a.dx = dx; a.lddx = lddx; a.dresidual = dresidual; a.lddr = lddr;
-  a.rows = rows; a.cols = (uint32_t)cols; a.rows_per_block = plan.rows_per_block;
+  a.rows = rows; a.cols = (uint32_t)cols; a.rows_per_block = plan.rows_per_block; a.waves = (uint32_t)plan.row_waves;
   a.partial = sums ? (float *)workspace : nullptr;
-  a.stats = plan.tpr ? nullptr : (float *)((char *)workspace + need - 8 * rows);
+  a.stats = plan.lanes ? nullptr : (float *)((char *)workspace + need - 8 * rows);
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
+  a.once = rows * cols * (c.t() + (dsum ? 2 : 1) * c.res()) > kCachedReads;
   k.norm_bwd(a, plan, dbias != nullptr, stream);
   if ((st = launch_status()) != TK_OK || !sums) return st;
   return finish(t, flags, a.partial, plan.lines, cols, dgamma, dbeta, dbias, stream);

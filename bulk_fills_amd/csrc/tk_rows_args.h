@@ -21,9 +21,9 @@ struct FwdArgs {
   void *sum, *y;
   float *mean, *rstd;
   uint64_t rows, ldx, ldr, lds, ldy;
-  uint32_t cols;
+  uint32_t cols, waves;  // waves: of a row (kernels with a row to whole waves)
   float eps;
-  bool params_f32;
+  bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
 };
 
@@ -36,8 +36,8 @@ struct BwdArgs {
   float *partial;  // lines of partial column sums: dgamma's, dbeta's, then dbias's; null: no sums wanted
   float *stats;    // mean(g), mean(g h) of every row (wide rows)
   uint64_t rows, lddy, ldds, lds, lddx, lddr, rows_per_block;
-  uint32_t cols;
-  bool params_f32;
+  uint32_t cols, waves;
+  bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
 };
 
@@ -47,14 +47,15 @@ struct AddArgs {
   uint64_t row0, ldx, ldr, ldy, cols64;
   uint32_t chunks, chunks_per_row, div_mul;
   int div_shift;
-  bool params_f32;
+  bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
 };
 
-// How a backward call is cut: `lines` lines of partial sums; tpr threads a row with ept
-// elements each, or tpr = 0 and strips of columns.
+// How a backward call is cut: `lines` lines of partial sums.  Rows in registers: `lanes` lanes
+// to a row (64: row_waves whole waves), `waves` waves to a work-group.
+// Wide rows (lanes 0) and dropout-add: strips of columns.
 struct BwdPlan {
-  int tpr, ept;
+  int lanes, waves, row_waves;
   uint64_t lines, strips, rows_per_block;
 };
 

@@ -206,11 +206,11 @@ tk_status tk_dropout_backward_f32(uint32_t key, uint64_t start_draw, uint64_t n,
  *          Otherwise no output may share bytes with any other argument; slices of one buffer
  *          with one row pitch are told apart exactly, other matrices by their whole extent.
  *   p must lie in [0, 1) and eps be finite and >= 0, else TK_EINVAL.  rows and cols are below
- *          2^31 and ld below 2^40, else TK_ERANGE; start_draw + rows * cols <= 2^32 where
+ *          2^31 and so is ld, else TK_ERANGE; start_draw + rows * cols <= 2^32 where
  *          p > 0, else TK_ERANGE.  rows == 0 or cols == 0 is TK_OK: the forward calls and dx
  *          have nothing to write, gradients over rows == 0 are written as zeros.
  *   workspace: the backward calls that give dgamma, dbeta or dbias, and those of the layer
- *          norms at more than 16384 columns, need device memory of at least the size that
+ *          norms at more than 8192 columns, need device memory of at least the size that
  *          tk_backward_workspace_bytes names (64-bit count in *bytes; TK_ERANGE as above),
  *          4-byte aligned, else TK_EINVAL.  It holds nothing between calls; calls that may
  *          overlap in time (other streams, graphs replayed together) need one each.

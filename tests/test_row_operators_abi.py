@@ -93,7 +93,7 @@ def test_missing_misaligned_and_short_rows(t):
                      (both_b, ("lddy", "lds", "lddx", "lddr"))):
         for name in names:
             assert f(t, **{name: 7}) == EINVAL, (f.__name__, name)
-            assert f(t, **{name: 1 << 40}) == ERANGE, (f.__name__, name)
+            assert f(t, **{name: 1 << 31}) == ERANGE, (f.__name__, name)
     for name in ("bias", "gamma", "beta", "mean", "rstd"):
         assert both(t, **{name: H + 1}) == EINVAL
     for name in ("dgamma", "dbeta", "dbias"):
@@ -141,7 +141,7 @@ def test_workspace(t):
         assert f(t, **{name: H}, ws=WS, n=need - 1) == EINVAL
         assert f(t, **{name: H}, ws=WS + 2, n=need) == EINVAL
     # wide rows need one even without parameter gradients
-    assert norm_b(t, cols=16385, lddy=16385, ldx=16385, lddx=16385) == EINVAL
+    assert norm_b(t, cols=8193, lddy=8193, ldx=8193, lddx=8193) == EINVAL
     assert tk.tk_backward_workspace_bytes(0, 8) == 0 and tk.tk_backward_workspace_bytes(8, 0) == 0
     v = C.c_uint64()
     assert L.tk_backward_workspace_bytes(4, 8, None) == EINVAL
