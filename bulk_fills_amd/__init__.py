@@ -12,6 +12,7 @@ check that it holds n elements of the right size) or a raw device address (int).
 a torch.cuda.Stream to choose another.
 """
 import ctypes as C
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -238,6 +239,7 @@ def tk_dropout_backward_f32(key, start_draw, n, p, dy, dx, stream=None):
            "tk_dropout_backward_f32")
 
 
+@functools.lru_cache(maxsize=256)
 def tk_backward_workspace_bytes(rows, cols):
     """Device bytes that the row operators' backward calls need for their column sums."""
     v = C.c_uint64()
@@ -245,30 +247,43 @@ def tk_backward_workspace_bytes(rows, cols):
     return v.value
 
 
+# The current device and its current stream's handle, as torch.cuda.current_device() and
+# torch.cuda.current_stream() give them, without making a Stream object for every call: for one
+# row of 4096 columns half of the call's time on the host.
+_device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None)
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+if _device is None or _raw_stream is None:  # a torch without a GPU build, or another version's names
+    def _device():
+        return torch.cuda.current_device()
+
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+_SUMS_ALONE = 8192  # columns up to which a backward call needs its workspace for column sums alone
+
+
 class _Args:
     """Checks and marshals one row operator's buffers.  A matrix is a tensor of rows x cols (any
     shape that flattens to it, the last dimension contiguous), whose row distance is taken where
     the call gives None for its ld; or a raw address (ld None: cols)."""
 
-    __slots__ = ("where", "rows", "cols", "dtype", "residual", "params", "device")
+    __slots__ = ("where", "rows", "cols", "device")
 
-    def __init__(self, where, rows, cols, dtype, flags):
-        self.where, self.rows, self.cols, self.dtype = where, rows, cols, dtype
-        self.residual = torch.float32 if flags & TK_RESIDUAL_F32 else dtype
-        self.params = torch.float32 if flags & TK_PARAMS_F32 else dtype
-        self.device = None
+    def __init__(self, where, rows, cols):
+        self.where, self.rows, self.cols = where, rows, cols
+        self.device = -1
 
-    def _tensor(self, x, dtype):
+    def _address(self, x, dtype):
         if x.dtype is not dtype:
             raise ValueError(f"{self.where}: a buffer's type is {x.dtype}, not {dtype}")
         index = x.get_device()  # -1 on the host
-        if index != self.device:
+        if index != self.device or index < 0:
             if index < 0:
                 raise ValueError(f"{self.where}: buffer must live on a HIP device")
-            if index != torch.cuda.current_device():
+            if index != _device():
                 # the library launches on the calling thread's current device
-                raise ValueError(f"{self.where}: buffer is on {x.device}, the current device is "
-                                 f"cuda:{torch.cuda.current_device()}")
+                raise ValueError(f"{self.where}: buffer is on {x.device}, the current device is cuda:{_device()}")
             self.device = index
         return x.data_ptr()
 
@@ -276,34 +291,29 @@ class _Args:
         """(address, ld) of a matrix argument."""
         if x is None:
             return None, 0
+        cols = self.cols
         if isinstance(x, int):
-            return x, self.cols if ld is None else ld
-        ptr = self._tensor(x, dtype)
+            return x, cols if ld is None else ld
         if x.is_contiguous():
-            own = self.cols
-            fits = x.numel() == self.rows * self.cols and (ld is None or ld == own or self.rows <= 1)
-        else:
-            own = x.stride(-2) if x.dim() > 1 else self.cols
-            fits = tuple(x.shape) == (self.rows, self.cols) and (self.cols == 1 or x.stride(1) == 1)
-            if self.rows <= 1:  # one row has no distance to a next
-                own = self.cols
-            fits = fits and own >= self.cols and (ld is None or ld == own or self.rows <= 1)
-        if not fits:
-            raise ValueError(f"{self.where}: need a {self.rows} x {self.cols} matrix with contiguous rows that do not "
-                             f"overlap (and its own row distance as ld, or None), got shape {tuple(x.shape)}, strides "
-                             f"{x.stride()}, ld {ld}")
-        return ptr, own if ld is None else ld
+            if x.numel() == self.rows * cols and (ld is None or ld == cols or self.rows <= 1):
+                return self._address(x, dtype), cols if ld is None else ld
+        elif tuple(x.shape) == (self.rows, cols) and (cols == 1 or x.stride(1) == 1):
+            own = cols if self.rows <= 1 else x.stride(0)  # one row has no distance to a next
+            if own >= cols and (ld is None or ld == own or self.rows <= 1):
+                return self._address(x, dtype), own if ld is None else ld
+        raise ValueError(f"{self.where}: need a {self.rows} x {cols} matrix with contiguous rows that do not overlap (and "
+                         f"its own row distance as ld, or None), got shape {tuple(x.shape)}, strides {x.stride()}, ld {ld}")
 
     def vector(self, x, n, dtype):
         if x is None or isinstance(x, int):
             return x
         if x.numel() != n or not x.is_contiguous():
             raise ValueError(f"{self.where}: need a contiguous vector of {n} elements, got shape {tuple(x.shape)}")
-        return self._tensor(x, dtype)
+        return self._address(x, dtype)
 
-    def raw_stream(self, stream):
+    def stream(self, stream):
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
+            return _raw_stream(self.device if self.device >= 0 else _device())
         return stream if isinstance(stream, int) else stream.cuda_stream
 
     def workspace(self, x, stream, needed):
@@ -313,13 +323,13 @@ class _Args:
             n = tk_backward_workspace_bytes(self.rows, self.cols) if needed else 0
             if n == 0:
                 return None, 0, None
-            if stream is not None and self.raw_stream(stream) != self.raw_stream(None):
+            if stream is not None and self.stream(stream) != self.stream(None):
                 raise ValueError(f"{self.where}: a call on a stream that is not the current one needs a workspace")
             x = torch.empty(n, dtype=torch.uint8, device="cuda")
             return x.data_ptr(), n, x
         if not x.is_contiguous():
             raise ValueError(f"{self.where}: the workspace must be contiguous")
-        return self._tensor(x, x.dtype), x.numel() * x.element_size(), x
+        return self._address(x, x.dtype), x.numel() * x.element_size(), x
 
 
 def _row_operators(suffix, dtype):
@@ -329,73 +339,88 @@ def _row_operators(suffix, dtype):
     both_fwd = getattr(lib, "tk_dropout_add_layer_norm_" + suffix)
     both_bwd = getattr(lib, "tk_dropout_add_layer_norm_backward_" + suffix)
 
+    float32 = torch.float32
+
+    def residual_type(flags):
+        return float32 if flags & TK_RESIDUAL_F32 else dtype
+
+    def params_type(flags):
+        return float32 if flags & TK_PARAMS_F32 else dtype
+
     def dropout_add(key, start_draw, rows, cols, p, flags, x, ldx, bias, residual, ldr, y, ldy, stream=None):
         where = "tk_dropout_add_" + suffix
-        a = _Args(where, rows, cols, dtype, flags)
+        a = _Args(where, rows, cols)
+        res, par = residual_type(flags), params_type(flags)
         px, ldx = a.matrix(x, ldx, dtype)
-        pr, ldr = a.matrix(residual, ldr, a.residual)
-        py, ldy = a.matrix(y, ldy, a.residual)
-        pb = a.vector(bias, cols, a.params)
-        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, a.raw_stream(stream)), where)
+        pr, ldr = a.matrix(residual, ldr, res)
+        py, ldy = a.matrix(y, ldy, res)
+        pb = a.vector(bias, cols, par)
+        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, a.stream(stream)), where)
 
     def dropout_add_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dx, lddx, dbias, workspace=None, stream=None):
         where = "tk_dropout_add_backward_" + suffix
-        a = _Args(where, rows, cols, dtype, flags)
-        pdy, lddy = a.matrix(dy, lddy, a.residual)
+        a = _Args(where, rows, cols)
+        res, par = residual_type(flags), params_type(flags)
+        pdy, lddy = a.matrix(dy, lddy, res)
         pdx, lddx = a.matrix(dx, lddx, dtype)
-        pb = a.vector(dbias, cols, a.params)
+        pb = a.vector(dbias, cols, par)
         ws, n, keep = a.workspace(workspace, stream, dbias is not None)
-        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, a.raw_stream(stream)), where)
+        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, a.stream(stream)), where)
 
     def layer_norm(rows, cols, eps, flags, x, ldx, gamma, beta, y, ldy, mean=None, rstd=None, stream=None):
         where = "tk_layer_norm_" + suffix
-        a = _Args(where, rows, cols, dtype, flags)
-        px, ldx = a.matrix(x, ldx, a.residual)
+        a = _Args(where, rows, cols)
+        res, par = residual_type(flags), params_type(flags)
+        px, ldx = a.matrix(x, ldx, res)
         py, ldy = a.matrix(y, ldy, dtype)
-        pg, pb = a.vector(gamma, cols, a.params), a.vector(beta, cols, a.params)
-        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
-        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, a.raw_stream(stream)), where)
+        pg, pb = a.vector(gamma, cols, par), a.vector(beta, cols, par)
+        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
+        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, a.stream(stream)), where)
 
     def layer_norm_backward(rows, cols, flags, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta,
                             workspace=None, stream=None):
         where = "tk_layer_norm_backward_" + suffix
-        a = _Args(where, rows, cols, dtype, flags)
+        a = _Args(where, rows, cols)
+        res, par = residual_type(flags), params_type(flags)
         pdy, lddy = a.matrix(dy, lddy, dtype)
-        px, ldx = a.matrix(x, ldx, a.residual)
-        pdx, lddx = a.matrix(dx, lddx, a.residual)
-        pg, pdg, pdb = (a.vector(v, cols, a.params) for v in (gamma, dgamma, dbeta))
-        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
-        ws, n, keep = a.workspace(workspace, stream, True)
+        px, ldx = a.matrix(x, ldx, res)
+        pdx, lddx = a.matrix(dx, lddx, res)
+        pg, pdg, pdb = (a.vector(v, cols, par) for v in (gamma, dgamma, dbeta))
+        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
+        ws, n, keep = a.workspace(workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None)
         _check(norm_bwd(rows, cols, flags, pdy, lddy, px, ldx, pg, pm, ps, pdx, lddx, pdg, pdb, ws, n,
-                        a.raw_stream(stream)), where)
+                        a.stream(stream)), where)
 
     def dropout_add_layer_norm(key, start_draw, rows, cols, p, eps, flags, x, ldx, bias, residual, ldr, gamma, beta, sum,
                                lds, y, ldy, mean=None, rstd=None, stream=None):
         where = "tk_dropout_add_layer_norm_" + suffix
-        a = _Args(where, rows, cols, dtype, flags)
+        a = _Args(where, rows, cols)
+        res, par = residual_type(flags), params_type(flags)
         px, ldx = a.matrix(x, ldx, dtype)
-        pr, ldr = a.matrix(residual, ldr, a.residual)
-        pv, lds = a.matrix(sum, lds, a.residual)
+        pr, ldr = a.matrix(residual, ldr, res)
+        pv, lds = a.matrix(sum, lds, res)
         py, ldy = a.matrix(y, ldy, dtype)
-        pb, pg, pt = (a.vector(v, cols, a.params) for v in (bias, gamma, beta))
-        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
+        pb, pg, pt = (a.vector(v, cols, par) for v in (bias, gamma, beta))
+        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
         _check(both_fwd(key, start_draw, rows, cols, p, eps, flags, px, ldx, pb, pr, ldr, pg, pt, pv, lds, py, ldy, pm, ps,
-                        a.raw_stream(stream)), where)
+                        a.stream(stream)), where)
 
     def dropout_add_layer_norm_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, gamma, mean,
                                         rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace=None, stream=None):
         where = "tk_dropout_add_layer_norm_backward_" + suffix
-        a = _Args(where, rows, cols, dtype, flags)
+        a = _Args(where, rows, cols)
+        res, par = residual_type(flags), params_type(flags)
         pdy, lddy = a.matrix(dy, lddy, dtype)
-        pds, ldds = a.matrix(dsum, ldds, a.residual)
-        pv, lds = a.matrix(sum, lds, a.residual)
+        pds, ldds = a.matrix(dsum, ldds, res)
+        pv, lds = a.matrix(sum, lds, res)
         pdx, lddx = a.matrix(dx, lddx, dtype)
-        pdr, lddr = a.matrix(dresidual, lddr, a.residual)
-        pg, pdg, pdb, pdt = (a.vector(v, cols, a.params) for v in (gamma, dgamma, dbeta, dbias))
-        pm, ps = a.vector(mean, rows, torch.float32), a.vector(rstd, rows, torch.float32)
-        ws, n, keep = a.workspace(workspace, stream, True)
+        pdr, lddr = a.matrix(dresidual, lddr, res)
+        pg, pdg, pdb, pdt = (a.vector(v, cols, par) for v in (gamma, dgamma, dbeta, dbias))
+        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
+        ws, n, keep = a.workspace(workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None
+                                  or dbias is not None)
         _check(both_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pds, ldds, pv, lds, pg, pm, ps, pdx, lddx, pdr,
-                        lddr, pdg, pdb, pdt, ws, n, a.raw_stream(stream)), where)
+                        lddr, pdg, pdb, pdt, ws, n, a.stream(stream)), where)
 
     out = {}
     for f in (dropout_add, dropout_add_backward, layer_norm, layer_norm_backward, dropout_add_layer_norm,

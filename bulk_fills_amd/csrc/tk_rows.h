@@ -706,26 +706,26 @@ __global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
 // Work-groups over sets of rows; the kernels loop beyond.
 static inline uint32_t row_grid(uint64_t sets, uint32_t most) { return (uint32_t)(sets < most ? sets : most); }
 
-// About 20 waves a compute unit, each set of rows prefetched: layer norm bf16 32768x2048 takes
-// 61, 49, 46, 45, 48 and 55 us with 8, 12, 16, 20, 24 and 32 waves, and 71 us with a work-group
-// for each row and no prefetch; the fused forward 8192x4096 49 to 53 us, and 62.
-constexpr uint32_t kFwdWaves = 20;
-
+// A grid that the device holds at once, each set of rows prefetched: up to 20 waves a compute
+// unit with eight elements a lane (80 registers), 24 where that makes two work-groups of one,
+// and 16 with more elements (128 registers).  Layer norm bf16 32768x2048 takes 61, 49, 46, 45,
+// 48 and 55 us with 8, 12, 16, 20, 24 and 32 waves, and 71 us with a work-group for each row
+// and no prefetch; the fused forward 8192x4096 49 to 53, and 62.
 template <class T, class R, bool kX, bool kOnce, int CH, int kLanes, int V, bool kKeep = true>
 static void launch_fwd(FwdArgs a, hipStream_t s) {
   constexpr uint32_t kCols = kLanes * V * CH;
   a.waves = kLanes < 64 ? 1 : (a.cols + kCols - 1) / kCols;
   const uint32_t waves = a.waves >= 4 ? a.waves : 4 / a.waves * a.waves;  // of a work-group
   const uint32_t rows = kLanes < 64 ? 64 * waves / kLanes : waves / a.waves;
-  const uint32_t most = 256 * (waves < kFwdWaves ? kFwdWaves / waves : 1);
-  hipLaunchKernelGGL((k_norm_fwd<T, R, kX, kOnce, CH, kLanes, V, kKeep>), dim3(row_grid((a.rows + rows - 1) / rows, most)),
-                     dim3(64 * waves), 0, s, a);
+  const uint32_t each = (V * CH > 8 ? 16 : waves > 8 ? 24 : 20) / waves;  // work-groups of a compute unit
+  hipLaunchKernelGGL((k_norm_fwd<T, R, kX, kOnce, CH, kLanes, V, kKeep>),
+                     dim3(row_grid((a.rows + rows - 1) / rows, 256 * (each ? each : 1))), dim3(64 * waves), 0, s, a);
 }
 
-// Lanes to a row by its width, eight elements a lane.  Beyond ten waves a row (5120 columns) a
-// lane takes sixteen, so that several rows share a compute unit (layer norm bf16 8192x8192: 46
-// against 53 us; f16 4095x5001 at ten waves of eight elements 38 against 41), and beyond
-// sixteen waves of those thirty-two, with the parameters read again for every row.
+// Lanes to a row by its width, eight elements a lane.  Beyond twelve waves a row (6144 columns)
+// a lane takes sixteen, so that two rows share a compute unit (layer norm bf16 8192x8192 45.5
+// against 53 us), and beyond sixteen waves of those thirty-two, with the parameters read again
+// for every row (fused forward 1024x32768 59 us, 118 in three passes).
 template <class T, class R, bool kX, bool kOnce>
 static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   constexpr int CH = kChunk<T, R>, K = 8 / CH;
@@ -733,7 +733,7 @@ static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   else if (a.cols <= 64) launch_fwd<T, R, kX, kOnce, CH, 8, K>(a, s);
   else if (a.cols <= 128) launch_fwd<T, R, kX, kOnce, CH, 16, K>(a, s);
   else if (a.cols <= 256) launch_fwd<T, R, kX, kOnce, CH, 32, K>(a, s);
-  else if (a.cols <= 5120) launch_fwd<T, R, kX, kOnce, CH, 64, K>(a, s);
+  else if (a.cols <= 6144) launch_fwd<T, R, kX, kOnce, CH, 64, K>(a, s);
   else if (a.cols <= 16384) launch_fwd<T, R, kX, kOnce, CH, 64, 2 * K>(a, s);
   else if (a.cols <= 32768) launch_fwd<T, R, kX, kOnce, CH, 64, 4 * K, false>(a, s);
   else hipLaunchKernelGGL((k_norm_fwd_wide<T, R, kX>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);

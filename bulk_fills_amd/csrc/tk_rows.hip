@@ -28,7 +28,7 @@ __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
   const float *p = a.partial + (uint64_t)blockIdx.y * a.lines * a.cols + c;
   float s = 0.0f;
   if (c < a.cols) {
-#pragma unroll 8
+#pragma unroll 16
     for (uint64_t l = wave; l < a.lines; l += kWaves) s += p[l * a.cols];
   }
   part[wave][lane] = s;

@@ -193,3 +193,363 @@ def test_dropout_add_layer_norm(kind):
                 if got is not None:
                     ref.check(got, want[name], what + " " + name)
             m.untouched(what)
+
+
+# ---- further properties ----
+
+def run_block(kind, n, cols, m, p=0.1):
+    """Inputs and outputs of one fused forward and backward, for the tests below."""
+    T, R, W = types(kind)
+    g = torch.Generator().manual_seed(m)
+    rnd = lambda *s, k=1.0: torch.randn(*s, generator=g) * k  # noqa: E731
+    d = {"x": rnd(n, cols).to(T), "r": rnd(n, cols, k=2.0).to(R), "bias": rnd(cols).to(W), "gamma": rnd(cols).to(W),
+         "beta": rnd(cols).to(W), "dy": rnd(n, cols).to(T), "dsum": rnd(n, cols).to(R)}
+    d = {k: v.cuda() for k, v in d.items()}
+    for k, (shape, t) in {"sum": ((n, cols), R), "y": ((n, cols), T), "mean": ((n,), torch.float32),
+                          "rstd": ((n,), torch.float32), "dx": ((n, cols), T), "dr": ((n, cols), R), "dg": ((cols,), W),
+                          "db": ((cols,), W), "dbias": ((cols,), W)}.items():
+        d[k] = torch.full(shape, FILL, dtype=t, device="cuda")
+    d["ws"] = torch.empty(max(4, tk.tk_backward_workspace_bytes(n, cols)), dtype=torch.uint8, device="cuda")
+
+    def go(stream=None):
+        fn("dropout_add_layer_norm", kind)(8, 64, n, cols, p, 1e-5, flags(kind), d["x"], None, d["bias"], d["r"], None,
+                                           d["gamma"], d["beta"], d["sum"], None, d["y"], None, d["mean"], d["rstd"],
+                                           stream)
+        fn("dropout_add_layer_norm_backward", kind)(8, 64, n, cols, p, flags(kind), d["dy"], None, d["dsum"], None, d["sum"],
+                                                    None, d["gamma"], d["mean"], d["rstd"], d["dx"], None, d["dr"], None,
+                                                    d["dg"], d["db"], d["dbias"], d["ws"], stream)
+    return d, go
+
+
+OUTS = ("sum", "y", "mean", "rstd", "dx", "dr", "dg", "db", "dbias")
+
+
+def assert_same(a, b, what):
+    for k in OUTS:
+        assert torch.equal(a[k].view(torch.uint8), b[k].view(torch.uint8)), f"{what}: {k}"
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_f32_dropout_add_is_dropout(kind):
+    """Without bias and residual the float operator is tk_dropout_f32, bit for bit; the others
+    keep the same elements."""
+    T, R, _ = types(kind)
+    n, cols = 301, 1003
+    x = torch.randn(n, cols, device="cuda").to(T)
+    x[x == 0] = 1
+    for start, p in ((0, 0.1), (5, 0.5), (64, 0.999), (3, 1.0 - 2.0 ** -24), (0, 2.0 ** -25)):
+        y, want = torch.empty(n, cols, dtype=R, device="cuda"), torch.empty(n, cols, device="cuda")
+        fn("dropout_add", kind)(9, start, n, cols, p, flags(kind), x, None, None, None, None, y, None)
+        tk.tk_dropout_f32(9, start, n * cols, p, x.float(), want)
+        if kind[0] == "f32":
+            assert torch.equal(y.view(torch.int32), want.view(torch.int32))
+        assert torch.equal(y == 0, want == 0), (start, p)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("cols", [5, 100, 1024, 4097, 16384, 33000])
+def test_cut_calls_equal_the_whole(kind, cols):
+    """Rows do not depend on each other: a call cut at any row, with the counters that belong to
+    it, gives the whole call's rows, bit for bit (its column sums add up otherwise)."""
+    T, R, W = types(kind)
+    n, cut = 37, 11
+    log(f"cut {kind} {cols}")
+    whole, go = run_block(kind, n, cols, 3)
+    go()
+    for lo, hi in ((0, cut), (cut, n)):
+        sub, _ = run_block(kind, n, cols, 3)
+        f = {k: v[lo:hi] if v.dim() == 2 or k in ("mean", "rstd") else v for k, v in sub.items() if k != "ws"}
+        fn("dropout_add_layer_norm", kind)(8, 64 + lo * cols, hi - lo, cols, 0.1, 1e-5, flags(kind), f["x"], None, f["bias"],
+                                           f["r"], None, f["gamma"], f["beta"], f["sum"], None, f["y"], None, f["mean"],
+                                           f["rstd"])
+        fn("dropout_add_layer_norm_backward", kind)(8, 64 + lo * cols, hi - lo, cols, 0.1, flags(kind), f["dy"], None,
+                                                    f["dsum"], None, f["sum"], None, f["gamma"], f["mean"], f["rstd"],
+                                                    f["dx"], None, f["dr"], None, f["dg"], f["db"], f["dbias"])
+        for k in ("sum", "y", "mean", "rstd", "dx", "dr"):
+            assert torch.equal(f[k], whole[k][lo:hi]), (k, lo, hi)
+            outside = torch.cat([sub[k][:lo], sub[k][hi:]])
+            assert bool((outside == FILL).all()), f"{k}: rows of the other part were written"
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("cols", [3, 200, 1001, 4096, 9000, 33001])
+def test_in_place(kind, cols):
+    """Outputs in the place of inputs of the same type give the same bits."""
+    T, R, _ = types(kind)
+    n = 19
+    log(f"in place {kind} {cols}")
+    d, go = run_block(kind, n, cols, 4)
+    go()
+    same = T == R
+    for sum_at, y_at in (("r", "x"), ("x" if same else "r", "r" if same else "x")):
+        e, _ = run_block(kind, n, cols, 4)
+        fn("dropout_add_layer_norm", kind)(8, 64, n, cols, 0.1, 1e-5, flags(kind), e["x"], None, e["bias"], e["r"], None,
+                                           e["gamma"], e["beta"], e[sum_at], None, e[y_at], None, e["mean"], e["rstd"])
+        assert torch.equal(e[sum_at], d["sum"]) and torch.equal(e[y_at], d["y"])
+    for dr_at, dx_at in (("dsum", "dy"), ("sum", "dy")):
+        e, _ = run_block(kind, n, cols, 4)
+        for k in ("sum", "mean", "rstd"):
+            e[k].copy_(d[k])
+        fn("dropout_add_layer_norm_backward", kind)(8, 64, n, cols, 0.1, flags(kind), e["dy"], None, e["dsum"], None,
+                                                    e["sum"], None, e["gamma"], e["mean"], e["rstd"], e[dx_at], None,
+                                                    e[dr_at], None, e["dg"], e["db"], e["dbias"])
+        assert torch.equal(e[dr_at], d["dr"]) and torch.equal(e[dx_at], d["dx"]) and torch.equal(e["dg"], d["dg"])
+    y = torch.empty(n, cols, dtype=R, device="cuda")
+    fn("dropout_add", kind)(2, 7, n, cols, 0.3, flags(kind), d["x"], None, d["bias"], d["r"], None, y, None)
+    e, _ = run_block(kind, n, cols, 4)
+    fn("dropout_add", kind)(2, 7, n, cols, 0.3, flags(kind), e["x"], None, e["bias"], e["r"], None, e["r"], None)
+    assert torch.equal(e["r"], y)
+    x2, y2 = torch.empty_like(y), torch.empty(n, cols, dtype=T, device="cuda")
+    x2.copy_(d["r"])
+    fn("layer_norm", kind)(n, cols, 1e-5, flags(kind), x2, None, d["gamma"], d["beta"], y2, None)
+    if same:
+        fn("layer_norm", kind)(n, cols, 1e-5, flags(kind), x2, None, d["gamma"], d["beta"], x2, None)
+        assert torch.equal(x2, y2)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_slices_of_one_buffer(kind):
+    """x and y as column slices of one buffer, read and written side by side."""
+    T, R, W = types(kind)
+    if T != R:
+        pytest.skip("one buffer has one type")
+    n, cols = 23, 1000
+    d, go = run_block(kind, n, cols, 5)
+    packed = torch.full((n, 3 * cols + 7), FILL, dtype=T, device="cuda")
+    packed[:, 2:2 + cols] = d["x"]
+    x, y = packed[:, 2:2 + cols], packed[:, 2 * cols + 5:3 * cols + 5]
+    want = torch.empty(n, cols, dtype=T, device="cuda")
+    fn("dropout_add", kind)(2, 7, n, cols, 0.3, flags(kind), d["x"], None, d["bias"], d["r"], None, want, None)
+    fn("dropout_add", kind)(2, 7, n, cols, 0.3, flags(kind), x, None, d["bias"], d["r"], None, y, None)
+    assert torch.equal(y, want) and torch.equal(x, d["x"])
+    left = torch.cat([packed[:, :2], packed[:, 2 + cols:2 * cols + 5], packed[:, 3 * cols + 5:]], 1)
+    assert bool((left == FILL).all())
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("cols", [64, 3000, 12000])
+def test_special_values(kind, cols):
+    """Constant rows, infinities and NaN follow the formulas; a dropped element is 0 whatever it was."""
+    T, R, W = types(kind)
+    n = 8
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(n, cols, generator=g).to(T)
+    r = torch.randn(n, cols, generator=g).to(R)
+    keep = ref.keep_mask(8, 0, n, cols, 0.5)
+    kept, dropped = [[int(i) for i in (keep[k] == v).nonzero()[:, 0]] for k, v in ((1, 1), (1, 0))]
+    x[0], r[0] = 0, 3.0              # a constant row: y = beta
+    x[1, dropped[0]] = float("nan")  # dropped: no NaN anywhere
+    x[1, dropped[1]] = float("inf")
+    x[2, int((keep[2] == 1).nonzero()[0, 0])] = float("nan")
+    r[3, 5] = float("inf")
+    assert kept
+    gm, bt = torch.randn(cols, generator=g).to(W), torch.randn(cols, generator=g).to(W)
+    s, y = torch.empty(n, cols, dtype=R, device="cuda"), torch.empty(n, cols, dtype=T, device="cuda")
+    mean, rstd = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    fn("dropout_add_layer_norm", kind)(8, 0, n, cols, 0.5, 1e-5, flags(kind), x.cuda(), None, None, r.cuda(), None,
+                                       gm.cuda(), bt.cuda(), s, None, y, None, mean, rstd)
+    v, e = ref.dropout_add(x.double(), None, r.double(), keep, 0.5)
+    want = ref.layer_norm(v, e, gm.double(), bt.double(), 1e-5)
+    for k in (0, 1, 4, 5, 6, 7):
+        ref.check(s[k:k + 1], (v[k:k + 1], e[k:k + 1]), f"sum row {k}")
+        ref.check(y[k:k + 1], (want["y"][0][k:k + 1], want["y"][1][k:k + 1]), f"y row {k}")
+    assert torch.equal(y[0].cpu(), bt.to(T)), "a constant row gives beta"
+    for k in (2, 3):
+        assert bool(torch.isnan(y[k]).all()) and not bool(torch.isfinite(rstd[k]))
+    # eps = 0: tiny variances keep their reciprocal root; a constant row has none
+    x = (torch.randn(2, cols, generator=g, dtype=torch.float64) * 2.0 ** -55).float()
+    x[1] = 1.0
+    xr, yr = x.to(R), torch.empty(2, cols, dtype=T, device="cuda")
+    fn("layer_norm", kind)(2, cols, 0.0, flags(kind), xr.cuda(), None, None, None, yr, None)
+    if R != torch.float16:  # 2^-55 is no f16
+        z = xr.double()[:1]
+        w = ref.layer_norm(z, torch.zeros_like(z), None, None, 0.0)
+        ref.check(yr[:1], w["y"], "tiny variance")
+    assert bool(torch.isnan(yr[1]).all())
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_no_rows(kind):
+    """Over no rows the forward calls write nothing and the gradients are zeros."""
+    T, R, W = types(kind)
+    cols = 100
+    e = lambda t: torch.empty(0, cols, dtype=t, device="cuda")  # noqa: E731
+    st = torch.empty(0, device="cuda")
+    g, b, c = (torch.full((cols,), FILL, dtype=W, device="cuda") for _ in range(3))
+    fn("layer_norm", kind)(0, cols, 1e-5, flags(kind), e(R), None, None, None, e(T), None)
+    fn("dropout_add_layer_norm_backward", kind)(1, 0, 0, cols, 0.1, flags(kind), e(T), None, None, None, e(R), None, None, st,
+                                                st, e(T), None, e(R), None, g, b, c)
+    assert not g.any() and not b.any() and not c.any()
+    c.fill_(FILL)
+    fn("dropout_add_backward", kind)(1, 0, 0, cols, 0.1, flags(kind), e(R), None, e(T), None, c)
+    assert not c.any()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("shape", [(300, 768), (40, 9000)])
+def test_captured_calls_replay_to_the_eager_result(kind, shape):
+    """Forward and backward captured into two graphs with a workspace each; replayed in turn with
+    eager work between, new inputs in place, and the outputs cleared."""
+    want, go = run_block(kind, *shape, 6)
+    go()
+    want = {k: v.clone() for k, v in want.items()}
+    other, go_other = run_block(kind, *shape, 7)
+    go_other()
+    want2 = {k: v.clone() for k, v in other.items()}
+    runs = [run_block(kind, *shape, s) for s in (6, 7)]
+    graphs = []
+    for d, go in runs:
+        go()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            go()
+        graphs.append(g)
+    for r in range(4):
+        for (d, _), w in zip(runs, (want, want2)):
+            for k in OUTS:
+                d[k].fill_(FILL)
+        log(f"graph {kind} {shape} replay {r}")
+        for g in graphs:
+            g.replay()
+        go_other()  # eager calls beside them
+        torch.cuda.synchronize()
+        assert_same(runs[0][0], want, f"replay {r}")
+        assert_same(runs[1][0], want2, f"replay {r}, second graph")
+        for k in ("x", "r", "dy"):  # the second graph's inputs into the first
+            runs[0][0][k].copy_(want[k] if r % 2 else want[k].clone())
+    del graphs
+
+
+def test_captured_calls_with_an_allocated_workspace():
+    """A workspace of None inside a capture comes from the graph's own pool."""
+    d, go = run_block(KINDS[3], 200, 1024, 8)
+    go()
+    want = {k: v.clone() for k, v in d.items()}
+    back = tk.tk_dropout_add_layer_norm_backward_bf16
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        back(8, 64, 200, 1024, 0.1, 0, d["dy"], None, d["dsum"], None, d["sum"], None, d["gamma"], d["mean"], d["rstd"],
+             d["dx"], None, d["dr"], None, d["dg"], d["db"], d["dbias"])
+    for r in range(3):
+        for k in ("dx", "dr", "dg", "db", "dbias"):
+            d[k].fill_(FILL)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(4)]  # would land in a freed workspace
+        g.replay()
+        torch.cuda.synchronize()
+        assert_same(d, want, f"replay {r}")
+        del junk
+
+
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[4]], ids=["f32", "bf16-r32"])
+def test_two_streams(kind):
+    """Two calls at once on two streams, each with its own workspace, and the same call again."""
+    a, go_a = run_block(kind, 2000, 1000, 9)
+    b, go_b = run_block(kind, 700, 9001, 10)
+    go_a()
+    go_b()
+    torch.cuda.synchronize()
+    want = [{k: v.clone() for k, v in d.items()} for d in (a, b)]
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for r in range(3):
+        for d in (a, b):
+            for k in OUTS:
+                d[k].fill_(FILL)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            go_a(s)
+            go_b(t)
+        torch.cuda.synchronize()
+        assert_same(a, want[0], f"stream a, round {r}")
+        assert_same(b, want[1], f"stream b, round {r}")
+
+
+def test_binding_checks_on_the_device():
+    """What the binding refuses of device tensors, before any launch."""
+    x, y = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 8, device="cuda")
+    call = tk.tk_layer_norm_f32
+    with pytest.raises(ValueError, match="matrix"):
+        call(4, 9, 1e-5, 0, x, None, None, None, y, None)
+    with pytest.raises(ValueError, match="matrix"):
+        call(4, 8, 1e-5, 0, x.t().contiguous().t(), None, None, None, y, None)
+    with pytest.raises(ValueError, match="matrix"):
+        call(4, 8, 1e-5, 0, torch.zeros(1, 8, device="cuda").expand(4, 8), None, None, None, y, None)
+    with pytest.raises(ValueError, match="matrix"):
+        call(4, 8, 1e-5, 0, x, 16, None, None, y, None)
+    with pytest.raises(ValueError, match="vector"):
+        call(4, 8, 1e-5, 0, x, None, torch.zeros(7, device="cuda"), None, y, None)
+    with pytest.raises(ValueError, match="type"):
+        tk.tk_layer_norm_bf16(4, 8, 1e-5, tk.TK_RESIDUAL_F32, x, None, None, None, y, None)
+    with pytest.raises(tk.TkError):
+        call(4, 8, -1.0, 0, x, None, None, None, y, None)
+    mu = torch.zeros(4, device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, torch.zeros(8, device="cuda"), None,
+                                      None, torch.cuda.Stream())
+    # a call that needs none takes none
+    tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, None, None, None, torch.cuda.Stream())
+    torch.cuda.synchronize()
+    call(4, 8, 1e-5, 0, x.view(2, 2, 8), None, None, None, y, 8)  # any shape that flattens
+    call(1, 8, 1e-5, 0, x[1:2], 100, None, None, y[:1], None)     # one row has no distance to a next
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_a_blocks_run(kind):
+    """A transformer block's run of them, pre-norm: norm, a product, dropout-add with the next
+    norm fused, a product, dropout-add; and back.  Against float64 autograd of the same block,
+    on the values that the operators exchange in their own types."""
+    T, R, W = types(kind)
+    n, cols, p = 61, 520, 0.2
+    g = torch.Generator().manual_seed(2)
+    rnd = lambda *s, k=1.0: torch.randn(*s, generator=g) * k  # noqa: E731
+    x0 = rnd(n, cols, k=1.5).to(R)
+    w1, w2 = (rnd(cols, cols, k=cols ** -0.5).to(T) for _ in range(2))
+    prm = {k: (rnd(cols, k=0.3) + (1 if k[0] == "g" else 0)).to(W) for k in ("g1", "b1", "bias1", "g2", "b2", "bias2")}
+    dout = rnd(n, cols).to(R)
+    cu = {k: v.cuda() for k, v in prm.items()}
+    fl, e = flags(kind), lambda t: torch.empty(n, cols, dtype=t, device="cuda")  # noqa: E731
+    st = lambda: torch.empty(n, device="cuda")  # noqa: E731
+    mm = lambda a, b: (a.float() @ b.float().cuda()).to(T)  # noqa: E731
+    # forward
+    x = x0.cuda()
+    h1, m1, r1 = e(T), st(), st()
+    fn("layer_norm", kind)(n, cols, 1e-5, fl, x, None, cu["g1"], cu["b1"], h1, None, m1, r1)
+    a1 = mm(h1, w1)
+    s, h2, m2, r2 = e(R), e(T), st(), st()
+    fn("dropout_add_layer_norm", kind)(11, 0, n, cols, p, 1e-5, fl, a1, None, cu["bias1"], x, None, cu["g2"], cu["b2"], s,
+                                       None, h2, None, m2, r2)
+    a2 = mm(h2, w2)
+    out = e(R)
+    fn("dropout_add", kind)(12, 0, n, cols, p, fl, a2, None, cu["bias2"], s, None, out, None)
+    # backward
+    da2, gb2 = e(T), torch.empty(cols, dtype=W, device="cuda")
+    fn("dropout_add_backward", kind)(12, 0, n, cols, p, fl, dout.cuda(), None, da2, None, gb2)
+    dh2 = mm(da2, w2.t().contiguous())
+    da1, dx = e(T), e(R)
+    gg2, gt2, gb1 = (torch.empty(cols, dtype=W, device="cuda") for _ in range(3))
+    fn("dropout_add_layer_norm_backward", kind)(11, 0, n, cols, p, fl, dh2, None, dout.cuda(), None, s, None, cu["g2"], m2,
+                                                r2, da1, None, dx, None, gg2, gt2, gb1)
+    dh1 = mm(da1, w1.t().contiguous())
+    dx1 = e(R)
+    gg1, gt1 = (torch.empty(cols, dtype=W, device="cuda") for _ in range(2))
+    fn("layer_norm_backward", kind)(n, cols, fl, dh1, None, x, None, cu["g1"], m1, r1, dx1, None, gg1, gt1)
+    got = {"x": (dx.double() + dx1.double()).cpu(), "g1": gg1, "b1": gt1, "bias1": gb1, "g2": gg2, "b2": gt2, "bias2": gb2}
+
+    def block(x, g1, b1, bias1, g2, b2, bias2):
+        ln = lambda v, a, b: torch.nn.functional.layer_norm(v, (cols,), a, b, 1e-5)  # noqa: E731
+        k1, k2 = (ref.keep_mask(k, 0, n, cols, p) / ref.quotient(p) for k in (11, 12))
+        v = x + k1 * (ln(x, g1, b1) @ w1.double() + bias1)
+        return v + k2 * (ln(v, g2, b2) @ w2.double() + bias2)
+
+    leaves = {k: v.double().requires_grad_() for k, v in {"x": x0, **prm}.items()}
+    want = block(**leaves)
+    want.backward(dout.double())
+    # every value passes at most eight roundings to T or R between the inputs and a gradient, each
+    # off by up to half a step, relative to values of the same size: 16 half steps of the coarsest
+    # type, and twice that because a gradient is itself a difference of terms of its size
+    half = torch.finfo(T).eps / 2
+    rel = lambda a, b: float((a.detach().cpu().double() - b).norm() / b.norm())  # noqa: E731
+    assert rel(out, want.detach()) <= 32 * half + 1e-5
+    for k, v in got.items():
+        assert rel(v, leaves[k].grad) <= 32 * half + 1e-5, k
