@@ -51,9 +51,9 @@ struct AddArgs {
   Drop drop;
 };
 
-// How a backward call is cut: `lines` lines of partial sums.  Rows in registers: `lanes` lanes
-// to a row (64: row_waves whole waves), `waves` waves to a work-group.
-// Wide rows (lanes 0) and dropout-add: strips of columns.
+// How a backward call is cut: `lines` lines of partial sums.  Rows in registers (strips 0):
+// `lanes` lanes to a row (64: row_waves whole waves), `waves` waves to a work-group.  Wide rows
+// and dropout-add: `strips` strips of `lanes` lanes' columns.
 struct BwdPlan {
   int lanes, waves, row_waves;
   uint64_t lines, strips, rows_per_block;
