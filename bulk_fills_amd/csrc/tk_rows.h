@@ -592,11 +592,15 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
   }
 }
 
-// A strip of kLanes lanes' chunks by a range of rows, 64 / kLanes rows to each of sixteen waves
-// at a time, the next ones prefetched: each lane keeps the sums of its own columns.  kNorm:
-// layer norm's gradient with the rows' numbers from k_row_stats; else dy (of the residual
-// stream's type) is the sum's gradient itself.  Sixteen waves to a work-group keep the lines of
-// partial sums few: dropout-add's backward bf16 32768x512 takes 14.7 us, with four waves and
+// A strip of kLanes lanes' chunks, 64 / kLanes rows to each of sixteen waves at a time, the next
+// ones prefetched: each lane keeps the sums of its own columns.  kNorm: layer norm's gradient
+// with the rows' numbers from k_row_stats; else dy (of the residual stream's type) is the sum's
+// gradient itself.
+//
+// The work-groups of a strip take every gridDim.y-th set of rows, so that all of them together
+// are within some MB at any time (ranges of rows, with powers of two between them, took 26 to 39
+// us for dropout-add's backward bf16 8192x4096, by where the buffers lay).  Sixteen waves to a
+// work-group keep the lines of partial sums few: 32768x512 takes 14.7 us, with four waves and
 // 2048 lines 20.5; 65536x64, eight rows to a wave, 7.4 us, with one row to a wave 24.
 template <class T, class R, bool kNorm, bool kX, bool kBias, bool kOnce, int CH, int kLanes>
 __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
@@ -605,8 +609,7 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
   const uint32_t lane = threadIdx.x & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t c = (blockIdx.x * kLanes + lane % kLanes) * CH;
   const int nv = (int)(a.cols - c);
-  const uint64_t r0 = (uint64_t)blockIdx.y * a.rows_per_block;
-  const uint64_t r1 = r0 + a.rows_per_block < a.rows ? r0 + a.rows_per_block : a.rows;
+  const uint64_t step = (uint64_t)gridDim.y * (16 * kGroups);
   float acc[kSums ? kSums : 1][CH];
 #pragma unroll
   for (int k = 0; k < kSums; ++k)
@@ -616,11 +619,11 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
     float w[CH];
     if (kNorm) load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, w);
     BwdIn<T, R, D, kNorm, kOnce, CH> next;
-    uint64_t row = r0 + wave * kGroups + (kGroups > 1 ? lane / kLanes : 0);
-    if (row < r1) next.load(a, row, c);
-    for (; row < r1; row += 16 * kGroups) {
+    uint64_t row = ((uint64_t)blockIdx.y * 16 + wave) * kGroups + (kGroups > 1 ? lane / kLanes : 0);
+    if (row < a.rows) next.load(a, row, c);
+    for (; row < a.rows; row += step) {
       const BwdIn<T, R, D, kNorm, kOnce, CH> in = next;
-      if (row + 16 * kGroups < r1) next.load(a, row + 16 * kGroups, c);
+      if (row + step < a.rows) next.load(a, row + step, c);
       float v[CH];
       unpack<CH, D>(in.dy, nv, v);
       if constexpr (kNorm) {

@@ -50,7 +50,7 @@ constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 31;
 constexpr uint64_t kRowsInRegisters = 8192;      // columns that k_norm_bwd holds
 constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through the caches (tk_rows.h)
 
-// Strips of columns by ranges of rows: one work-group of 16 waves a compute unit, or fewer that
+// Strips of columns by sets of rows: one work-group of 16 waves a compute unit, or fewer that
 // have one row for each of their groups of lanes.  Dropout-add's backward bf16 8192x4096 takes
 // 25.9, 26.8, 28.3 and 28.8 us with 256, 512, 768 and 1024 work-groups, the fused backward
 // 512x24576 31.8, 33.0, 35.2 and 38.2.
@@ -60,10 +60,8 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
   p.lanes = cols <= 8ull * ch ? 8 : cols <= 16ull * ch ? 16 : cols <= 32ull * ch ? 32 : 64;
   p.strips = (cols + p.lanes * ch - 1) / (p.lanes * ch);
   const uint64_t at_once = 16 * 64 / p.lanes, most = (rows + at_once - 1) / at_once;
-  uint64_t lines = p.strips < 256 ? 256 / p.strips : 1;
-  if (lines > most) lines = most;
-  p.rows_per_block = (rows + lines - 1) / lines;
-  p.lines = (rows + p.rows_per_block - 1) / p.rows_per_block;
+  p.lines = p.strips < 256 ? 256 / p.strips : 1;
+  if (p.lines > most) p.lines = most;
   return p;
 }
 
@@ -309,7 +307,7 @@ static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, u
   const BwdPlan plan = strips_plan(k.chunk, rows, cols);
   BwdArgs a{};
   a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
-  a.rows = rows; a.cols = (uint32_t)cols; a.rows_per_block = plan.rows_per_block;
+  a.rows = rows; a.cols = (uint32_t)cols;
   a.partial = (float *)workspace;
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
@@ -389,7 +387,7 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   a.dy = dy; a.lddy = lddy; a.dsum = dsum; a.ldds = ldds; a.sum = sum; a.lds = lds;
   a.gamma = gamma; a.mean = mean; a.rstd = rstd;
   a.dx = dx; a.lddx = lddx; a.dresidual = dresidual; a.lddr = lddr;
-  a.rows = rows; a.cols = (uint32_t)cols; a.rows_per_block = plan.rows_per_block; a.waves = (uint32_t)plan.row_waves;
+  a.rows = rows; a.cols = (uint32_t)cols; a.waves = (uint32_t)plan.row_waves;
   a.partial = sums ? (float *)workspace : nullptr;
   a.stats = !plan.strips ? nullptr : (float *)((char *)workspace + need - 8 * rows);
   a.params_f32 = params_f32(t, flags);

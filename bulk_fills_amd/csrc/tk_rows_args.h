@@ -35,7 +35,7 @@ struct BwdArgs {
   void *dx, *dresidual;
   float *partial;  // lines of partial column sums: dgamma's, dbeta's, then dbias's; null: no sums wanted
   float *stats;    // mean(g), mean(g h) of every row (wide rows)
-  uint64_t rows, lddy, ldds, lds, lddx, lddr, rows_per_block;
+  uint64_t rows, lddy, ldds, lds, lddx, lddr;
   uint32_t cols, waves;
   bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
@@ -56,7 +56,7 @@ struct AddArgs {
 // and dropout-add: `strips` strips of `lanes` lanes' columns.
 struct BwdPlan {
   int lanes, waves, row_waves;
-  uint64_t lines, strips, rows_per_block;
+  uint64_t lines, strips;
 };
 
 struct RowTable {
