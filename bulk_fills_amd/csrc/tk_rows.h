@@ -675,50 +675,38 @@ __device__ __forceinline__ uint32_t row_of(const AddArgs &a, uint32_t n) {
   return a.div_shift < 0 ? n : __umulhi(n, a.div_mul) >> a.div_shift;
 }
 
-template <class TI, class TO, bool kOnce, int CH>
-struct AddChunk {
-  uint64_t row0, c;
-  uint32_t dr;
-  Chunk<TI, CH> x;
-  Chunk<TO, CH> d;
-  __device__ __forceinline__ uint64_t at(uint64_t ld, uint64_t column) const {
-    return row0 * ld + ((uint64_t)dr * (uint32_t)ld + column);
-  }
-  __device__ __forceinline__ void load(const AddArgs &a, uint32_t first) {
-    const uint32_t r0 = row_of(a, first), n = first - r0 * a.chunks_per_row + threadIdx.x;  // from that row's start
-    row0 = a.row0 + r0;
-    dr = row_of(a, n);
-    c = (uint64_t)(n - dr * a.chunks_per_row) * CH;
-    if (first + threadIdx.x >= a.chunks) return;
-    const uint64_t from = chunk_at<CH>(c, a.cols64);
-    x = load_chunk<kOnce, CH>((const TI *)a.x + at(a.ldx, from));
-    if (a.residual) d = load_chunk<kOnce, CH>((const TO *)a.residual + at(a.ldr, from));
-  }
-};
-
-template <class TI, class TO, bool kDivide, bool kOnce, int CH, class TP>
+template <class TI, class TO, bool kDivide, bool kOnce, bool kFlat, int CH, class TP>
 __global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
   const uint32_t first = blockIdx.x * 256u;
-  AddChunk<TI, TO, kOnce, CH> p;
-  p.load(a, first);
+  uint32_t dr = 0, column = 0;  // rows from the work-group's first, chunks from the row's start
+  uint64_t row0 = 0;
+  if (!kFlat || a.bias) {
+    const uint32_t r0 = row_of(a, first), n = first - r0 * a.chunks_per_row + threadIdx.x;  // from that row's start
+    dr = row_of(a, n);
+    column = n - dr * a.chunks_per_row;
+    row0 = a.row0 + r0;
+  }
   if (first + threadIdx.x >= a.chunks) return;
-  const int nv = a.cols64 - p.c < CH ? (int)(a.cols64 - p.c) : CH;
-  float v[CH];
-  unpack<CH, TI>(p.x, nv, v);
-  if (a.bias) {
-    float b[CH];
-    load_param<CH, TP>(a.bias, a.params_f32, (uint32_t)p.c, (uint32_t)a.cols64, 0.0f, b);
+  const uint64_t c = (uint64_t)(kFlat ? first + threadIdx.x : column) * CH, from = chunk_at<CH>(c, a.cols64);
+  const auto at = [&](uint64_t ld, uint64_t k) { return kFlat ? k : row0 * ld + ((uint64_t)dr * (uint32_t)ld + k); };
+  const Chunk<TI, CH> x = load_chunk<kOnce, CH>((const TI *)a.x + at(a.ldx, from));
+  Chunk<TO, CH> d;
+  if (a.residual) d = load_chunk<kOnce, CH>((const TO *)a.residual + at(a.ldr, from));
+  const int nv = a.cols64 - c < CH ? (int)(a.cols64 - c) : CH;
+  float v[CH], b[CH];
+  if (a.bias) load_param<CH, TP>(a.bias, a.params_f32, column * CH, (uint32_t)a.bias_cols, 0.0f, b);
+  unpack<CH, TI>(x, nv, v);
+  if (a.bias)
 #pragma unroll
     for (int e = 0; e < CH; ++e) v[e] += b[e];
-  }
-  if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)p.at(a.cols64, p.c), v);
+  if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)at(a.cols64, c), v);
   if (a.residual) {
     float t[CH];
-    unpack<CH, TO>(p.d, nv, t);
+    unpack<CH, TO>(d, nv, t);
 #pragma unroll
     for (int e = 0; e < CH; ++e) v[e] += t[e];
   }
-  store_chunk<CH>((TO *)a.y + p.at(a.ldy, p.c), nv, v);
+  store_chunk<CH>((TO *)a.y + at(a.ldy, c), nv, v);
 }
 
 // ---- launches --------------------------------------------------------------------------
@@ -807,8 +795,9 @@ static void norm_bwd_of(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
 template <class TI, class TO, bool kDivide, class TP, bool kOnce>
 static void drop_add_as(const AddArgs &a, int chunk, hipStream_t s) {
   const dim3 g((a.chunks + 255) / 256);
-  if (chunk == 1) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, 1, TP>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
+  if (chunk == 1) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, false, 1, TP>), g, dim3(256), 0, s, a);
+  else if (a.flat) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, true, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, false, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
 }
 
 template <class TI, class TO, class TP>

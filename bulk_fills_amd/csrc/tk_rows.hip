@@ -211,26 +211,34 @@ static bool serves(const void *workspace, uint64_t have, uint64_t need) {
 // ---------------------------------------------------------------------------------------
 // Dropout-add
 // ---------------------------------------------------------------------------------------
-// The element-wise launches.  A contiguous call without a bias is one long row; a call of 2^31
-// chunks or more is cut.
+// The element-wise launches.  A contiguous call is one long row (with a bias, if its rows are
+// whole chunks).  A call of more than 2^30 chunks is cut.
 static tk_status run_add(void (*launch)(const AddArgs &, int, hipStream_t), int chunk, AddArgs a, uint64_t rows, uint64_t cols,
                          int in_size, int out_size, hipStream_t stream) {
-  const bool flat = !a.bias && (rows == 1 || (a.ldx == cols && a.ldy == cols && (!a.residual || a.ldr == cols)));
-  if ((flat ? rows * cols : cols) < (uint64_t)chunk) chunk = 1;  // no row holds a whole chunk
-  const uint64_t most = 1ull << 30;  // chunks of a launch
-  if (flat) {
-    const uint64_t n = rows * cols, piece = most * chunk;
+  const bool dense = rows == 1 || (a.ldx == cols && a.ldy == cols && (!a.residual || a.ldr == cols));
+  a.flat = dense && rows * cols >= (uint64_t)chunk && (!a.bias || cols % chunk == 0);
+  if (!a.flat && cols < (uint64_t)chunk) chunk = 1;  // no row holds a whole chunk
+  const uint64_t per_row = (cols + chunk - 1) / chunk, most = 1ull << 30;  // chunks
+  a.bias_cols = cols;
+  // n / d for n < 2^31: n ceil(2^(31 + l) / d) >> (31 + l), l = ceil(log2 d)
+  if (!a.flat || a.bias) {
+    int l = 0;
+    while ((1ull << l) < per_row) ++l;
+    a.chunks_per_row = (uint32_t)per_row;
+    a.div_shift = l - 1;
+    a.div_mul = (uint32_t)(((1ull << (31 + l)) + per_row - 1) / per_row);
+  }
+  if (a.flat) {
+    // pieces of whole rows where there is a bias, and none shorter than a chunk
+    const uint64_t n = rows * cols, piece = a.bias ? most / per_row * cols : most * chunk;
     for (uint64_t k = 0, m; k < n; k += m) {
       AddArgs b = a;
-      m = n - k < piece + chunk ? n - k : piece;  // no piece is shorter than a chunk
+      m = n - k < piece + chunk ? n - k : piece;
       b.x = (const char *)a.x + k * in_size;
       if (a.residual) b.residual = (const char *)a.residual + k * out_size;
       b.y = (char *)a.y + k * out_size;
       b.drop.start = a.drop.start + (uint32_t)k;
       b.chunks = (uint32_t)((m + chunk - 1) / chunk);
-      b.chunks_per_row = b.chunks;
-      b.div_mul = 0;  // every chunk is in row 0
-      b.div_shift = 0;
       b.cols64 = m;
       launch(b, chunk, stream);
       const tk_status st = launch_status();
@@ -238,15 +246,8 @@ static tk_status run_add(void (*launch)(const AddArgs &, int, hipStream_t), int 
     }
     return TK_OK;
   }
-  const uint64_t per_row = (cols + chunk - 1) / chunk;
-  const uint64_t rows_each = most / per_row ? most / per_row : 1;
-  a.chunks_per_row = (uint32_t)per_row;
+  const uint64_t rows_each = most / per_row;
   a.cols64 = cols;
-  // n / d for n < 2^31: n ceil(2^(31 + l) / d) >> (31 + l), l = ceil(log2 d)
-  int l = 0;
-  while ((1ull << l) < per_row) ++l;
-  a.div_shift = l - 1;
-  a.div_mul = (uint32_t)(((1ull << (31 + l)) + per_row - 1) / per_row);
   for (uint64_t r = 0; r < rows; r += rows_each) {
     AddArgs b = a;
     b.row0 = r;

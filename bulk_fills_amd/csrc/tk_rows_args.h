@@ -44,9 +44,10 @@ struct BwdArgs {
 struct AddArgs {
   const void *x, *bias, *residual;
   void *y;
-  uint64_t row0, ldx, ldr, ldy, cols64;
+  uint64_t row0, ldx, ldr, ldy, cols64, bias_cols;
   uint32_t chunks, chunks_per_row, div_mul;
   int div_shift;
+  bool flat;  // the call's matrices are one row of cols64 elements; a bias repeats in it
   bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
 };
