@@ -248,88 +248,95 @@ def tk_backward_workspace_bytes(rows, cols):
 
 
 # The current device and its current stream's handle, as torch.cuda.current_device() and
-# torch.cuda.current_stream() give them, without making a Stream object for every call: for one
-# row of 4096 columns half of the call's time on the host.
-_device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None)
+# torch.cuda.current_stream() give them, without making a Stream object for every call (1.1 of the
+# 8.7 us that one row's layer norm took on the host); by those where torch lacks the names.
+_get_device = getattr(getattr(torch, "_C", None), "_cuda_getDevice", None)
 _raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
-if _device is None or _raw_stream is None:  # a torch without a GPU build, or another version's names
-    def _device():
-        return torch.cuda.current_device()
+_device_ready = False
 
-    def _raw_stream(device):
-        return torch.cuda.current_stream(device).cuda_stream
+
+def _device():
+    """The current device's index, or -2 (no tensor's) where there is no device."""
+    global _device_ready
+    if not _device_ready:
+        if not torch.cuda.is_available():
+            return -2
+        torch.cuda.init()
+        _device_ready = True
+    return _get_device()
+
+
+if _get_device is None or _raw_stream is None:
+    def _device():
+        return torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+    def _raw_stream(dev):
+        return torch.cuda.current_stream(dev).cuda_stream
 
 
 _SUMS_ALONE = 8192  # columns up to which a backward call needs its workspace for column sums alone
 
 
-class _Args:
-    """Checks and marshals one row operator's buffers.  A matrix is a tensor of rows x cols (any
-    shape that flattens to it, the last dimension contiguous), whose row distance is taken where
-    the call gives None for its ld; or a raw address (ld None: cols)."""
+def _refuse(where, x, dtype, dev, need):
+    """Raises what is wrong with a buffer of a row operator."""
+    if x.dtype is not dtype:
+        raise ValueError(f"{where}: a buffer's type is {x.dtype}, not {dtype}")
+    if x.get_device() < 0:
+        raise ValueError(f"{where}: buffer must live on a HIP device")
+    if x.get_device() != dev:  # the library launches on the calling thread's current device
+        raise ValueError(f"{where}: buffer is on {x.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{where}: need {need}, got shape {tuple(x.shape)}, strides {x.stride()}")
 
-    __slots__ = ("where", "rows", "cols", "device")
 
-    def __init__(self, where, rows, cols):
-        self.where, self.rows, self.cols = where, rows, cols
-        self.device = -1
-
-    def _address(self, x, dtype):
-        if x.dtype is not dtype:
-            raise ValueError(f"{self.where}: a buffer's type is {x.dtype}, not {dtype}")
-        index = x.get_device()  # -1 on the host
-        if index != self.device or index < 0:
-            if index < 0:
-                raise ValueError(f"{self.where}: buffer must live on a HIP device")
-            if index != _device():
-                # the library launches on the calling thread's current device
-                raise ValueError(f"{self.where}: buffer is on {x.device}, the current device is cuda:{_device()}")
-            self.device = index
-        return x.data_ptr()
-
-    def matrix(self, x, ld, dtype):
-        """(address, ld) of a matrix argument."""
-        if x is None:
-            return None, 0
-        cols = self.cols
-        if isinstance(x, int):
-            return x, cols if ld is None else ld
+def _matrix(where, dev, x, ld, rows, cols, dtype):
+    """(address, ld) of a row operator's matrix: a tensor of rows x cols on the current device
+    `dev` (any shape that flattens to it, or two dimensions with the last contiguous), whose row
+    distance is taken where the call gives None for its ld; or a raw address (ld None: cols)."""
+    if x is None:
+        return None, 0
+    if isinstance(x, int):
+        return x, cols if ld is None else ld
+    if x.dtype is dtype and x.get_device() == dev:
         if x.is_contiguous():
-            if x.numel() == self.rows * cols and (ld is None or ld == cols or self.rows <= 1):
-                return self._address(x, dtype), cols if ld is None else ld
-        elif tuple(x.shape) == (self.rows, cols) and (cols == 1 or x.stride(1) == 1):
-            own = cols if self.rows <= 1 else x.stride(0)  # one row has no distance to a next
-            if own >= cols and (ld is None or ld == own or self.rows <= 1):
-                return self._address(x, dtype), own if ld is None else ld
-        raise ValueError(f"{self.where}: need a {self.rows} x {cols} matrix with contiguous rows that do not overlap (and "
-                         f"its own row distance as ld, or None), got shape {tuple(x.shape)}, strides {x.stride()}, ld {ld}")
+            if x.numel() == rows * cols and (ld is None or ld == cols or rows <= 1):
+                return x.data_ptr(), cols if ld is None else ld
+        elif tuple(x.shape) == (rows, cols) and (cols == 1 or x.stride(1) == 1):
+            own = cols if rows <= 1 else x.stride(0)  # one row has no distance to a next
+            if own >= cols and (ld is None or ld == own or rows <= 1):
+                return x.data_ptr(), own if ld is None else ld
+    _refuse(where, x, dtype, dev, f"a {rows} x {cols} matrix with contiguous rows that do not overlap (and its own row "
+                                  f"distance as ld, or None; here {ld})")
 
-    def vector(self, x, n, dtype):
-        if x is None or isinstance(x, int):
-            return x
-        if x.numel() != n or not x.is_contiguous():
-            raise ValueError(f"{self.where}: need a contiguous vector of {n} elements, got shape {tuple(x.shape)}")
-        return self._address(x, dtype)
 
-    def stream(self, stream):
-        if stream is None:
-            return _raw_stream(self.device if self.device >= 0 else _device())
-        return stream if isinstance(stream, int) else stream.cuda_stream
+def _vector(where, dev, x, n, dtype):
+    """Address of a contiguous vector of n elements on the current device."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype is dtype and x.get_device() == dev and x.numel() == n and x.is_contiguous():
+        return x.data_ptr()
+    _refuse(where, x, dtype, dev, f"a contiguous vector of {n} elements")
 
-    def workspace(self, x, stream, needed):
-        """(address, bytes, what keeps it alive).  None allocates it with torch, in the order of
-        the current stream: for a call on another stream the caller passes one."""
-        if x is None:
-            n = tk_backward_workspace_bytes(self.rows, self.cols) if needed else 0
-            if n == 0:
-                return None, 0, None
-            if stream is not None and self.stream(stream) != self.stream(None):
-                raise ValueError(f"{self.where}: a call on a stream that is not the current one needs a workspace")
-            x = torch.empty(n, dtype=torch.uint8, device="cuda")
-            return x.data_ptr(), n, x
-        if not x.is_contiguous():
-            raise ValueError(f"{self.where}: the workspace must be contiguous")
-        return self._address(x, x.dtype), x.numel() * x.element_size(), x
+
+def _on(stream, dev):
+    if stream is None:
+        return _raw_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _workspace(where, dev, x, stream, rows, cols, needed):
+    """(address, bytes, what keeps it alive).  None allocates it with torch, in the order of the
+    current stream: for a call on another stream the caller passes one."""
+    if x is None:
+        n = tk_backward_workspace_bytes(rows, cols) if needed else 0
+        if n == 0:
+            return None, 0, None
+        if stream is not None and _on(stream, dev) != _raw_stream(dev):
+            raise ValueError(f"{where}: a call on a stream that is not the current one needs a workspace")
+        x = torch.empty(n, dtype=torch.uint8, device="cuda")
+        return x.data_ptr(), n, x
+    if x.get_device() != dev or not x.is_contiguous():
+        _refuse(where, x, x.dtype, dev, "a contiguous workspace")
+    return x.data_ptr(), x.numel() * x.element_size(), x
 
 
 def _row_operators(suffix, dtype):
@@ -338,89 +345,81 @@ def _row_operators(suffix, dtype):
     norm_fwd, norm_bwd = getattr(lib, "tk_layer_norm_" + suffix), getattr(lib, "tk_layer_norm_backward_" + suffix)
     both_fwd = getattr(lib, "tk_dropout_add_layer_norm_" + suffix)
     both_bwd = getattr(lib, "tk_dropout_add_layer_norm_backward_" + suffix)
-
     float32 = torch.float32
-
-    def residual_type(flags):
-        return float32 if flags & TK_RESIDUAL_F32 else dtype
-
-    def params_type(flags):
-        return float32 if flags & TK_PARAMS_F32 else dtype
+    name_dropout_add, name_dropout_add_backward = "tk_dropout_add_" + suffix, "tk_dropout_add_backward_" + suffix
+    name_layer_norm, name_layer_norm_backward = "tk_layer_norm_" + suffix, "tk_layer_norm_backward_" + suffix
+    name_dropout_add_layer_norm = "tk_dropout_add_layer_norm_" + suffix
+    name_dropout_add_layer_norm_backward = "tk_dropout_add_layer_norm_backward_" + suffix
 
     def dropout_add(key, start_draw, rows, cols, p, flags, x, ldx, bias, residual, ldr, y, ldy, stream=None):
-        where = "tk_dropout_add_" + suffix
-        a = _Args(where, rows, cols)
-        res, par = residual_type(flags), params_type(flags)
-        px, ldx = a.matrix(x, ldx, dtype)
-        pr, ldr = a.matrix(residual, ldr, res)
-        py, ldy = a.matrix(y, ldy, res)
-        pb = a.vector(bias, cols, par)
-        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, a.stream(stream)), where)
+        w, dev = name_dropout_add, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        px, ldx = _matrix(w, dev, x, ldx, rows, cols, dtype)
+        pr, ldr = _matrix(w, dev, residual, ldr, rows, cols, res)
+        py, ldy = _matrix(w, dev, y, ldy, rows, cols, res)
+        pb = _vector(w, dev, bias, cols, par)
+        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, _on(stream, dev)), w)
 
     def dropout_add_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dx, lddx, dbias, workspace=None, stream=None):
-        where = "tk_dropout_add_backward_" + suffix
-        a = _Args(where, rows, cols)
-        res, par = residual_type(flags), params_type(flags)
-        pdy, lddy = a.matrix(dy, lddy, res)
-        pdx, lddx = a.matrix(dx, lddx, dtype)
-        pb = a.vector(dbias, cols, par)
-        ws, n, keep = a.workspace(workspace, stream, dbias is not None)
-        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, a.stream(stream)), where)
+        w, dev = name_dropout_add_backward, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pdy, lddy = _matrix(w, dev, dy, lddy, rows, cols, res)
+        pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, dtype)
+        pb = _vector(w, dev, dbias, cols, par)
+        ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols, dbias is not None)
+        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, _on(stream, dev)), w)
 
     def layer_norm(rows, cols, eps, flags, x, ldx, gamma, beta, y, ldy, mean=None, rstd=None, stream=None):
-        where = "tk_layer_norm_" + suffix
-        a = _Args(where, rows, cols)
-        res, par = residual_type(flags), params_type(flags)
-        px, ldx = a.matrix(x, ldx, res)
-        py, ldy = a.matrix(y, ldy, dtype)
-        pg, pb = a.vector(gamma, cols, par), a.vector(beta, cols, par)
-        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
-        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, a.stream(stream)), where)
+        w, dev = name_layer_norm, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        px, ldx = _matrix(w, dev, x, ldx, rows, cols, res)
+        py, ldy = _matrix(w, dev, y, ldy, rows, cols, dtype)
+        pg, pb = _vector(w, dev, gamma, cols, par), _vector(w, dev, beta, cols, par)
+        pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
+        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, _on(stream, dev)), w)
 
     def layer_norm_backward(rows, cols, flags, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta,
                             workspace=None, stream=None):
-        where = "tk_layer_norm_backward_" + suffix
-        a = _Args(where, rows, cols)
-        res, par = residual_type(flags), params_type(flags)
-        pdy, lddy = a.matrix(dy, lddy, dtype)
-        px, ldx = a.matrix(x, ldx, res)
-        pdx, lddx = a.matrix(dx, lddx, res)
-        pg, pdg, pdb = (a.vector(v, cols, par) for v in (gamma, dgamma, dbeta))
-        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
-        ws, n, keep = a.workspace(workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None)
+        w, dev = name_layer_norm_backward, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pdy, lddy = _matrix(w, dev, dy, lddy, rows, cols, dtype)
+        px, ldx = _matrix(w, dev, x, ldx, rows, cols, res)
+        pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, res)
+        pg, pdg, pdb = (_vector(w, dev, v, cols, par) for v in (gamma, dgamma, dbeta))
+        pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
+        ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols,
+                                 cols > _SUMS_ALONE or dgamma is not None or dbeta is not None)
         _check(norm_bwd(rows, cols, flags, pdy, lddy, px, ldx, pg, pm, ps, pdx, lddx, pdg, pdb, ws, n,
-                        a.stream(stream)), where)
+                        _on(stream, dev)), w)
 
     def dropout_add_layer_norm(key, start_draw, rows, cols, p, eps, flags, x, ldx, bias, residual, ldr, gamma, beta, sum,
                                lds, y, ldy, mean=None, rstd=None, stream=None):
-        where = "tk_dropout_add_layer_norm_" + suffix
-        a = _Args(where, rows, cols)
-        res, par = residual_type(flags), params_type(flags)
-        px, ldx = a.matrix(x, ldx, dtype)
-        pr, ldr = a.matrix(residual, ldr, res)
-        pv, lds = a.matrix(sum, lds, res)
-        py, ldy = a.matrix(y, ldy, dtype)
-        pb, pg, pt = (a.vector(v, cols, par) for v in (bias, gamma, beta))
-        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
+        w, dev = name_dropout_add_layer_norm, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        px, ldx = _matrix(w, dev, x, ldx, rows, cols, dtype)
+        pr, ldr = _matrix(w, dev, residual, ldr, rows, cols, res)
+        pv, lds = _matrix(w, dev, sum, lds, rows, cols, res)
+        py, ldy = _matrix(w, dev, y, ldy, rows, cols, dtype)
+        pb, pg, pt = (_vector(w, dev, v, cols, par) for v in (bias, gamma, beta))
+        pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
         _check(both_fwd(key, start_draw, rows, cols, p, eps, flags, px, ldx, pb, pr, ldr, pg, pt, pv, lds, py, ldy, pm, ps,
-                        a.stream(stream)), where)
+                        _on(stream, dev)), w)
 
     def dropout_add_layer_norm_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, gamma, mean,
                                         rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace=None, stream=None):
-        where = "tk_dropout_add_layer_norm_backward_" + suffix
-        a = _Args(where, rows, cols)
-        res, par = residual_type(flags), params_type(flags)
-        pdy, lddy = a.matrix(dy, lddy, dtype)
-        pds, ldds = a.matrix(dsum, ldds, res)
-        pv, lds = a.matrix(sum, lds, res)
-        pdx, lddx = a.matrix(dx, lddx, dtype)
-        pdr, lddr = a.matrix(dresidual, lddr, res)
-        pg, pdg, pdb, pdt = (a.vector(v, cols, par) for v in (gamma, dgamma, dbeta, dbias))
-        pm, ps = a.vector(mean, rows, float32), a.vector(rstd, rows, float32)
-        ws, n, keep = a.workspace(workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None
-                                  or dbias is not None)
+        w, dev = name_dropout_add_layer_norm_backward, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pdy, lddy = _matrix(w, dev, dy, lddy, rows, cols, dtype)
+        pds, ldds = _matrix(w, dev, dsum, ldds, rows, cols, res)
+        pv, lds = _matrix(w, dev, sum, lds, rows, cols, res)
+        pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, dtype)
+        pdr, lddr = _matrix(w, dev, dresidual, lddr, rows, cols, res)
+        pg, pdg, pdb, pdt = (_vector(w, dev, v, cols, par) for v in (gamma, dgamma, dbeta, dbias))
+        pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
+        ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols, cols > _SUMS_ALONE or dgamma is not None
+                                 or dbeta is not None or dbias is not None)
         _check(both_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pds, ldds, pv, lds, pg, pm, ps, pdx, lddx, pdr,
-                        lddr, pdg, pdb, pdt, ws, n, a.stream(stream)), where)
+                        lddr, pdg, pdb, pdt, ws, n, _on(stream, dev)), w)
 
     out = {}
     for f in (dropout_add, dropout_add_backward, layer_norm, layer_norm_backward, dropout_add_layer_norm,
