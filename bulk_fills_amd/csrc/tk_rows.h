@@ -1,7 +1,13 @@
 // tk_rows.h -- kernels of the row operators (dropout-add, layer norm, both fused) for one
 // pair of types: T of the activations, R of the residual stream.  Instantiated by
-// tk_rows_f32.hip, tk_rows_f16.hip and tk_rows_bf16.hip; the C entry points are in
-// tk_rows.hip.
+// tk_rows_{f32,f16,bf16}.hip and, with a float residual stream, tk_rows_{f16,bf16}_r32.hip; the
+// C entry points are in tk_rows.hip.
+//
+// All of them are bound by memory: 4 to 16 bytes an element for 15 to 40 vector instructions.
+// Bytes that must move over the time that was measured, on MI355X (streams of this size reach
+// 6.5 TB/s): dropout-add bf16 8192x4096 6.2 TB/s, its backward 5.5; layer norm bf16 16384x8192
+// with a float stream 6.2, its backward 16384x4096 5.5; fused forward bf16 16384x8192 5.9, fused
+// backward 8192x8192 5.6.
 //
 // A lane handles chunks of CH consecutive elements of a row: 16 bytes of the wider of the two
 // types.  Addresses need only element alignment (gfx950 takes vector loads and stores at any),
@@ -607,7 +613,7 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
   constexpr int kSums = (kNorm ? 2 : 0) + (kBias ? 1 : 0), kGroups = 64 / kLanes;
   typedef typename std::conditional<kNorm, T, R>::type D;
   const uint32_t lane = threadIdx.x & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t c = (blockIdx.x * kLanes + lane % kLanes) * CH;
+  const uint32_t strip = a.strip0 + blockIdx.x, c = (strip * kLanes + lane % kLanes) * CH;
   const int nv = (int)(a.cols - c);
   const uint64_t step = (uint64_t)gridDim.y * (16 * kGroups);
   float acc[kSums ? kSums : 1][CH];
@@ -655,7 +661,7 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
       if (lane < kLanes) put_sums<CH>(tile[wave] + lane * CH, CH, acc[k]);
       __syncthreads();
       float *line = a.partial + ((uint64_t)k * gridDim.y + blockIdx.y) * a.cols;
-      const uint32_t i = threadIdx.x, col = blockIdx.x * (kLanes * CH) + i;
+      const uint32_t i = threadIdx.x, col = strip * (kLanes * CH) + i;
       if (i < kLanes * CH && col < a.cols) {
         float s = 0.0f;
 #pragma unroll
@@ -765,8 +771,15 @@ static void norm_bwd_as(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
 
 template <class T, class R, bool kNorm, bool kX, bool kBias, bool kOnce, int CH, int kLanes>
 static void launch_cols(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
-  hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kOnce, CH, kLanes>), dim3((uint32_t)p.strips, (uint32_t)p.lines),
-                     dim3(1024), 0, s, a);
+  // a launch holds fewer than 2^32 threads to a dimension
+  constexpr uint64_t kMost = 1u << 20;
+  BwdArgs b = a;
+  for (uint64_t strip = 0; strip < p.strips; strip += kMost) {
+    b.strip0 = (uint32_t)strip;
+    hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kOnce, CH, kLanes>),
+                       dim3((uint32_t)(p.strips - strip < kMost ? p.strips - strip : kMost), (uint32_t)p.lines), dim3(1024), 0,
+                       s, b);
+  }
 }
 
 template <class T, class R, bool kOnce>

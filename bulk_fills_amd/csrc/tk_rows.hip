@@ -15,8 +15,8 @@ struct FinishArgs {
   const float *partial;
   void *out[3];  // null: not wanted
   uint64_t lines;
-  uint32_t cols;
-  int kind;  // 0 float, 1 binary16, 2 bfloat16
+  uint32_t cols, col0;  // col0: the launch's first column
+  int kind;             // 0 float, 1 binary16, 2 bfloat16
 };
 
 __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
@@ -24,7 +24,7 @@ __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
   __shared__ float part[kWaves][64];
   void *out = a.out[blockIdx.y];
   if (!out) return;
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = a.col0 + blockIdx.x * 64 + lane;
   const float *p = a.partial + (uint64_t)blockIdx.y * a.lines * a.cols + c;
   float s = 0.0f;
   if (c < a.cols) {
@@ -198,8 +198,13 @@ static bool params_f32(RowType t, uint32_t flags) { return t == kF32 || (flags &
 
 static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
                         void *c, hipStream_t stream) {
-  FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
-  hipLaunchKernelGGL(k_finish, dim3((uint32_t)((cols + 63) / 64), c ? 3 : b ? 2 : 1), dim3(1024), 0, stream, f);
+  FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, 0, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
+  const uint64_t most = 1ull << 27;  // columns of a launch, which holds fewer than 2^32 threads
+  for (uint64_t k = 0; k < cols; k += most) {
+    f.col0 = (uint32_t)k;
+    const uint64_t n = cols - k < most ? cols - k : most;
+    hipLaunchKernelGGL(k_finish, dim3((uint32_t)((n + 63) / 64), c ? 3 : b ? 2 : 1), dim3(1024), 0, stream, f);
+  }
   return launch_status();
 }
 

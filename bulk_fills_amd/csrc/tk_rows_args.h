@@ -36,7 +36,7 @@ struct BwdArgs {
   float *partial;  // lines of partial column sums: dgamma's, dbeta's, then dbias's; null: no sums wanted
   float *stats;    // mean(g), mean(g h) of every row (wide rows)
   uint64_t rows, lddy, ldds, lds, lddx, lddr;
-  uint32_t cols, waves;
+  uint32_t cols, waves, strip0;  // strip0: the launch's first strip of columns
   bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
 };

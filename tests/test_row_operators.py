@@ -2,7 +2,8 @@
 both fused, forward and backward, at the sizes where a shape of kernel begins or ends, for
 every pair of types; rows cut from wider buffers at odd addresses, whose neighbours must stay
 as they were; in place; cut calls; captured calls; two streams; and a block's run of them."""
-import numpy as np
+import contextlib
+
 import pytest
 import torch
 
@@ -307,12 +308,10 @@ def test_in_place(kind, cols):
         assert torch.equal(x2, y2)
 
 
-@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("kind", [k for k in KINDS if not k[1]], ids=[i for i, k in zip(IDS, KINDS) if not k[1]])
 def test_slices_of_one_buffer(kind):
     """x and y as column slices of one buffer, read and written side by side."""
     T, R, W = types(kind)
-    if T != R:
-        pytest.skip("one buffer has one type")
     n, cols = 23, 1000
     d, go = run_block(kind, n, cols, 5)
     packed = torch.full((n, 3 * cols + 7), FILL, dtype=T, device="cuda")
@@ -464,6 +463,76 @@ def test_two_streams(kind):
         assert_same(b, want[1], f"stream b, round {r}")
 
 
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("cols", [3, 40, 100, 200, 1000, 5001, 7000, 20000, 40000])
+def test_large_calls(kind, cols):
+    """Calls whose reads pass the caches (over 96 MB of them) against calls on quarters of their
+    rows, most of which read through them: bit for bit by rows; and their column sums
+    against float64 sums, which may be off by a half step of each term and of the sum."""
+    T, R, W = types(kind)
+    n, p = -(-52_000_000 // cols), 0.25
+    log(f"large {kind} {n}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    mat = lambda t: torch.empty(n, cols, dtype=t, device="cuda").normal_(generator=g)  # noqa: E731
+    vec = lambda: torch.randn(cols, generator=g, device="cuda").to(W)  # noqa: E731
+    out = lambda t: torch.full((n, cols), FILL, dtype=t, device="cuda")  # noqa: E731
+    x, r, dy, ds, bias, gamma, beta = mat(T), mat(R), mat(T), mat(R), vec(), vec(), vec()
+
+    def go(lo, hi, o):
+        m, sl, fl = hi - lo, slice(lo, hi), flags(kind)
+        start = 40 + lo * cols
+        fn("dropout_add", kind)(8, start, m, cols, p, fl, x[sl], None, bias, r[sl], None, o["add"][sl], None)
+        fn("dropout_add", kind)(8, start, m, cols, p, fl, x[sl], None, None, None, None, o["drop"][sl], None)
+        fn("dropout_add_backward", kind)(8, start, m, cols, p, fl, ds[sl], None, o["dx0"][sl], None, o["dbias0"])
+        fn("dropout_add_layer_norm", kind)(8, start, m, cols, p, 1e-5, fl, x[sl], None, bias, r[sl], None, gamma, beta,
+                                           o["sum"][sl], None, o["y"][sl], None, o["mean"][sl], o["rstd"][sl])
+        fn("layer_norm", kind)(m, cols, 1e-5, fl, r[sl], None, gamma, beta, o["y1"][sl], None)
+        fn("dropout_add_layer_norm_backward", kind)(8, start, m, cols, p, fl, dy[sl], None, ds[sl], None, o["sum"][sl], None,
+                                                    gamma, o["mean"][sl], o["rstd"][sl], o["dx"][sl], None, o["dr"][sl],
+                                                    None, o["dg"], o["db"], o["dbias"])
+
+    def outs():
+        o = {k: out(t) for k, t in (("add", R), ("drop", R), ("dx0", T), ("sum", R), ("y", T), ("y1", T), ("dx", T), ("dr", R))}
+        o.update({k: torch.full((n,), FILL, device="cuda") for k in ("mean", "rstd")})
+        o.update({k: torch.full((cols,), FILL, dtype=W, device="cuda") for k in ("dg", "db", "dbias", "dbias0")})
+        return o
+
+    whole, cut = outs(), outs()
+    go(0, n, whole)
+    for k in range(4):
+        go(n * k // 4, n * (k + 1) // 4, cut)
+    for k in ("add", "drop", "dx0", "sum", "y", "y1", "mean", "rstd", "dx", "dr"):
+        assert torch.equal(whole[k], cut[k]), k
+    h = (whole["sum"].double() - whole["mean"].double()[:, None]) * whole["rstd"].double()[:, None]
+    for k, terms, half in (("dg", dy.double() * h, 4 * ref.U), ("db", dy.double(), 0.0),
+                           ("dbias", whole["dx"].double(), torch.finfo(T).eps / 2),
+                           ("dbias0", whole["dx0"].double(), torch.finfo(T).eps / 2)):
+        size = terms.abs().sum(0)
+        limit = size * (half + (n + 16) * ref.U)
+        want = terms.sum(0)
+        limit = limit + (want.abs() + limit) * torch.finfo(W).eps / 2 + n * ref.TINY[T]
+        far = (whole[k].double() - want).abs() > limit
+        assert not bool(far.any()), (k, int(far.sum()))
+
+
+def test_very_long_rows():
+    """More columns than one launch of the strips and of their sums covers (2^28 and 2^27): over one
+    row the bias's gradient is dx, and each is dy over 1 - p or 0."""
+    cols = (1 << 28) + 777
+    log("very long rows")
+    dy = torch.full((1, cols), 0.75, device="cuda")
+    dx, db = torch.full((1, cols), FILL, device="cuda"), torch.full((cols,), FILL, device="cuda")
+    tk.tk_dropout_add_backward_f32(3, 9, 1, cols, 0.25, 0, dy, None, dx, None, db)
+    assert torch.equal(dx[0], db)
+    kept = dx == 1.0
+    assert bool((kept | (dx == 0)).all())
+    tail = ref.keep_mask(3, 9 + cols - 5000, 1, 5000, 0.25)
+    assert torch.equal(kept[:, -5000:].cpu().double(), tail)
+    y = torch.empty_like(dx)
+    tk.tk_dropout_add_f32(3, 9, 1, cols, 0.25, 0, dy, None, None, None, None, y, None)
+    assert torch.equal(y, dx)
+
+
 def test_binding_checks_on_the_device():
     """What the binding refuses of device tensors, before any launch."""
     x, y = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 8, device="cuda")
@@ -489,6 +558,13 @@ def test_binding_checks_on_the_device():
     # a call that needs none takes none
     tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, None, None, None, torch.cuda.Stream())
     torch.cuda.synchronize()
+    # up to 8192 columns the gradients of the rows alone need none, beyond they do
+    for cols, refused in ((8192, False), (8193, True)):
+        z = torch.zeros(2, cols, device="cuda")
+        args = (2, cols, 0, z, None, z, None, None, mu[:2], mu[:2], torch.empty_like(z), None, None, None)
+        with pytest.raises(tk.TkError) if refused else contextlib.nullcontext():
+            tk.tk_layer_norm_backward_f32(*args, (0, 0))
+        tk.tk_layer_norm_backward_f32(*args)
     call(4, 8, 1e-5, 0, x.view(2, 2, 8), None, None, None, y, 8)  # any shape that flattens
     call(1, 8, 1e-5, 0, x[1:2], 100, None, None, y[:1], None)     # one row has no distance to a next
     torch.cuda.synchronize()
