@@ -737,8 +737,9 @@ static void launch_fwd(FwdArgs a, hipStream_t s) {
 
 // Lanes to a row by its width, eight elements a lane.  Beyond twelve waves a row (6144 columns)
 // a lane takes sixteen, so that two rows share a compute unit (layer norm bf16 8192x8192 45.5
-// against 53 us), and beyond sixteen waves of those thirty-two, with the parameters read again
-// for every row (fused forward 1024x32768 59 us, 118 in three passes).
+// against 53 us), and beyond sixteen waves of those 24 or 32, with the parameters read again for
+// every row (fused forward bf16 1024x32768 59 us, in three passes 118; 655x20000 27 us with 24,
+// 31 with 32; 4096x12288 71 us with sixteen and the parameters kept, 81 with 24).
 template <class T, class R, bool kX, bool kOnce>
 static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   constexpr int CH = kChunk<T, R>, K = 8 / CH;
@@ -748,6 +749,7 @@ static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   else if (a.cols <= 256) launch_fwd<T, R, kX, kOnce, CH, 32, K>(a, s);
   else if (a.cols <= 6144) launch_fwd<T, R, kX, kOnce, CH, 64, K>(a, s);
   else if (a.cols <= 16384) launch_fwd<T, R, kX, kOnce, CH, 64, 2 * K>(a, s);
+  else if (a.cols <= 24576) launch_fwd<T, R, kX, kOnce, CH, 64, 3 * K, false>(a, s);
   else if (a.cols <= 32768) launch_fwd<T, R, kX, kOnce, CH, 64, 4 * K, false>(a, s);
   else hipLaunchKernelGGL((k_norm_fwd_wide<T, R, kX>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
 }
