@@ -566,7 +566,8 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
 }
 
 // Rows wider than k_norm_bwd's registers hold with their column sums: first norm_grad's two
-// numbers for every row, then k_cols_bwd over columns.
+// numbers for every row, then k_cols_bwd over columns, which reads dy and sum again (here they
+// are read through the caches).
 template <class T, class R>
 __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
   constexpr int CH = kChunk<T, R>, kTpr = 1024;
@@ -575,14 +576,23 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s[2] = {0.0f, 0.0f};
-    for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
+    const T *dy = (const T *)a.dy + row * a.lddy;
+    const R *sum = (const R *)a.sum + row * a.lds;
+    uint32_t c = threadIdx.x * CH;
+    // the next chunk is loaded before the present one is used (past the end: the row's last, unused)
+    Chunk<T, CH> next_dy = load_chunk<false, CH>(dy + chunk_at<CH>(c, a.cols));
+    Chunk<R, CH> next_sum = load_chunk<false, CH>(sum + chunk_at<CH>(c, a.cols));
+    for (; c < a.cols; c += kTpr * CH) {
       const int nv = (int)(a.cols - c);
-      const uint32_t at = chunk_at<CH>(c, a.cols);
+      const uint32_t at = chunk_at<CH>(c + kTpr * CH, a.cols);
       float g[CH], h[CH], w[CH];
-      // read again by k_cols_bwd: kept in the caches
-      unpack<CH, T>(*(const Chunk<T, CH> *)((const T *)a.dy + row * a.lddy + at), nv, g);
-      unpack<CH, R>(*(const Chunk<R, CH> *)((const R *)a.sum + row * a.lds + at), nv, h);
+      const Chunk<T, CH> here_dy = next_dy;
+      const Chunk<R, CH> here_sum = next_sum;
+      next_dy = load_chunk<false, CH>(dy + at);
+      next_sum = load_chunk<false, CH>(sum + at);
       load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, w);
+      unpack<CH, T>(here_dy, nv, g);
+      unpack<CH, R>(here_sum, nv, h);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         const float x = g[e] * w[e];
