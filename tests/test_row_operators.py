@@ -238,7 +238,9 @@ def test_f32_dropout_add_is_dropout(kind):
     n, cols = 301, 1003
     x = torch.randn(n, cols, device="cuda").to(T)
     x[x == 0] = 1
-    for start, p in ((0, 0.1), (5, 0.5), (64, 0.999), (3, 1.0 - 2.0 ** -24), (0, 2.0 ** -25)):
+    last = (1 << 32) - n * cols  # the last counters there are
+    for start, p in ((0, 0.1), (5, 0.5), (64, 0.999), (3, 1.0 - 2.0 ** -24), (0, 2.0 ** -25), (last, 0.3), (last - 5, 0.3),
+                     ((1 << 16) - 3, 0.5)):
         y, want = torch.empty(n, cols, dtype=R, device="cuda"), torch.empty(n, cols, device="cuda")
         fn("dropout_add", kind)(9, start, n, cols, p, flags(kind), x, None, None, None, None, y, None)
         tk.tk_dropout_f32(9, start, n * cols, p, x.float(), want)
