@@ -8,9 +8,12 @@
 namespace tk {
 
 // ---------------------------------------------------------------------------------------
-// The end of the column sums: line k of the partial sums into element type float or the
-// parameters', one column a lane, the lines in a fixed order
+// The end of the column sums: lines of partial sums into element type float or the parameters',
+// in a fixed order
 // ---------------------------------------------------------------------------------------
+// A plan's lines, one to a work-group: at most one work-group to a compute unit.
+constexpr uint64_t kMaxLines = 256;
+
 struct FinishArgs {
   const float *partial;
   void *out[3];  // null: not wanted
@@ -19,24 +22,53 @@ struct FinishArgs {
   int kind;             // 0 float, 1 binary16, 2 bfloat16
 };
 
+// A work-group takes kCols columns, a wave 64 / kCols lines of them at a time: 64, or 32 up to
+// 4096 columns, where work-groups are few (layer norm backward bf16 1000x2048: 11.1 us, with 64
+// columns 11.5; 300x12000: 15.1 and 14.2).
+//
+// The sum of every kLines-th of a column's lines from the first one, at most kSteps of them.  All
+// are read at once, beyond the last line that line again: a loop over the lines waits for loads
+// one by one (2000x1024, of 250 lines: 9.2 against 12.9 us).  Several lines have fewer than 2^18
+// columns: the distances fit 32 bits.
+template <int kLines, int kSteps>
+__device__ __forceinline__ float column_sum(const float *p, uint32_t first, uint32_t lines, uint32_t pitch) {
+  float v[kSteps], s = 0.0f;
+  uint32_t at = first * pitch;
+  const uint32_t last = (lines - 1) * pitch;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    v[i] = __builtin_nontemporal_load(p + (at < last ? at : last));
+    at += kLines * pitch;
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) s += first + kLines * i < lines ? v[i] : 0.0f;
+  return s;
+}
+
+template <int kCols>
 __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
-  constexpr int kWaves = 16;
-  __shared__ float part[kWaves][64];
+  constexpr uint32_t kLines = 1024 / kCols, kMost = kMaxLines / kLines;
+  __shared__ float part[16][kCols];
   void *out = a.out[blockIdx.y];
   if (!out) return;
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = a.col0 + blockIdx.x * 64 + lane;
-  const float *p = a.partial + (uint64_t)blockIdx.y * a.lines * a.cols + c;
-  float s = 0.0f;
+  const uint32_t i = threadIdx.x % kCols, first = threadIdx.x / kCols, c = a.col0 + blockIdx.x * kCols + i;
   if (c < a.cols) {
-#pragma unroll 16
-    for (uint64_t l = wave; l < a.lines; l += kWaves) s += p[l * a.cols];
+    const uint32_t lines = (uint32_t)a.lines, pitch = (uint32_t)line_pitch(a.cols);
+    const float *p = a.partial + (uint64_t)blockIdx.y * lines * pitch + c;
+    float s = lines == 0            ? 0.0f  // no rows, no workspace
+              : lines <= kLines     ? column_sum<kLines, 1>(p, first, lines, pitch)
+              : lines <= 2 * kLines ? column_sum<kLines, 2>(p, first, lines, pitch)
+              : lines <= 4 * kLines ? column_sum<kLines, 4>(p, first, lines, pitch)
+              : lines <= 8 * kLines ? column_sum<kLines, 8>(p, first, lines, pitch)
+                                    : column_sum<kLines, kMost>(p, first, lines, pitch);
+    if (kCols == 32) s += __shfl_xor(s, 32);
+    part[threadIdx.x >> 6][i] = s;
   }
-  part[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < a.cols) {
-    s = 0.0f;
+  if (threadIdx.x < kCols && c < a.cols) {
+    float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) s += part[w][lane];
+    for (int w = 0; w < 16; ++w) s += part[w][i];
     if (a.kind == 0) ((float *)out)[c] = s;
     else if (a.kind == 1) ((_Float16 *)out)[c] = (_Float16)s;
     else ((__bf16 *)out)[c] = (__bf16)s;
@@ -50,6 +82,16 @@ constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 31;
 constexpr uint64_t kRowsInRegisters = 8192;      // columns that k_norm_bwd holds
 constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through the caches (tk_rows.h)
 
+// Up to this many sets of rows one work-group (or one to a strip) takes them all and writes the
+// gradients itself (layer norm backward bf16 128x128 5.1 us, with a second kernel 6.4; four sets
+// to a work-group take up to 3 us longer than one with that kernel).
+constexpr uint64_t kAloneSets = 2;
+
+// Partial sums of this many floats or more (of one gradient) are written past the caches: the
+// second kernel starts when they are out of the L2s (256x8192 11.9 us, through them 12.5;
+// 1000x4096 12.6 and 13.5).  Fewer are read from there (100x4096 9.1 us, past them 9.4).
+constexpr uint64_t kPastFloats = 9 << 16;
+
 // Strips of columns by sets of rows: one work-group of 16 waves a compute unit, or fewer that
 // have one row for each of their groups of lanes.  Dropout-add's backward bf16 8192x4096 takes
 // 25.9, 26.8, 28.3 and 28.8 us with 256, 512, 768 and 1024 work-groups, the fused backward
@@ -60,7 +102,7 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
   p.lanes = cols <= 8ull * ch ? 8 : cols <= 16ull * ch ? 16 : cols <= 32ull * ch ? 32 : 64;
   p.strips = (cols + p.lanes * ch - 1) / (p.lanes * ch);
   const uint64_t at_once = 16 * 64 / p.lanes, most = (rows + at_once - 1) / at_once;
-  p.lines = p.strips < 256 ? 256 / p.strips : 1;
+  p.lines = most <= kAloneSets ? 1 : p.strips < kMaxLines ? kMaxLines / p.strips : 1;
   if (p.lines > most) p.lines = most;
   return p;
 }
@@ -77,11 +119,16 @@ static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
   p.row_waves = p.lanes < 64 ? 1 : (int)((cols + 511) / 512);
   p.waves = 16 / p.row_waves * p.row_waves;
   const uint64_t per = p.lanes < 64 ? 64 * p.waves / p.lanes : p.waves / p.row_waves, sets = (rows + per - 1) / per;
-  p.lines = sets < 256 ? sets : 256;
+  // What a set reads and what its line costs to write and read are alike: wide rows go several
+  // sets to a work-group (256x8192 with 256, 128 and 64 lines: 16.4, 13.0 and 12.4 us).
+  uint64_t least = sets <= kAloneSets ? sets : 1;
+  while (sets > kAloneSets && least < 4 && sets * cols >= (least * least) << 19) least *= 2;
+  p.lines = (sets + least - 1) / least;
+  if (p.lines > kMaxLines) p.lines = kMaxLines;
   return p;
 }
 
-static uint64_t bytes_of(const BwdPlan &p, uint64_t cols) { return 12 * p.lines * cols; }
+static uint64_t bytes_of(const BwdPlan &p, uint64_t cols) { return p.lines > 1 ? 12 * p.lines * line_pitch(cols) : 0; }
 
 // The larger of both chunk sizes and both kinds of call, so that one size serves every type.
 static uint64_t workspace_bytes(uint64_t rows, uint64_t cols) {
@@ -199,11 +246,14 @@ static bool params_f32(RowType t, uint32_t flags) { return t == kF32 || (flags &
 static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
                         void *c, hipStream_t stream) {
   FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, 0, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
-  const uint64_t most = 1ull << 27;  // columns of a launch, which holds fewer than 2^32 threads
+  const uint64_t wide = cols > 4096 ? 64 : 32;
+  const uint64_t most = 1ull << 26;  // columns of a launch, which holds fewer than 2^32 threads
   for (uint64_t k = 0; k < cols; k += most) {
     f.col0 = (uint32_t)k;
     const uint64_t n = cols - k < most ? cols - k : most;
-    hipLaunchKernelGGL(k_finish, dim3((uint32_t)((n + 63) / 64), c ? 3 : b ? 2 : 1), dim3(1024), 0, stream, f);
+    const dim3 grid((uint32_t)((n + wide - 1) / wide), c ? 3 : b ? 2 : 1);
+    if (wide == 64) hipLaunchKernelGGL(k_finish<64>, grid, dim3(1024), 0, stream, f);
+    else hipLaunchKernelGGL(k_finish<32>, grid, dim3(1024), 0, stream, f);
   }
   return launch_status();
 }
@@ -314,12 +364,14 @@ static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, u
   BwdArgs a{};
   a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
   a.rows = rows; a.cols = (uint32_t)cols;
-  a.partial = (float *)workspace;
+  a.alone = plan.lines == 1;
+  a.sums[2] = dbias;
+  a.partial = a.alone ? nullptr : (float *)workspace;
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
   a.once = rows * cols * c.res() > kCachedReads;
   k.add_bwd_sums(a, plan, stream);
-  if ((st = launch_status()) != TK_OK) return st;
+  if ((st = launch_status()) != TK_OK || a.alone) return st;
   return finish(t, flags, a.partial, plan.lines, cols, dbias, nullptr, nullptr, stream);
 }
 
@@ -394,13 +446,16 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   a.gamma = gamma; a.mean = mean; a.rstd = rstd;
   a.dx = dx; a.lddx = lddx; a.dresidual = dresidual; a.lddr = lddr;
   a.rows = rows; a.cols = (uint32_t)cols; a.waves = (uint32_t)plan.row_waves;
-  a.partial = sums ? (float *)workspace : nullptr;
+  a.alone = sums && plan.lines == 1;
+  a.sums[0] = dgamma; a.sums[1] = dbeta; a.sums[2] = dbias;
+  a.partial = sums && !a.alone ? (float *)workspace : nullptr;
+  a.past = plan.lines * cols >= kPastFloats;
   a.stats = !plan.strips ? nullptr : (float *)((char *)workspace + need - 8 * rows);
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
   a.once = rows * cols * (c.t() + (dsum ? 2 : 1) * c.res()) > kCachedReads;
   k.norm_bwd(a, plan, dbias != nullptr, stream);
-  if ((st = launch_status()) != TK_OK || !sums) return st;
+  if ((st = launch_status()) != TK_OK || !sums || a.alone) return st;
   return finish(t, flags, a.partial, plan.lines, cols, dgamma, dbeta, dbias, stream);
 }
 

@@ -21,7 +21,9 @@ IDS = ["f32", "f16", "f16-r32-p32", "bf16", "bf16-r32", "bf16-p32"]
 SIZES = [(1, 1), (3, 1), (5, 2), (1, 7), (33, 8), (9, 9), (2, 64), (17, 127), (50, 128), (7, 129), (6, 511), (70, 512),
          (3, 513), (5, 1000), (8, 1024), (5, 1025), (3, 2047), (2, 2048), (4, 2049), (33, 4096), (3, 4097), (5, 5001),
          (2, 8192), (3, 8193), (2, 16384), (3, 16385), (2, 24577), (1, 32768), (2, 32769), (1, 70001), (2500, 40),
-         (1300, 136), (1201, 1032)]
+         (1300, 136), (1201, 1032),
+         # backward: 3, 60, 75, 256 lines of partial sums; 100 and 160 of more than the caches are to hold
+         (40, 300), (300, 1500), (600, 520), (4200, 600), (200, 8000), (640, 4096)]
 FILL = -77.0
 
 
@@ -521,14 +523,16 @@ def test_large_calls(kind, cols):
 
 
 def test_very_long_rows():
-    """More columns than one launch of the strips and of their sums covers (2^28 and 2^27): over one
-    row the bias's gradient is dx, and each is dy over 1 - p or 0."""
+    """More columns than one launch of the strips and of their sums covers (2^28 and 2^26): over one
+    row the bias's gradient is dx, and each is dy over 1 - p or 0; over none it is 0."""
     cols = (1 << 28) + 777
     log("very long rows")
     dy = torch.full((1, cols), 0.75, device="cuda")
     dx, db = torch.full((1, cols), FILL, device="cuda"), torch.full((cols,), FILL, device="cuda")
     tk.tk_dropout_add_backward_f32(3, 9, 1, cols, 0.25, 0, dy, None, dx, None, db)
     assert torch.equal(dx[0], db)
+    tk.tk_dropout_add_backward_f32(3, 9, 0, cols, 0.25, 0, dy[:0], None, dx[:0], None, db)
+    assert not bool(db.any())
     kept = dx == 1.0
     assert bool((kept | (dx == 0)).all())
     tail = ref.keep_mask(3, 9 + cols - 5000, 1, 5000, 0.25)
@@ -557,9 +561,15 @@ def test_binding_checks_on_the_device():
     with pytest.raises(tk.TkError):
         call(4, 8, -1.0, 0, x, None, None, None, y, None)
     mu = torch.zeros(4, device="cuda")
+    many, stats, sums = torch.zeros(4000, 8, device="cuda"), torch.zeros(4000, device="cuda"), torch.zeros(8, device="cuda")
     with pytest.raises(ValueError, match="workspace"):
-        tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, torch.zeros(8, device="cuda"), None,
-                                      None, torch.cuda.Stream())
+        tk.tk_layer_norm_backward_f32(4000, 8, 0, many, None, many, None, None, stats, stats, torch.empty_like(many), None,
+                                      sums, None, None, torch.cuda.Stream())
+    # one work-group's sums need none
+    assert tk.tk_backward_workspace_bytes(4, 8) == 0
+    torch.cuda.synchronize()
+    tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, sums, None, None, torch.cuda.Stream())
+    tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, sums, None, (0, 0))
     # a call that needs none takes none
     tk.tk_layer_norm_backward_f32(4, 8, 0, x, None, x, None, None, mu, mu, y, None, None, None, None, torch.cuda.Stream())
     torch.cuda.synchronize()

@@ -125,23 +125,24 @@ def test_overlaps(t):
     assert both(t, gamma=E) == EINVAL
     assert both_b(t, dx=G) == EINVAL
     assert both_b(t, dgamma=H, dbeta=H, ws=WS, n=1 << 30) == EINVAL
-    assert both_b(t, dgamma=H, ws=H, n=1 << 30) == EINVAL
-    assert both_b(t, dgamma=H, ws=F, n=1 << 30) == EINVAL
+    assert both_b(t, dgamma=H, rows=4000, ws=H, n=1 << 30) == EINVAL
+    assert both_b(t, dgamma=H, rows=4000, ws=F, n=1 << 30) == EINVAL
     if t != "f32":
         assert add(t, flags=tk.TK_RESIDUAL_F32, y=A) == EINVAL  # one address, two types
 
 
 @pytest.mark.parametrize("t", TYPES)
 def test_workspace(t):
-    need = tk.tk_backward_workspace_bytes(4, 8)
+    need = tk.tk_backward_workspace_bytes(4000, 8)
     assert need > 0
     for f in (add_b, norm_b, both_b):
         name = "dbias" if f is add_b else "dgamma"
-        assert f(t, **{name: H}) == EINVAL
-        assert f(t, **{name: H}, ws=WS, n=need - 1) == EINVAL
-        assert f(t, **{name: H}, ws=WS + 2, n=need) == EINVAL
+        assert f(t, rows=4000, **{name: H}) == EINVAL
+        assert f(t, rows=4000, **{name: H}, ws=WS, n=need - 1) == EINVAL
+        assert f(t, rows=4000, **{name: H}, ws=WS + 2, n=need) == EINVAL
     # wide rows need one even without parameter gradients
     assert norm_b(t, cols=8193, lddy=8193, ldx=8193, lddx=8193) == EINVAL
+    assert tk.tk_backward_workspace_bytes(4, 8) == 0  # one work-group's sums
     assert tk.tk_backward_workspace_bytes(0, 8) == 0 and tk.tk_backward_workspace_bytes(8, 0) == 0
     v = C.c_uint64()
     assert L.tk_backward_workspace_bytes(4, 8, None) == EINVAL
