@@ -55,12 +55,13 @@ __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
   if (c < a.cols) {
     const uint32_t lines = (uint32_t)a.lines, pitch = (uint32_t)line_pitch(a.cols);
     const float *p = a.partial + (uint64_t)blockIdx.y * lines * pitch + c;
-    float s = lines == 0            ? 0.0f  // no rows, no workspace
-              : lines <= kLines     ? column_sum<kLines, 1>(p, first, lines, pitch)
-              : lines <= 2 * kLines ? column_sum<kLines, 2>(p, first, lines, pitch)
-              : lines <= 4 * kLines ? column_sum<kLines, 4>(p, first, lines, pitch)
-              : lines <= 8 * kLines ? column_sum<kLines, 8>(p, first, lines, pitch)
-                                    : column_sum<kLines, kMost>(p, first, lines, pitch);
+    float s;
+    if (lines == 0) s = 0.0f;  // no rows, no workspace
+    else if (lines <= kLines) s = column_sum<kLines, 1>(p, first, lines, pitch);
+    else if (lines <= 2 * kLines) s = column_sum<kLines, 2>(p, first, lines, pitch);
+    else if (lines <= 4 * kLines) s = column_sum<kLines, 4>(p, first, lines, pitch);
+    else if (kMost > 8 && lines <= 8 * kLines) s = column_sum<kLines, 8>(p, first, lines, pitch);
+    else s = column_sum<kLines, kMost>(p, first, lines, pitch);
     if (kCols == 32) s += __shfl_xor(s, 32);
     part[threadIdx.x >> 6][i] = s;
   }
@@ -88,8 +89,9 @@ constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through
 constexpr uint64_t kAloneSets = 2;
 
 // Partial sums of this many floats or more (of one gradient) are written past the caches: the
-// second kernel starts when they are out of the L2s (256x8192 11.9 us, through them 12.5;
-// 1000x4096 12.6 and 13.5).  Fewer are read from there (100x4096 9.1 us, past them 9.4).
+// second kernel starts when they are out of the L2s (layer norm backward bf16 300x8192 12.2 us,
+// through them 12.9; 1000x4096 12.6 and 13.5).  Fewer are read from there (8000x2048 22.0 us,
+// past them 22.6).
 constexpr uint64_t kPastFloats = 9 << 16;
 
 // Strips of columns by sets of rows: one work-group of 16 waves a compute unit, or fewer that
@@ -104,6 +106,7 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
   const uint64_t at_once = 16 * 64 / p.lanes, most = (rows + at_once - 1) / at_once;
   p.lines = most <= kAloneSets ? 1 : p.strips < kMaxLines ? kMaxLines / p.strips : 1;
   if (p.lines > most) p.lines = most;
+  p.room = p.lines;
   return p;
 }
 
@@ -120,15 +123,18 @@ static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
   p.waves = 16 / p.row_waves * p.row_waves;
   const uint64_t per = p.lanes < 64 ? 64 * p.waves / p.lanes : p.waves / p.row_waves, sets = (rows + per - 1) / per;
   // What a set reads and what its line costs to write and read are alike: wide rows go several
-  // sets to a work-group (256x8192 with 256, 128 and 64 lines: 16.4, 13.0 and 12.4 us).
+  // sets to a work-group (256x8192 with 256, 128 and 64 lines: 17.9, 13.0 and 12.4 us).
   uint64_t least = sets <= kAloneSets ? sets : 1;
   while (sets > kAloneSets && least < 4 && sets * cols >= (least * least) << 19) least *= 2;
   p.lines = (sets + least - 1) / least;
   if (p.lines > kMaxLines) p.lines = kMaxLines;
+  p.room = sets < kMaxLines ? sets : kMaxLines;
   return p;
 }
 
-static uint64_t bytes_of(const BwdPlan &p, uint64_t cols) { return p.lines > 1 ? 12 * p.lines * line_pitch(cols) : 0; }
+// Room for at least the plan's lines, and never less for more rows: a caller with batches of many
+// sizes keeps what the largest needs.
+static uint64_t bytes_of(const BwdPlan &p, uint64_t cols) { return p.lines > 1 ? 12 * p.room * line_pitch(cols) : 0; }
 
 // The larger of both chunk sizes and both kinds of call, so that one size serves every type.
 static uint64_t workspace_bytes(uint64_t rows, uint64_t cols) {

@@ -61,10 +61,11 @@ constexpr uint64_t line_pitch(uint64_t cols) { return (cols + 31) & ~31ull; }
 
 // How a backward call is cut: `lines` lines of partial sums.  Rows in registers (strips 0):
 // `lanes` lanes to a row (64: row_waves whole waves), `waves` waves to a work-group.  Wide rows
-// and dropout-add: `strips` strips of `lanes` lanes' columns.
+// and dropout-add: `strips` strips of `lanes` lanes' columns.  `room`: lines that the workspace
+// holds.
 struct BwdPlan {
   int lanes, waves, row_waves;
-  uint64_t lines, strips;
+  uint64_t lines, strips, room;
 };
 
 struct RowTable {

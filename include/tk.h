@@ -213,8 +213,9 @@ tk_status tk_dropout_backward_f32(uint32_t key, uint64_t start_draw, uint64_t n,
  *          norms at more than 8192 columns, need device memory of at least the size that
  *          tk_backward_workspace_bytes names (64-bit count in *bytes; TK_ERANGE as above),
  *          4-byte aligned, else TK_EINVAL (a size of 0: none is needed, as where one work-group
- *          takes all rows).  It holds nothing between calls; calls that may overlap in time
- *          (other streams, graphs replayed together) need one each.
+ *          takes all rows).  The size never falls as rows grow, so one for the most rows serves
+ *          all.  It holds nothing between calls; calls that may overlap in time (other streams,
+ *          graphs replayed together) need one each.
  * NaN and infinity follow the formulas; a dropped element is +0.0 whatever it was.  Column
  * sums are taken in a fixed order: equal arguments give equal bits, run after run.          */
 #define TK_RESIDUAL_F32 1u

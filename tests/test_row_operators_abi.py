@@ -150,6 +150,14 @@ def test_workspace(t):
     assert L.tk_backward_workspace_bytes(8, 1 << 31, C.byref(v)) == ERANGE
 
 
+@pytest.mark.parametrize("cols", [1, 5, 8, 40, 64, 129, 300, 513, 1024, 1500, 2049, 4096, 5001, 8192, 8193, 20000, 70001,
+                                  140000])
+def test_a_workspace_serves_fewer_rows(cols):
+    rows = list(range(1, 1500)) + list(range(1500, 80000, 997)) + [1 << 20, (1 << 20) + 1, 1 << 30]
+    sizes = [tk.tk_backward_workspace_bytes(r, cols) for r in rows]
+    assert sizes == sorted(sizes)
+
+
 def test_binding_refuses_bad_tensors():
     x = torch.zeros(4, 8)
     with pytest.raises(ValueError, match="HIP device"):
