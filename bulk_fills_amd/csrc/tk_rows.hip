@@ -176,7 +176,7 @@ static bool clash(const Region &a, const Region &b) {
 
 enum RowType { kF32, kF16, kBF16 };
 
-struct Checker {
+struct Arguments {
   RowType type;
   uint64_t rows, cols;
   uint32_t flags;
@@ -325,7 +325,7 @@ static tk_status dropout_add(RowType t, uint32_t key, uint64_t start, uint64_t r
                              uint64_t ldy, hipStream_t stream) {
   tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
   if (st != TK_OK || rows == 0 || cols == 0) return st;
-  Checker c{t, rows, cols, flags};
+  Arguments c{t, rows, cols, flags};
   c.matrix(x, ldx, c.t(), false, true);
   c.vector(bias, cols, c.par(), false, false);
   c.matrix(residual, ldr, c.res(), false, false);
@@ -345,7 +345,7 @@ static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, u
                                       void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
   tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
   if (st != TK_OK || cols == 0) return st;
-  Checker c{t, rows, cols, flags};
+  Arguments c{t, rows, cols, flags};
   if (rows == 0) {
     c.vector(dbias, cols, c.par(), true, false);
     if ((st = c.done()) != TK_OK || !dbias) return st;
@@ -392,7 +392,7 @@ static tk_status norm_forward(RowType t, bool fused, uint32_t key, uint64_t star
                               uint64_t ldy, float *mean, float *rstd, hipStream_t stream) {
   tk_status st = check_scalars(start, rows, cols, p, eps, flags);
   if (st != TK_OK || rows == 0 || cols == 0) return st;
-  Checker c{t, rows, cols, flags};
+  Arguments c{t, rows, cols, flags};
   if (fused) c.matrix(x, ldx, c.t(), false, true);
   c.vector(bias, cols, c.par(), false, false);
   c.matrix(residual, ldr, c.res(), false, !fused);
@@ -421,7 +421,7 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
                                void *dbias, void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
   tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
   if (st != TK_OK || cols == 0) return st;
-  Checker c{t, rows, cols, flags};
+  Arguments c{t, rows, cols, flags};
   const bool sums = dgamma || dbeta || dbias;
   if (rows == 0) {
     c.vector(dgamma, cols, c.par(), true, false);
