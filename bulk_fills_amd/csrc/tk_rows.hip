@@ -14,6 +14,10 @@ namespace tk {
 // A plan's lines, one to a work-group: at most one work-group to a compute unit.
 constexpr uint64_t kMaxLines = 256;
 
+// Up to this many lines four waves of k_finish add up, more sixteen (fused backward bf16
+// 512x24576, of 5 lines, 31.4 us, with sixteen waves 32.7; layer norm's 40x32768 11.8 and 13.0).
+constexpr uint64_t kFewLines = 16;
+
 struct FinishArgs {
   const float *partial;
   void *out[3];  // null: not wanted
@@ -24,7 +28,7 @@ struct FinishArgs {
 
 // A work-group takes kCols columns, a wave 64 / kCols lines of them at a time: 64, or 32 up to
 // 4096 columns, where work-groups are few (layer norm backward bf16 1000x2048: 11.1 us, with 64
-// columns 11.5; 300x12000: 15.1 and 14.2).
+// columns 11.5; 300x12000 with sixteen waves 15.1 and 14.2).
 //
 // The sum of every kLines-th of a column's lines from the first one, at most kSteps of them.  All
 // are read at once, beyond the last line that line again: a loop over the lines waits for loads
@@ -45,10 +49,11 @@ __device__ __forceinline__ float column_sum(const float *p, uint32_t first, uint
   return s;
 }
 
-template <int kCols>
-__global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
-  constexpr uint32_t kLines = 1024 / kCols, kMost = kMaxLines / kLines;
-  __shared__ float part[16][kCols];
+template <int kCols, int kWaves>
+__global__ __launch_bounds__(64 * kWaves) void k_finish(FinishArgs a) {
+  constexpr uint32_t kLines = 64 * kWaves / kCols;
+  constexpr int kMost = (kWaves == 16 ? kMaxLines : kFewLines) / kLines;
+  __shared__ float part[kWaves][kCols];
   void *out = a.out[blockIdx.y];
   if (!out) return;
   const uint32_t i = threadIdx.x % kCols, first = threadIdx.x / kCols, c = a.col0 + blockIdx.x * kCols + i;
@@ -59,9 +64,9 @@ __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
     if (lines == 0) s = 0.0f;  // no rows, no workspace
     else if (lines <= kLines) s = column_sum<kLines, 1>(p, first, lines, pitch);
     else if (lines <= 2 * kLines) s = column_sum<kLines, 2>(p, first, lines, pitch);
-    else if (lines <= 4 * kLines) s = column_sum<kLines, 4>(p, first, lines, pitch);
-    else if (kMost > 8 && lines <= 8 * kLines) s = column_sum<kLines, 8>(p, first, lines, pitch);
-    else s = column_sum<kLines, kMost>(p, first, lines, pitch);
+    else if (kMost == 4 || lines <= 4 * kLines) s = column_sum<kLines, 4>(p, first, lines, pitch);
+    else if (kMost == 8 || lines <= 8 * kLines) s = column_sum<kLines, 8>(p, first, lines, pitch);
+    else s = column_sum<kLines, 16>(p, first, lines, pitch);
     if (kCols == 32) s += __shfl_xor(s, 32);
     part[threadIdx.x >> 6][i] = s;
   }
@@ -69,7 +74,7 @@ __global__ __launch_bounds__(1024) void k_finish(FinishArgs a) {
   if (threadIdx.x < kCols && c < a.cols) {
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += part[w][i];
+    for (int w = 0; w < kWaves; ++w) s += part[w][i];
     if (a.kind == 0) ((float *)out)[c] = s;
     else if (a.kind == 1) ((_Float16 *)out)[c] = (_Float16)s;
     else ((__bf16 *)out)[c] = (__bf16)s;
@@ -252,14 +257,15 @@ static bool params_f32(RowType t, uint32_t flags) { return t == kF32 || (flags &
 static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
                         void *c, hipStream_t stream) {
   FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, 0, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
-  const uint64_t wide = cols > 4096 ? 64 : 32;
+  const uint64_t wide = lines <= kFewLines || cols > 4096 ? 64 : 32;
   const uint64_t most = 1ull << 26;  // columns of a launch, which holds fewer than 2^32 threads
   for (uint64_t k = 0; k < cols; k += most) {
     f.col0 = (uint32_t)k;
     const uint64_t n = cols - k < most ? cols - k : most;
     const dim3 grid((uint32_t)((n + wide - 1) / wide), c ? 3 : b ? 2 : 1);
-    if (wide == 64) hipLaunchKernelGGL(k_finish<64>, grid, dim3(1024), 0, stream, f);
-    else hipLaunchKernelGGL(k_finish<32>, grid, dim3(1024), 0, stream, f);
+    if (lines <= kFewLines) hipLaunchKernelGGL((k_finish<64, 4>), grid, dim3(256), 0, stream, f);
+    else if (wide == 64) hipLaunchKernelGGL((k_finish<64, 16>), grid, dim3(1024), 0, stream, f);
+    else hipLaunchKernelGGL((k_finish<32, 16>), grid, dim3(1024), 0, stream, f);
   }
   return launch_status();
 }
