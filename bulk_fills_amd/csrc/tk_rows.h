@@ -178,9 +178,9 @@ __device__ __forceinline__ float groups_sum(float x) {
   return x;
 }
 
-// How a work-group's threads take rows: kLanes (8, 16 or 32) lanes to a row, or with kLanes =
-// 64 as many whole waves (1 to 16) as the row needs, `waves`.  Whole waves keep the row and
-// its addresses on the scalar unit.
+// How a work-group's threads take rows: kLanes (8, 16 or 32) lanes to a row, two waves (128,
+// forward), or with kLanes = 64 as many whole waves (1 to 16) as the row needs, `waves`.  Whole
+// waves keep the row and its addresses on the scalar unit.
 template <int kLanes>
 struct Team {
   uint32_t group, t, threads, groups;  // this thread's row group and place in it; a group's threads; groups
@@ -190,6 +190,7 @@ struct Team {
       t = threadIdx.x % kLanes;
       threads = kLanes;
     } else {
+      if (kLanes == 128) waves = 2;
       group = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / waves;
       threads = waves * 64;
       t = threadIdx.x - group * threads;
@@ -214,6 +215,24 @@ __device__ __forceinline__ void row_sums(float (&x)[kN], float (*slot)[kN], uint
 #pragma unroll
     for (int k = 0; k < kN; ++k) x[k] = lanes_sum<16>(lane < waves ? slot[group * waves + lane][k] : 0.0f);
   }
+}
+
+// The forward kernels' sum over a row, like row_sums.  kLanes = 128: `other` gets the sum over the
+// work-group's other row (elsewhere 0).
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float x, float *slot, uint32_t group, uint32_t waves, float &other) {
+  other = 0.0f;
+  x = lanes_sum<kLanes < 64 ? kLanes : 64>(x);
+  if (kLanes < 64 || (kLanes == 64 && waves == 1)) return x;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = x;
+  __syncthreads();
+  if (kLanes == 128) {
+    const float y = lanes_sum<2>(slot[(group * 2 + (threadIdx.x & 3)) & 3]);  // lanes 0 and 1 this row's, 2 and 3 the other's
+    other = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(y), 2));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(y), 0));
+  }
+  const uint32_t lane = threadIdx.x & 15;
+  return lanes_sum<16>(lane < waves ? slot[group * waves + lane] : 0.0f);
 }
 
 // ---- forward ---------------------------------------------------------------------------
@@ -266,13 +285,38 @@ __device__ __forceinline__ float rsqrt_any(float x) {
   return x < 0x1p-96f ? __builtin_amdgcn_rsqf(x * 0x1p96f) * 0x1p48f : __builtin_amdgcn_rsqf(x);
 }
 
+// Whether a row's mean is more than four standard deviations from zero.  It is corrected then: the
+// sum's rounding makes it some units of its last place wrong, no small part of a distance from it
+// (rows of 10000.1 in f32: h = -0.3 to -0.8 where it is 0), but the distances themselves are
+// nearly exact, and their own mean is what it is off by.  Nearer to zero their sum is no more exact
+// than the first one (layer norm bf16 16384x8192, float stream, mean 0: the mean's relative error
+// is 1.1e-7, corrected 7.6e-7).  Only such rows pay for one sum more: with the sum of the distances
+// in every row, layer norm bf16 16384x4096, which is bound by its instructions, took 51 us for 46.
+// Never true of sums beyond f32 or NaN; where it is true, all that follows is finite.
+__device__ __forceinline__ bool far_from_zero(float mean, float m2, float inv) { return mean * mean > m2 * inv * 16.0f; }
+
+// A sum over the columns divided by them, rounded once but for rare cases: the product with the
+// rounded reciprocal and one step of Newton's.  An exact quotient comes out exact, so that the
+// distances of a constant row end as zeros.
+__device__ __forceinline__ float mean_of(float sum, uint32_t n, float inv) {
+  __asm__ volatile("" : "+s"(n));  // converted here, not kept in a register between rows
+  const float cols = (float)n, q = sum * inv;
+  return __builtin_fmaf(__builtin_fmaf(-q, cols, sum), inv, q);
+}
+
+// The sum of squared distances to a mean that is `delta` higher: `off` is the distances' own sum.
+// The difference is some squared roundings of the mean (never below 0 but for its own rounding).
+__device__ __forceinline__ float squares_about(float m2, float off, float delta) {
+  return fmaxf(__builtin_fmaf(-off, delta, m2), 0.0f);
+}
+
 // The row stays in registers between the two sums (the mean, then the squared distances from
 // it: no cancellation) and the output: one read and one write of the data.  A work-group takes
 // every gridDim.x-th set of rows, keeps the parameters in registers, and loads its next rows
 // before it works on the present ones.
 template <class T, class R, bool kX, bool kOnce, int CH, int kLanes, int V, bool kKeep>
-__global__ __launch_bounds__(kLanes < 64 ? 256 : 1024) void k_norm_fwd(FwdArgs a) {
-  __shared__ float slot[2][16][1];
+__global__ __launch_bounds__(kLanes == 64 ? 1024 : 256) void k_norm_fwd(FwdArgs a) {
+  __shared__ float slot[3][16];  // one for each sum: a barrier lies between a slot's use and its next
   Team<kLanes> team(a.waves);
   const uint64_t step = (uint64_t)gridDim.x * team.groups;
   uint64_t base = (uint64_t)blockIdx.x * team.groups, row = base + team.group;
@@ -292,22 +336,20 @@ __global__ __launch_bounds__(kLanes < 64 ? 256 : 1024) void k_norm_fwd(FwdArgs a
   // every wave of a work-group runs the same rounds: the sums have barriers
   for (; base < a.rows; base += step, row += step) {
     if (V * CH > 8) __asm__ volatile("" : "+v"(team.t));  // addresses are made anew each round, not kept
-    float v[V][CH], s[1] = {0.0f};
+    float v[V][CH], s = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const uint32_t c = (j * team.threads + team.t) * CH;
       if (kX && !kKeep) load_param<CH, T>(a.bias, a.params_f32, c, a.cols, 0.0f, bias[0]);
       next[j].value(a, row, c, bias[kKeep ? j : 0], v[j]);
 #pragma unroll
-      for (int e = 0; e < CH; ++e) s[0] += v[j][e];
+      for (int e = 0; e < CH; ++e) s += v[j][e];
       if (!kKeep) __builtin_amdgcn_sched_barrier(0);  // one chunk's temporaries at a time
     }
     if (row + step < a.rows)
 #pragma unroll
       for (int j = 0; j < V; ++j) next[j].load(a, row + step, (j * team.threads + team.t) * CH);
-    row_sums<kLanes>(s, slot[0], team.group, a.waves);
-    const float mean = s[0] * inv;
-    float m2[1] = {0.0f};
+    float s_other, m2_other, mean = row_sum<kLanes>(s, slot[0], team.group, a.waves, s_other) * inv, m2 = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const uint32_t c = (j * team.threads + team.t) * CH;
@@ -319,10 +361,28 @@ __global__ __launch_bounds__(kLanes < 64 ? 256 : 1024) void k_norm_fwd(FwdArgs a
 #pragma unroll
         for (int e = 0; e < CH; ++e) v[j][e] = e < nv ? v[j][e] : 0.0f;
 #pragma unroll
-      for (int e = 0; e < CH; ++e) m2[0] = __builtin_fmaf(v[j][e], v[j][e], m2[0]);
+      for (int e = 0; e < CH; ++e) m2 = __builtin_fmaf(v[j][e], v[j][e], m2);
     }
-    row_sums<kLanes>(m2, slot[1], team.group, a.waves);
-    const float rstd = rsqrt_any(__builtin_fmaf(m2[0], inv, a.eps));
+    m2 = row_sum<kLanes>(m2, slot[1], team.group, a.waves, m2_other);
+    // The same bits, so the same answer, in all waves of a row; of two rows in a work-group either's:
+    // its waves meet the barrier below together.
+    const bool far = far_from_zero(mean, m2, inv);
+    if (__any(far || (kLanes == 128 && far_from_zero(s_other * inv, m2_other, inv)))) {
+      float off = 0.0f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int e = 0; e < CH; ++e) off += v[j][e];
+      off = row_sum<kLanes>(off, slot[2], team.group, a.waves, s_other);
+      const float delta = far ? mean_of(off, a.cols, inv) : 0.0f;  // of the wave's other rows: as it was
+      mean = far ? mean + delta : mean;
+      m2 = far ? squares_about(m2, off, delta) : m2;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int e = 0; e < CH; ++e) v[j][e] -= delta;
+    }
+    const float rstd = rsqrt_any(__builtin_fmaf(m2, inv, a.eps));
     if (row < a.rows) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -342,14 +402,14 @@ __global__ __launch_bounds__(kLanes < 64 ? 256 : 1024) void k_norm_fwd(FwdArgs a
   }
 }
 
-// Rows too wide for the registers of one work-group: the same sums over three passes, the
-// inputs read again in each (a row of some hundred KB stays in the caches).  Nothing is
-// written before the third pass, and there each element's inputs are read by the thread
-// that writes it, so outputs in place of inputs are fine.
+// Rows too wide for the registers of one work-group: the same sums over three passes (four far
+// from zero), the inputs read again in each (a row of some hundred KB stays in the caches).
+// Nothing is written before the last pass, and there each element's inputs are read by the
+// thread that writes it, so outputs in place of inputs are fine.
 template <class T, class R, bool kX>
 __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
   constexpr int CH = kChunk<T, R>, kTpr = 1024;
-  __shared__ float slot[2][kTpr / 64][1];
+  __shared__ float slot[3][kTpr / 64];
   const float inv = 1.0f / (float)a.cols;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const auto chunk = [&](uint32_t c, float *v) {
@@ -359,27 +419,37 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
       if (kX) load_param<CH, T>(a.bias, a.params_f32, c, a.cols, 0.0f, bias);
       in.value(a, row, c, bias, v);
     };
-    float v[CH], s[1] = {0.0f};
+    float v[CH], s = 0.0f;
     for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
       chunk(c, v);
       const int nv = (int)(a.cols - c);
 #pragma unroll
-      for (int e = 0; e < CH; ++e) s[0] += e < nv ? v[e] : 0.0f;
+      for (int e = 0; e < CH; ++e) s += e < nv ? v[e] : 0.0f;
     }
-    row_sums<64>(s, slot[0], 0, kTpr / 64);
-    const float mean = s[0] * inv;
-    float m2[1] = {0.0f};
+    float other, mean = row_sum<64>(s, slot[0], 0, kTpr / 64, other) * inv, delta = 0.0f, m2 = 0.0f;
     for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
       chunk(c, v);
       const int nv = (int)(a.cols - c);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         const float d = e < nv ? v[e] - mean : 0.0f;
-        m2[0] = __builtin_fmaf(d, d, m2[0]);
+        m2 = __builtin_fmaf(d, d, m2);
       }
     }
-    row_sums<64>(m2, slot[1], 0, kTpr / 64);
-    const float rstd = rsqrt_any(__builtin_fmaf(m2[0], inv, a.eps));
+    m2 = row_sum<64>(m2, slot[1], 0, kTpr / 64, other);
+    if (__any(far_from_zero(mean, m2, inv))) {  // the same in all waves
+      s = 0.0f;
+      for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
+        chunk(c, v);
+        const int nv = (int)(a.cols - c);
+#pragma unroll
+        for (int e = 0; e < CH; ++e) s += e < nv ? v[e] - mean : 0.0f;
+      }
+      s = row_sum<64>(s, slot[2], 0, kTpr / 64, other);
+      delta = mean_of(s, a.cols, inv);
+      m2 = squares_about(m2, s, delta);
+    }
+    const float rstd = rsqrt_any(__builtin_fmaf(m2, inv, a.eps));
     for (uint32_t c = threadIdx.x * CH; c < a.cols; c += kTpr * CH) {
       float gamma[CH], beta[CH];
       chunk(c, v);
@@ -387,11 +457,11 @@ __global__ __launch_bounds__(1024) void k_norm_fwd_wide(FwdArgs a) {
       load_param<CH, T>(a.beta, a.params_f32, c, a.cols, 0.0f, beta);
       if (a.sum) store_chunk<CH>((R *)a.sum + row * a.lds + c, (int)(a.cols - c), v);
 #pragma unroll
-      for (int e = 0; e < CH; ++e) v[e] -= mean;
+      for (int e = 0; e < CH; ++e) v[e] = v[e] - mean - delta;
       norm_out<T, CH>(a, row, c, rstd, gamma, beta, v);
     }
     if (threadIdx.x == 0) {
-      if (a.mean) a.mean[row] = mean;
+      if (a.mean) a.mean[row] = mean + delta;
       if (a.rstd) a.rstd[row] = rstd;
     }
   }
@@ -759,7 +829,7 @@ static inline uint32_t row_grid(uint64_t sets, uint32_t most) { return (uint32_t
 template <class T, class R, bool kX, bool kOnce, int CH, int kLanes, int V, bool kKeep = true>
 static void launch_fwd(FwdArgs a, hipStream_t s) {
   constexpr uint32_t kCols = kLanes * V * CH;
-  a.waves = kLanes < 64 ? 1 : (a.cols + kCols - 1) / kCols;
+  a.waves = kLanes < 64 ? 1 : kLanes == 128 ? 2 : (a.cols + kCols - 1) / kCols;
   const uint32_t waves = a.waves >= 4 ? a.waves : 4 / a.waves * a.waves;  // of a work-group
   const uint32_t rows = kLanes < 64 ? 64 * waves / kLanes : waves / a.waves;
   const uint32_t each = (V * CH > 8 ? 16 : waves > 8 ? 24 : 20) / waves;  // work-groups of a compute unit
@@ -779,6 +849,7 @@ static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   else if (a.cols <= 64) launch_fwd<T, R, kX, kOnce, CH, 8, K>(a, s);
   else if (a.cols <= 128) launch_fwd<T, R, kX, kOnce, CH, 16, K>(a, s);
   else if (a.cols <= 256) launch_fwd<T, R, kX, kOnce, CH, 32, K>(a, s);
+  else if (a.cols > 512 && a.cols <= 1024) launch_fwd<T, R, kX, kOnce, CH, 128, K>(a, s);
   else if (a.cols <= 6144) launch_fwd<T, R, kX, kOnce, CH, 64, K>(a, s);
   else if (a.cols <= 16384) launch_fwd<T, R, kX, kOnce, CH, 64, 2 * K>(a, s);
   else if (a.cols <= 24576) launch_fwd<T, R, kX, kOnce, CH, 64, 3 * K, false>(a, s);
