@@ -147,3 +147,61 @@ def test_rows_at_the_ends_of_f32(kind, cols):
     assert float(mean[0]) == 2.0 ** 80 and not bool(y[0].any())
     assert abs(float(mean[1]) / 1.1e30 - 1) <= ref.additions(cols) * U and bool(torch.isfinite(y[1]).all())
     assert float(rstd[4]) == 0 and not bool(y[4].any())
+
+
+def is_quotient(got, v, keep, p, what):
+    """`got` (f32) is v over 1 - p where kept, rounded once: off by half a step, and by 2^-20 of that
+    for a quotient that lies within 2^-46 of the middle of two floats; else +0."""
+    want = torch.where(keep > 0, v.double() / ref.quotient(p), 0.0)
+    got = got.detach().cpu()
+    assert not bool(((got.double() - want).abs() > (1 + 2.0 ** -20) * U * want.abs() + 2.0 ** -149).any()), what
+    assert not bool(got[keep == 0].view(torch.int32).any()), what
+
+
+@pytest.mark.parametrize("kind", [k for k in KINDS if k[1] or k[2]], ids=[i for i, k in zip(IDS, KINDS) if k[1] or k[2]])
+@pytest.mark.parametrize("cols", [5, 100, 1000, 5001, 20000, 40000])
+@pytest.mark.parametrize("p", [0.1, 0.3, 0.5, 0.9, 1.0 - 2.0 ** -24, 2.0 ** -25])
+def test_float_outputs_are_quotients(kind, cols, p):
+    """16-bit operators with a float residual stream or float parameters: kept values in float
+    outputs are the quotient by 1 - p, not a product with a rounded reciprocal."""
+    T, R, W = types(kind)
+    log(f"quotients {kind} {cols} {p}")
+    rows = 3
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g).to(T)
+    keep = ref.keep_mask(6, 2, rows, cols, p)
+    e = lambda t: torch.empty(rows, cols, dtype=t, device="cuda")  # noqa: E731
+    if kind[1]:
+        y, s = e(R), e(R)
+        fn("dropout_add", kind)(6, 2, rows, cols, p, flags(kind), x.cuda(), None, None, None, None, y, None)
+        is_quotient(y, x, keep, p, "dropout_add")
+        fn("dropout_add_layer_norm", kind)(6, 2, rows, cols, p, 1e-5, flags(kind), x.cuda(), None, None, None, None, None, None,
+                                           s, None, e(T), None)
+        is_quotient(s, x, keep, p, "dropout_add_layer_norm sum")
+    if kind[2]:  # over one row the bias's gradient is the kept gradient itself
+        dy = torch.randn(1, cols, generator=g).to(R)
+        keep = ref.keep_mask(6, 2, 1, cols, p)
+        db, dx = torch.empty(cols, device="cuda"), torch.empty(1, cols, dtype=T, device="cuda")
+        fn("dropout_add_backward", kind)(6, 2, 1, cols, p, flags(kind), dy.cuda(), None, dx, None, db)
+        is_quotient(db[None], dy, keep, p, "dropout_add_backward dbias")
+        if kind[1]:  # the sum's gradient comes out in float too
+            dt = torch.randn(1, cols, generator=g).to(T).cuda()
+            v, dr = torch.randn(1, cols, generator=g).to(R).cuda(), torch.empty(1, cols, device="cuda")
+            st = torch.ones(1, device="cuda")
+            fn("dropout_add_layer_norm_backward", kind)(6, 2, 1, cols, p, flags(kind), dt, None, dy.cuda(), None, v, None, None,
+                                                        st, st, dx, None, dr, None, None, None, db)
+            is_quotient(db[None], dr.cpu(), keep, p, "dropout_add_layer_norm_backward dbias")
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("p", [0.1, 0.3, 0.5, 0.75])
+def test_kept_infinities_stay(kind, p):
+    """An infinity over 1 - p is that infinity, also where 1 / (1 - p) is a float itself."""
+    T, R, _ = types(kind)
+    cols = 64
+    x = torch.full((2, cols), float("inf"), dtype=T, device="cuda")
+    x[1] = -float("inf")
+    y = torch.empty(2, cols, dtype=R, device="cuda")
+    fn("dropout_add", kind)(6, 0, 2, cols, p, flags(kind), x, None, None, None, None, y, None)
+    keep = ref.keep_mask(6, 0, 2, cols, p).cuda() > 0
+    assert torch.equal(y, torch.where(keep, x.to(R), torch.zeros_like(y)))
