@@ -324,11 +324,13 @@ def _on(stream, dev):
 
 
 def _workspace(where, dev, x, stream, rows, cols, needed):
-    """(address, bytes, what keeps it alive) of a workspace: a tensor, or a pair (address, bytes).
-    None allocates it with torch, in the order of the current stream: for a call on another stream
-    the caller passes one."""
+    """(address, bytes, what keeps it alive) of a workspace: a tensor, a pair (address, bytes), or an
+    address of as many bytes as tk_backward_workspace_bytes names.  None allocates it with torch, in
+    the order of the current stream: for a call on another stream the caller passes one."""
     if isinstance(x, tuple):
         return x[0], x[1], None
+    if isinstance(x, int):
+        return x, tk_backward_workspace_bytes(rows, cols), None
     if x is None:
         n = tk_backward_workspace_bytes(rows, cols) if needed else 0
         if n == 0:
