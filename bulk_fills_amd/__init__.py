@@ -317,10 +317,15 @@ def _vector(where, dev, x, n, dtype):
     _refuse(where, x, dtype, dev, f"a contiguous vector of {n} elements")
 
 
-def _on(stream, dev):
+def _on(where, stream, dev):
+    """The handle of a call's stream: the current device's current one for None."""
     if stream is None:
         return _raw_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device_index != dev:  # the kernels are the current device's, as the buffers are
+        raise ValueError(f"{where}: the stream is cuda:{stream.device_index}'s, the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _workspace(where, dev, x, stream, rows, cols, needed):
@@ -335,7 +340,7 @@ def _workspace(where, dev, x, stream, rows, cols, needed):
         n = tk_backward_workspace_bytes(rows, cols) if needed else 0
         if n == 0:
             return None, 0, None
-        if stream is not None and _on(stream, dev) != _raw_stream(dev):
+        if stream is not None and _on(where, stream, dev) != _raw_stream(dev):
             raise ValueError(f"{where}: a call on a stream that is not the current one needs a workspace")
         x = torch.empty(n, dtype=torch.uint8, device="cuda")
         return x.data_ptr(), n, x
@@ -363,7 +368,7 @@ def _row_operators(suffix, dtype):
         pr, ldr = _matrix(w, dev, residual, ldr, rows, cols, res)
         py, ldy = _matrix(w, dev, y, ldy, rows, cols, res)
         pb = _vector(w, dev, bias, cols, par)
-        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, _on(stream, dev)), w)
+        _check(add_fwd(key, start_draw, rows, cols, p, flags, px, ldx, pb, pr, ldr, py, ldy, _on(w, stream, dev)), w)
 
     def dropout_add_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dx, lddx, dbias, workspace=None, stream=None):
         w, dev = name_dropout_add_backward, _device()
@@ -372,7 +377,7 @@ def _row_operators(suffix, dtype):
         pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, dtype)
         pb = _vector(w, dev, dbias, cols, par)
         ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols, dbias is not None)
-        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, _on(stream, dev)), w)
+        _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, _on(w, stream, dev)), w)
 
     def layer_norm(rows, cols, eps, flags, x, ldx, gamma, beta, y, ldy, mean=None, rstd=None, stream=None):
         w, dev = name_layer_norm, _device()
@@ -381,7 +386,7 @@ def _row_operators(suffix, dtype):
         py, ldy = _matrix(w, dev, y, ldy, rows, cols, dtype)
         pg, pb = _vector(w, dev, gamma, cols, par), _vector(w, dev, beta, cols, par)
         pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
-        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, _on(stream, dev)), w)
+        _check(norm_fwd(rows, cols, eps, flags, px, ldx, pg, pb, py, ldy, pm, ps, _on(w, stream, dev)), w)
 
     def layer_norm_backward(rows, cols, flags, dy, lddy, x, ldx, gamma, mean, rstd, dx, lddx, dgamma, dbeta,
                             workspace=None, stream=None):
@@ -395,7 +400,7 @@ def _row_operators(suffix, dtype):
         ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols,
                                  cols > _SUMS_ALONE or dgamma is not None or dbeta is not None)
         _check(norm_bwd(rows, cols, flags, pdy, lddy, px, ldx, pg, pm, ps, pdx, lddx, pdg, pdb, ws, n,
-                        _on(stream, dev)), w)
+                        _on(w, stream, dev)), w)
 
     def dropout_add_layer_norm(key, start_draw, rows, cols, p, eps, flags, x, ldx, bias, residual, ldr, gamma, beta, sum,
                                lds, y, ldy, mean=None, rstd=None, stream=None):
@@ -408,7 +413,7 @@ def _row_operators(suffix, dtype):
         pb, pg, pt = (_vector(w, dev, v, cols, par) for v in (bias, gamma, beta))
         pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
         _check(both_fwd(key, start_draw, rows, cols, p, eps, flags, px, ldx, pb, pr, ldr, pg, pt, pv, lds, py, ldy, pm, ps,
-                        _on(stream, dev)), w)
+                        _on(w, stream, dev)), w)
 
     def dropout_add_layer_norm_backward(key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, gamma, mean,
                                         rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace=None, stream=None):
@@ -424,7 +429,7 @@ def _row_operators(suffix, dtype):
         ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols, cols > _SUMS_ALONE or dgamma is not None
                                  or dbeta is not None or dbias is not None)
         _check(both_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pds, ldds, pv, lds, pg, pm, ps, pdx, lddx, pdr,
-                        lddr, pdg, pdb, pdt, ws, n, _on(stream, dev)), w)
+                        lddr, pdg, pdb, pdt, ws, n, _on(w, stream, dev)), w)
 
     out = {}
     for f in (dropout_add, dropout_add_backward, layer_norm, layer_norm_backward, dropout_add_layer_norm,

@@ -24,6 +24,29 @@ def test_a_workspace_may_be_an_address(t):
             assert e.value.code == tk.TK_EINVAL
 
 
+class OtherStream:
+    """A stream of another device than the current one."""
+    device_index, cuda_stream = 7, 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    monkeypatch.setattr(tk, "_device", lambda: 0)
+    s = OtherStream()
+    for t in ("f32", "f16", "bf16"):
+        f = lambda n: getattr(tk, f"tk_{n}_{t}")  # noqa: E731
+        for call in (lambda: f("dropout_add")(1, 0, 4, 8, 0.1, 0, A, None, None, None, None, B, None, s),
+                     lambda: f("dropout_add_backward")(1, 0, 4, 8, 0.1, 0, A, None, B, None, None, None, s),
+                     lambda: f("dropout_add_backward")(1, 0, 4000, 8, 0.1, 0, A, None, B, None, H, None, s),
+                     lambda: f("layer_norm")(4, 8, 1e-5, 0, A, None, None, None, B, None, None, None, s),
+                     lambda: f("layer_norm_backward")(4, 8, 0, A, None, B, None, None, D, E, F, None, None, None, None, s),
+                     lambda: f("dropout_add_layer_norm")(1, 0, 4, 8, 0.1, 1e-5, 0, A, None, None, None, None, None, None, None,
+                                                         None, B, None, None, None, s),
+                     lambda: f("dropout_add_layer_norm_backward")(1, 0, 4, 8, 0.1, 0, A, None, None, None, B, None, None, D, E,
+                                                                  F, None, None, None, None, None, None, None, s)):
+            with pytest.raises(ValueError, match="stream"):
+                call()
+
+
 @pytest.mark.gpu
 def test_an_address_of_a_workspace_serves():
     rows, cols = 3000, 200
