@@ -98,20 +98,15 @@ __device__ __forceinline__ void load_param(const void *p, bool f32, uint32_t c, 
 }
 
 // ---- dropout ---------------------------------------------------------------------------
-// Kept values over 1 - p: the IEEE quotient for float.  For the 16-bit types a product with the
-// reciprocal: rounded to float where only 16-bit outputs come of it, whose own rounding (2^-11,
-// 2^-8) is far above its 2^-23; as two floats where float ones may (a float stream, mean and rstd,
-// the bias's gradient): within 2^-46 of the quotient before the one rounding, so the same float but
-// for a few in 10^7 (with a rounded reciprocal a quarter of all are others).  The second product
-// costs 1 % of a backward with bias, and nothing in the forward.
-enum Quotient { kProduct, kTwoProducts, kDivision };
-
-template <class T, bool kFloatOut>  // T: the activations
-constexpr Quotient kQuotient = std::is_same<T, float>::value ? kDivision : kFloatOut ? kTwoProducts : kProduct;
-
-template <Quotient kQ>
+// Kept values over 1 - p: the IEEE quotient for float, and for the 16-bit types a product with the
+// reciprocal as two floats, rounded once: within 2^-46 of the quotient before that rounding, so the
+// same float but for a few in 10^7 (with the reciprocal rounded to float a quarter of all are
+// others).  Their residual stream, statistics and the bias's gradient may be float, and all
+// calls of one mask are to agree, so every one takes both products: up to 2 % of a
+// backward (dropout-add 8192x4096 without bias 20.9 -> 21.3 us), nothing forward.
+template <bool kDivide>
 __device__ __forceinline__ float over_q(const Drop &d, float v) {
-  return kQ == kDivision ? __fdiv_rn(v, d.q) : kQ == kTwoProducts ? __builtin_fmaf(v, d.rq, v * d.rl) : v * d.r;
+  return kDivide ? __fdiv_rn(v, d.q) : __builtin_fmaf(v, d.rq, v * d.rl);
 }
 
 // The words of a chunk whose first counter c is a multiple of CH share most of the hash's first
@@ -122,13 +117,13 @@ __device__ __forceinline__ float over_q(const Drop &d, float v) {
 constexpr uint32_t kHashMul1 = 0x7FEB352Du, kHashMul2 = 0x846CA68Bu;  // tk_hash32's
 
 // The product does not wait for the hash; the choice comes last.
-template <Quotient kQ>
+template <bool kDivide>
 __device__ __forceinline__ float drop_one(const Drop &d, uint32_t word, float v) {
   const bool keep = (word & 0x7FFFFFu) >= d.threshold;
-  return keep ? over_q<kQ>(d, v) : 0.0f;
+  return keep ? over_q<kDivide>(d, v) : 0.0f;
 }
 
-template <Quotient kQ, int CH>
+template <bool kDivide, int CH>
 __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) {
   if (CH > 1 && (c & (CH - 1)) == 0) {
     uint32_t k = c ^ d.hk;
@@ -144,11 +139,11 @@ __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) 
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
       const uint32_t y = (x[e] ^ (x[e] >> 15)) * kHashMul2;
-      v[e] = drop_one<kQ>(d, y ^ (y >> 16), v[e]);
+      v[e] = drop_one<kDivide>(d, y ^ (y >> 16), v[e]);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < CH; ++e) v[e] = drop_one<kQ>(d, tk_word(d.hk, c + e), v[e]);
+    for (int e = 0; e < CH; ++e) v[e] = drop_one<kDivide>(d, tk_word(d.hk, c + e), v[e]);
   }
 }
 
@@ -268,7 +263,7 @@ struct FwdIn {
       if (a.bias)
 #pragma unroll
         for (int e = 0; e < CH; ++e) v[e] += bias[e];
-      if (a.drop.on) drop_chunk<kQuotient<T, true>, CH>(a.drop, a.drop.start + (uint32_t)row * a.cols + c, v);
+      if (a.drop.on) drop_chunk<std::is_same<T, float>::value, CH>(a.drop, a.drop.start + (uint32_t)row * a.cols + c, v);
       if (a.residual) {
         float u[CH];
         unpack<CH, R>(r, nv, u);
@@ -505,9 +500,8 @@ struct BwdIn {
 #pragma unroll
     for (int e = 0; e < CH; ++e) h[e] = (h[e] - mean) * rstd;
   }
-  // Outputs: dresidual = v + dsum and dx = drop(dresidual), which comes back in v, for
-  // the bias's gradient where there is one (kBias).
-  template <bool kX, bool kBias>
+  // Outputs: dresidual = v + dsum and dx = drop(dresidual), which comes back in v.
+  template <bool kX>
   __device__ __forceinline__ void out(const BwdArgs &a, uint64_t row, uint32_t c, float *v) const {
     const int nv = (int)(a.cols - c);
     if (a.dsum) {
@@ -518,7 +512,7 @@ struct BwdIn {
     }
     if (a.dresidual) store_chunk<CH>((R *)a.dresidual + row * a.lddr + c, nv, v);
     if constexpr (kX) {
-      if (a.drop.on) drop_chunk<kQuotient<T, kBias>, CH>(a.drop, a.drop.start + (uint32_t)row * a.cols + c, v);
+      if (a.drop.on) drop_chunk<std::is_same<T, float>::value, CH>(a.drop, a.drop.start + (uint32_t)row * a.cols + c, v);
       store_chunk<CH>((T *)a.dx + row * a.lddx + c, nv, v);
     }
   }
@@ -620,7 +614,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
         const uint32_t c = (j * team.threads + team.t) * CH;
 #pragma unroll
         for (int e = 0; e < CH; ++e) g[j][e] = norm_grad(g[j][e], h[j][e], rs, ka, kb);
-        in[j].template out<kX, kBias>(a, row, c, g[j]);
+        in[j].template out<kX>(a, row, c, g[j]);
         if constexpr (kBias) {
 #pragma unroll
           for (int e = 0; e < CH; ++e) acc[2][j][e] += g[j][e];
@@ -759,7 +753,7 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
           v[e] = norm_grad(v[e] * w[e], h[e], rstd, ka, kb);
         }
       }
-      in.template out<kX, kBias>(a, row, c, v);
+      in.template out<kX>(a, row, c, v);
       if constexpr (kBias) {
 #pragma unroll
         for (int e = 0; e < CH; ++e) acc[kSums - 1][e] += v[e];
@@ -798,7 +792,7 @@ __device__ __forceinline__ uint32_t row_of(const AddArgs &a, uint32_t n) {
   return a.div_shift < 0 ? n : __umulhi(n, a.div_mul) >> a.div_shift;
 }
 
-template <class TI, class TO, Quotient kQ, bool kOnce, bool kFlat, int CH, class TP>
+template <class TI, class TO, bool kDivide, bool kOnce, bool kFlat, int CH, class TP>
 __global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
   const uint32_t first = blockIdx.x * 256u;
   uint32_t dr = 0, column = 0;  // rows from the work-group's first, chunks from the row's start
@@ -822,7 +816,7 @@ __global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
   if (a.bias)
 #pragma unroll
     for (int e = 0; e < CH; ++e) v[e] += b[e];
-  if (a.drop.on) drop_chunk<kQ, CH>(a.drop, a.drop.start + (uint32_t)at(a.cols64, c), v);
+  if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)at(a.cols64, c), v);
   if (a.residual) {
     float t[CH];
     unpack<CH, TO>(d, nv, t);
@@ -925,19 +919,19 @@ static void norm_bwd_of(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
   }
 }
 
-template <class TI, class TO, Quotient kQ, class TP, bool kOnce>
+template <class TI, class TO, bool kDivide, class TP, bool kOnce>
 static void drop_add_as(const AddArgs &a, int chunk, hipStream_t s) {
   const dim3 g((a.chunks + 255) / 256);
-  if (chunk == 1) hipLaunchKernelGGL((k_drop_add<TI, TO, kQ, kOnce, false, 1, TP>), g, dim3(256), 0, s, a);
-  else if (a.flat) hipLaunchKernelGGL((k_drop_add<TI, TO, kQ, kOnce, true, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_drop_add<TI, TO, kQ, kOnce, false, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
+  if (chunk == 1) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, false, 1, TP>), g, dim3(256), 0, s, a);
+  else if (a.flat) hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, true, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((k_drop_add<TI, TO, kDivide, kOnce, false, kChunk<TI, TO>, TP>), g, dim3(256), 0, s, a);
 }
 
 template <class TI, class TO, class TP>
 static void drop_add_of(const AddArgs &a, int chunk, hipStream_t s) {
-  constexpr Quotient kQ = kQuotient<TP, std::is_same<TO, float>::value>;
-  if (a.once) drop_add_as<TI, TO, kQ, TP, true>(a, chunk, s);
-  else drop_add_as<TI, TO, kQ, TP, false>(a, chunk, s);
+  constexpr bool kDivide = std::is_same<TP, float>::value;
+  if (a.once) drop_add_as<TI, TO, kDivide, TP, true>(a, chunk, s);
+  else drop_add_as<TI, TO, kDivide, TP, false>(a, chunk, s);
 }
 
 template <class T, class R>

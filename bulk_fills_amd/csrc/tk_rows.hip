@@ -240,7 +240,7 @@ static Drop drop_of(uint32_t key, uint64_t start, float p) {
   d.threshold = (uint32_t)ceilf(p * 0x1p23f);  // the product is exact
   d.q = 1.0f - p;
   const double r = 1.0 / (double)d.q;
-  d.r = d.rq = (float)r;
+  d.rq = (float)r;
   if (d.rq > r) d.rq = nextafterf(d.rq, 0.0f);
   // never 0 nor below, also where the reciprocal is a float: infinity times both is infinity
   d.rl = fmaxf((float)(r - d.rq), d.rq * 0x1p-48f);

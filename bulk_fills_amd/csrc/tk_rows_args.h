@@ -12,8 +12,8 @@ struct Drop {
   uint32_t hk;         // hash of the key
   uint32_t start;      // counter of element (0, 0)
   uint32_t threshold;  // kept where the word's low 23 bits reach ceil(p 2^23): u >= p, exactly
-  float q, r;          // 1 - p, and its reciprocal rounded to float
-  float rq, rl;        // the reciprocal rounded down, and the rest
+  float q;             // 1 - p
+  float rq, rl;        // its reciprocal rounded down, and the rest
 };
 
 // Forward of the layer norm (x null: its input is `residual`) and of the fused operator.

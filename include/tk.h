@@ -190,10 +190,9 @@ tk_status tk_dropout_backward_f32(uint32_t key, uint64_t start_draw, uint64_t n,
  *                              sum's own rounding)
  *     _backward                dresidual = dsum + dx of the layer norm at `sum`;
  *                              dx = drop(dresidual);  dbias = column sums of dx;  dgamma, dbeta
- * The quotient is the IEEE division in the _f32 operators (as in tk_dropout_f32).  In the
- * 16-bit ones it is a product with 1 / (1 - p): held to 2^-46 where a float output comes of it
- * (float stream or parameters, mean, rstd), so that it is the quotient's float but next to the
- * middle of two, and rounded to float elsewhere, which the 16-bit rounding covers.  p == 0
+ * The quotient is the IEEE division in the _f32 operators (as in tk_dropout_f32).  The 16-bit
+ * ones multiply by 1 / (1 - p), held to 2^-46, and round once to float: the quotient's float
+ * but next to the middle of two.  p == 0
  * keeps every element and takes no draws (no limit on the counters then).
  *   flags: TK_RESIDUAL_F32  the residual stream is float: residual, dropout-add's y and dy,
  *                           sum, dsum, dresidual, and tk_layer_norm's x and dx

@@ -205,3 +205,31 @@ def test_kept_infinities_stay(kind, p):
     fn("dropout_add", kind)(6, 0, 2, cols, p, flags(kind), x, None, None, None, None, y, None)
     keep = ref.keep_mask(6, 0, 2, cols, p).cuda() > 0
     assert torch.equal(y, torch.where(keep, x.to(R), torch.zeros_like(y)))
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("cols", [40, 1000, 8000, 30000])
+def test_calls_of_one_mask_agree(kind, cols):
+    """The fused operator's sum is dropout-add's y bit for bit, and dx does not depend on whether the
+    bias's gradient is wanted, nor on who makes it from the same dresidual."""
+    T, R, W = types(kind)
+    rows, p = 200, 0.3
+    log(f"one mask {kind} {cols}")
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    mat = lambda t: torch.empty(rows, cols, dtype=t, device="cuda").normal_(generator=g)  # noqa: E731
+    x, r, bias = mat(T), mat(R), torch.randn(cols, generator=g, device="cuda").to(W)
+    y, s = torch.empty_like(r), torch.empty_like(r)
+    fn("dropout_add", kind)(6, 2, rows, cols, p, flags(kind), x, None, bias, r, None, y, None)
+    fn("dropout_add_layer_norm", kind)(6, 2, rows, cols, p, 1e-5, flags(kind), x, None, bias, r, None, None, None, s, None,
+                                       torch.empty_like(x), None)
+    assert torch.equal(s, y)
+    dy, st = mat(T), torch.ones(rows, device="cuda")
+    got = []
+    for wanted in (True, False):
+        db = torch.empty(cols, dtype=W, device="cuda") if wanted else None
+        dx, dr, dx2 = torch.empty_like(x), torch.empty_like(r), torch.empty_like(x)
+        fn("dropout_add_layer_norm_backward", kind)(6, 2, rows, cols, p, flags(kind), dy, None, r, None, s, None, None, st, st, dx,
+                                                    None, dr, None, None, None, db)
+        fn("dropout_add_backward", kind)(6, 2, rows, cols, p, flags(kind), r, None, dx2, None, db)
+        got.append((dx, dr, dx2))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
