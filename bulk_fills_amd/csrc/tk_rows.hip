@@ -90,7 +90,9 @@ constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through
 
 // Up to this many sets of rows one work-group (or one to a strip) takes them all and writes the
 // gradients itself (layer norm backward bf16 128x128 5.1 us, with a second kernel 6.4; four sets
-// to a work-group take up to 3 us longer than one with that kernel).
+// to a work-group take up to 3 us longer than one with that kernel).  Calls that want no column sums
+// (`sums` false) have nothing to gain by few work-groups: layer norm backward bf16 2x8192 3.6 us
+// with two and 4.5 with one, 256x8192 4.3 us with 256 and 7.0 with 64.
 constexpr uint64_t kAloneSets = 2;
 
 // Partial sums of this many floats or more (of one gradient) are written past the caches: the
@@ -103,13 +105,13 @@ constexpr uint64_t kPastFloats = 9 << 16;
 // have one row for each of their groups of lanes.  Dropout-add's backward bf16 8192x4096 takes
 // 25.9, 26.8, 28.3 and 28.8 us with 256, 512, 768 and 1024 work-groups, the fused backward
 // 512x24576 31.8, 33.0, 35.2 and 38.2.
-static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
+static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols, bool sums) {
   BwdPlan p{};
   const int ch = cols < (uint64_t)chunk ? 1 : chunk;
   p.lanes = cols <= 8ull * ch ? 8 : cols <= 16ull * ch ? 16 : cols <= 32ull * ch ? 32 : 64;
   p.strips = (cols + p.lanes * ch - 1) / (p.lanes * ch);
   const uint64_t at_once = 16 * 64 / p.lanes, most = (rows + at_once - 1) / at_once;
-  p.lines = most <= kAloneSets ? 1 : p.strips < kMaxLines ? kMaxLines / p.strips : 1;
+  p.lines = sums && most <= kAloneSets ? 1 : p.strips < kMaxLines ? kMaxLines / p.strips : 1;
   if (p.lines > most) p.lines = most;
   p.room = p.lines;
   return p;
@@ -120,8 +122,8 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols) {
 // 68 us with two rows of eight waves to a work-group, 79 with one row and twice the lines).
 // Beyond 8192 columns the column sums do not fit the registers beside a row: two kernels and a
 // second read of dy and sum are faster (4096x16384: 166 against 286 us).
-static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
-  if (cols > kRowsInRegisters) return strips_plan(chunk, rows, cols);
+static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols, bool sums) {
+  if (cols > kRowsInRegisters) return strips_plan(chunk, rows, cols, sums);
   BwdPlan p{};
   p.lanes = cols <= 64 ? 8 : cols <= 128 ? 16 : cols <= 256 ? 32 : 64;
   p.row_waves = p.lanes < 64 ? 1 : (int)((cols + 511) / 512);
@@ -129,8 +131,8 @@ static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols) {
   const uint64_t per = p.lanes < 64 ? 64 * p.waves / p.lanes : p.waves / p.row_waves, sets = (rows + per - 1) / per;
   // What a set reads and what its line costs to write and read are alike: wide rows go several
   // sets to a work-group (256x8192 with 256, 128 and 64 lines: 17.9, 13.0 and 12.4 us).
-  uint64_t least = sets <= kAloneSets ? sets : 1;
-  while (sets > kAloneSets && least < 4 && sets * cols >= (least * least) << 19) least *= 2;
+  uint64_t least = sums && sets <= kAloneSets ? sets : 1;
+  while (sums && sets > kAloneSets && least < 4 && sets * cols >= (least * least) << 19) least *= 2;
   p.lines = (sets + least - 1) / least;
   if (p.lines > kMaxLines) p.lines = kMaxLines;
   p.room = sets < kMaxLines ? sets : kMaxLines;
@@ -146,7 +148,7 @@ static uint64_t workspace_bytes(uint64_t rows, uint64_t cols) {
   if (rows == 0 || cols == 0) return 0;
   uint64_t b = 0;
   for (int chunk = 4; chunk <= 8; chunk += 4) {
-    const uint64_t s = bytes_of(strips_plan(chunk, rows, cols), cols), n = bytes_of(norm_plan(chunk, rows, cols), cols);
+    const uint64_t s = bytes_of(strips_plan(chunk, rows, cols, true), cols), n = bytes_of(norm_plan(chunk, rows, cols, true), cols);
     b = s > b ? s : b;
     b = n > b ? n : b;
   }
@@ -376,7 +378,7 @@ static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, u
     a.once = rows * cols * c.res() > kCachedReads;
     return run_add(k.add_bwd, k.chunk, a, rows, cols, c.res(), c.t(), stream);
   }
-  const BwdPlan plan = strips_plan(k.chunk, rows, cols);
+  const BwdPlan plan = strips_plan(k.chunk, rows, cols, true);
   BwdArgs a{};
   a.dy = dy; a.lddy = lddy; a.dx = dx; a.lddx = lddx;
   a.rows = rows; a.cols = (uint32_t)cols;
@@ -456,7 +458,7 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   if (need) c.vector(workspace, need / 4, 4, true, true);
   if ((st = c.done()) != TK_OK) return st;
   const RowTable k = table_of(t, flags);
-  const BwdPlan plan = norm_plan(k.chunk, rows, cols);
+  const BwdPlan plan = norm_plan(k.chunk, rows, cols, sums);
   BwdArgs a{};
   a.dy = dy; a.lddy = lddy; a.dsum = dsum; a.ldds = ldds; a.sum = sum; a.lds = lds;
   a.gamma = gamma; a.mean = mean; a.rstd = rstd;

@@ -3,6 +3,7 @@ can pass, and the operators at further changes of kernel shape."""
 import pytest
 import torch
 
+import bulk_fills_amd as tk
 import row_reference as ref
 import test_row_operators as base
 from gpu_harness import log
@@ -94,3 +95,25 @@ MORE = [(70, 65), (9, 128), (600, 128), (9, 256), (70, 257), (70, 1024), (5, 614
 def test_further_sizes(kind, test, monkeypatch):
     monkeypatch.setattr(base, "SIZES", MORE)
     test(kind)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("rows,cols", [(2, 8192), (5, 2), (40, 512), (64, 128), (200, 8000), (600, 5001), (33, 9000), (50, 66001)])
+def test_gradients_without_column_sums(kind, rows, cols):
+    """Calls that want none of them are cut otherwise and give the rows' gradients bit for bit."""
+    T, R, W = types(kind)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    mat = lambda t: torch.empty(rows, cols, dtype=t, device="cuda").normal_(generator=g)  # noqa: E731
+    dy, ds, x, gamma = mat(T), mat(R), mat(R), torch.randn(cols, generator=g, device="cuda").to(W)
+    mean, rstd = x.float().mean(1), (x.float().var(1, unbiased=False) + 1e-5).rsqrt()
+    ws = torch.empty(max(4, tk.tk_backward_workspace_bytes(rows, cols)), dtype=torch.uint8, device="cuda")
+    got = []
+    for wanted in (True, False):
+        sums = [torch.empty(cols, dtype=W, device="cuda") if wanted else None for _ in range(3)]
+        d = [torch.full((rows, cols), FILL, dtype=t, device="cuda") for t in (R, T, R)]
+        fn("layer_norm_backward", kind)(rows, cols, flags(kind), dy, None, x, None, gamma, mean, rstd, d[0], None, sums[0], sums[1],
+                                        ws)
+        fn("dropout_add_layer_norm_backward", kind)(8, 3, rows, cols, 0.25, flags(kind), dy, None, ds, None, x, None, gamma, mean,
+                                                    rstd, d[1], None, d[2], None, *sums, ws)
+        got.append(d)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
