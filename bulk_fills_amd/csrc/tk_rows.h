@@ -834,14 +834,17 @@ static inline uint32_t row_grid(uint64_t sets, uint32_t most) { return (uint32_t
 // unit with eight elements a lane (80 registers), 24 where that makes two work-groups of one,
 // and 16 with more elements (128 registers).  Layer norm bf16 32768x2048 takes 61, 49, 46, 45,
 // 48 and 55 us with 8, 12, 16, 20, 24 and 32 waves, and 71 us with a work-group for each row
-// and no prefetch; the fused forward 8192x4096 49 to 53, and 62.
+// and no prefetch; the fused forward 8192x4096 49 to 53, and 62.  The fused forward with a float
+// stream has 84 registers, five waves to a SIMD: it stays at 20 waves (bf16 512x6144 9.6 us, with
+// two work-groups of twelve, half of which wait, 12.7; 8192x6144 102 and 106).
 template <class T, class R, bool kX, bool kOnce, int CH, int kLanes, int V, bool kKeep = true>
 static void launch_fwd(FwdArgs a, hipStream_t s) {
   constexpr uint32_t kCols = kLanes * V * CH;
   a.waves = kLanes < 64 ? 1 : kLanes == 128 ? 2 : (a.cols + kCols - 1) / kCols;
   const uint32_t waves = a.waves >= 4 ? a.waves : 4 / a.waves * a.waves;  // of a work-group
   const uint32_t rows = kLanes < 64 ? 64 * waves / kLanes : waves / a.waves;
-  const uint32_t each = (V * CH > 8 ? 16 : waves > 8 ? 24 : 20) / waves;  // work-groups of a compute unit
+  constexpr bool kMixed = kX && !std::is_same<T, R>::value;
+  const uint32_t each = (V * CH > 8 ? 16 : waves > 8 && !kMixed ? 24 : 20) / waves;  // work-groups of a compute unit
   hipLaunchKernelGGL((k_norm_fwd<T, R, kX, kOnce, CH, kLanes, V, kKeep>),
                      dim3(row_grid((a.rows + rows - 1) / rows, 256 * (each ? each : 1))), dim3(64 * waves), 0, s, a);
 }
@@ -850,7 +853,10 @@ static void launch_fwd(FwdArgs a, hipStream_t s) {
 // a lane takes sixteen, so that two rows share a compute unit (layer norm bf16 8192x8192 45.5
 // against 53 us), and beyond sixteen waves of those 24 or 32, with the parameters read again for
 // every row (fused forward bf16 1024x32768 59 us, in three passes 118; 655x20000 27 us with 24,
-// 31 with 32; 4096x12288 71 us with sixteen and the parameters kept, 81 with 24).
+// 31 with 32; 4096x12288 71 us with sixteen and the parameters kept, 81 with 24).  The fused
+// kernels with 32 elements a lane spill in f32 (50 registers) and with a float stream (26), and are
+// faster all the same: f32 1024x32768 146 us, in three passes 172; bf16 with a float
+// stream 102 and 147, 8x24577 16.9 and 20.2.
 template <class T, class R, bool kX, bool kOnce>
 static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   constexpr int CH = kChunk<T, R>, K = 8 / CH;
