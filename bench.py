@@ -16,6 +16,10 @@ ceiling (the library's constant fill, which has the fills' store path and no gen
 and hipMemsetAsync, at each output size); per-start rows; the roofline of the dominant
 kernel (algorithmic bytes per launch over its HIP-event-timed average duration); and the
 CPU oracle timed on this host's cores over the same step.
+
+The one line on standard output holds the step, its roofline, the baseline and every fill's rate;
+the rows' details are a line of JSON on standard error before it ("bench: details {...}"), so that
+a reader who keeps the end of the output has the whole line.
 """
 import argparse
 import json
@@ -635,6 +639,20 @@ def rate(nbytes, ms):
     return nbytes / (ms / 1e3) / GIB
 
 
+DETAILS = ("protocol", "store_ceiling", "fills", "per_start", "store_pattern", "next_rows", "device")
+
+
+def split_record(rec):
+    """The record as the line for standard output, of under 2000 characters, and the rows' details."""
+    line = {k: v for k, v in rec.items() if k not in DETAILS}
+    details = {k: rec[k] for k in DETAILS}
+    line["fills_GiB_per_s"] = {k: v["GiB_per_s"] for k, v in rec["fills"].items()}
+    if rec["cpu_baseline"] is not None:
+        line["cpu_baseline"] = {k: v for k, v in rec["cpu_baseline"].items() if k != "per_fill"}
+        details["cpu_baseline_per_fill"] = rec["cpu_baseline"].get("per_fill")
+    return line, details
+
+
 def main():
     args = parse()
     if args.trace_summary:
@@ -809,7 +827,9 @@ def main():
         "next_rows": nxt,
         "device": dict(device_info(), clocks_during_fill_rows=clocks.result),
     }
-    print(json.dumps(rec), flush=True)
+    line, details = split_record(rec)
+    progress("details " + json.dumps(details))
+    print(json.dumps(line), flush=True)
     del keep
 
 
