@@ -3,7 +3,8 @@
 // tk_rows_{f32,f16,bf16}.hip and, with a float residual stream, tk_rows_{f16,bf16}_r32.hip; the
 // C entry points are in tk_rows.hip.
 //
-// All of them are bound by memory: 4 to 16 bytes an element for 15 to 40 vector instructions.
+// All of them are bound by memory, and are not far from being bound by their instructions: 4 to 20
+// bytes an element for 15 to 40 vector instructions.
 // Bytes that must move over the time that was measured, on MI355X (streams of this size reach
 // 6.5 TB/s): dropout-add bf16 8192x4096 6.2 TB/s, its backward 5.5; layer norm bf16 16384x8192
 // with a float stream 6.2, its backward 16384x4096 5.5; fused forward bf16 16384x8192 5.9, fused
@@ -551,7 +552,9 @@ __device__ __forceinline__ void put_sums(float *p, int nv, const float *v, bool 
 // Rows in registers, as forward: as loaded, between the sums and the output.  A work-group
 // takes every gridDim.x-th set of rows and keeps the column sums of its own rows in registers;
 // at the end its groups' sums are added up through LDS and written to the workspace, one line
-// of partial sums per work-group, which k_finish adds up in order.
+// of partial sums per work-group, which k_finish adds up in order.  Sixteen waves have 128
+// registers; with three sums, the f32 kernels and those of whole waves with a float stream spill 2
+// (9 with 32 lanes to a row), 12 to 16 bytes a lane.
 template <class T, class R, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
 __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
   constexpr int kSums = kBias ? 3 : 2;

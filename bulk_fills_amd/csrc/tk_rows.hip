@@ -121,7 +121,7 @@ static BwdPlan strips_plan(int chunk, uint64_t rows, uint64_t cols, bool sums) {
 // it has waves for, so that there are few lines of partial sums (fused backward bf16 8192x4096:
 // 68 us with two rows of eight waves to a work-group, 79 with one row and twice the lines).
 // Beyond 8192 columns the column sums do not fit the registers beside a row: two kernels and a
-// second read of dy and sum are faster (4096x16384: 166 against 286 us).
+// second read of dy and sum are faster (fused backward bf16 4096x16384: 160 against 286 us).
 static BwdPlan norm_plan(int chunk, uint64_t rows, uint64_t cols, bool sums) {
   if (cols > kRowsInRegisters) return strips_plan(chunk, rows, cols, sums);
   BwdPlan p{};
@@ -215,7 +215,7 @@ struct Arguments {
     if (!ok) return TK_EINVAL;
     if (!range) return TK_ERANGE;
     for (int i = 0; i < n; ++i) {
-      // a matrix must end within the address space (47 bits on this platform)
+      // a matrix must end below 2^57, above every address of a process: no sum of clash() wraps
       const unsigned __int128 end = (unsigned __int128)r[i].at + (unsigned __int128)(r[i].rows - 1) * r[i].pitch + r[i].width;
       if (end >> 57) return TK_ERANGE;
     }

@@ -36,7 +36,7 @@ struct BwdArgs {
   void *dx, *dresidual;
   float *partial;  // lines of partial column sums: dgamma's, dbeta's, then dbias's
   void *sums[3];   // those gradients (null: not wanted), written by the kernel where `alone`
-  float *stats;    // mean(g), mean(g h) of every row (wide rows)
+  float *stats;    // -rstd mean(g), -rstd mean(g h) of every row (wide rows)
   uint64_t rows, lddy, ldds, lds, lddx, lddr;
   uint32_t cols, waves, strip0;  // strip0: the launch's first strip of columns
   bool alone;                    // one line of sums: they are the gradients
