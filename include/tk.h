@@ -217,6 +217,9 @@ tk_status tk_dropout_backward_f32(uint32_t key, uint64_t start_draw, uint64_t n,
  *          takes all rows).  The size never falls as rows grow, so one for the most rows serves
  *          all.  It holds nothing between calls; calls that may overlap in time (other streams,
  *          graphs replayed together) need one each.
+ * Far from zero: the forward's y holds h to float also where the mean is many times the row's
+ *          spread.  The backward's h is made from the mean as a float, so it is off by up to
+ *          2^-24 |mean| rstd there.
  * NaN and infinity follow the formulas; a dropped element is +0.0 whatever it was.  Column
  * sums are taken in a fixed order: equal arguments give equal bits, run after run.          */
 #define TK_RESIDUAL_F32 1u
