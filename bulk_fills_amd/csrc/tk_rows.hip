@@ -1,9 +1,6 @@
-// tk_rows.hip -- entry points of the row operators: argument checks, how a backward call is
-// cut, and the kernel that adds up the partial column sums.
-#include <math.h>
-
-#include "tk_internal.h"
-#include "tk_rows_args.h"
+// tk_rows.hip -- entry points of the row operators: how a backward call is cut, and the kernel
+// that adds up the partial column sums.
+#include "tk_row_checks.h"
 
 namespace tk {
 
@@ -11,9 +8,6 @@ namespace tk {
 // The end of the column sums: lines of partial sums into element type float or the parameters',
 // in a fixed order
 // ---------------------------------------------------------------------------------------
-// A plan's lines, one to a work-group: at most one work-group to a compute unit.
-constexpr uint64_t kMaxLines = 256;
-
 // Up to this many lines four waves of k_finish add up, more sixteen (fused backward bf16
 // 512x24576, of 5 lines, 31.4 us, with sixteen waves 32.7; layer norm's 40x32768 11.8 and 13.0).
 constexpr uint64_t kFewLines = 16;
@@ -84,7 +78,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_finish(FinishArgs a) {
 // ---------------------------------------------------------------------------------------
 // How a backward call is cut
 // ---------------------------------------------------------------------------------------
-constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 31;
 constexpr uint64_t kRowsInRegisters = 8192;      // columns that k_norm_bwd holds
 constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through the caches (tk_rows.h)
 
@@ -155,99 +148,7 @@ static uint64_t workspace_bytes(uint64_t rows, uint64_t cols) {
   return b + (cols > kRowsInRegisters ? 8 * rows : 0);
 }
 
-// ---------------------------------------------------------------------------------------
-// Argument checks
-// ---------------------------------------------------------------------------------------
-struct Region {
-  uintptr_t at;
-  uint64_t rows, pitch, width;  // bytes
-  int size;                     // element bytes
-  bool out, matrix;
-};
-
-// Whether two arguments share bytes in a way a call may not have: an output matrix may be an
-// input matrix; matrices of one pitch are told apart by their place within it.
-static bool clash(const Region &a, const Region &b) {
-  if (!a.out && !b.out) return false;
-  const uintptr_t ea = a.at + (a.rows - 1) * a.pitch + a.width, eb = b.at + (b.rows - 1) * b.pitch + b.width;
-  if (ea <= b.at || eb <= a.at) return false;
-  if (a.matrix && b.matrix) {
-    if (a.at == b.at && a.size == b.size && (a.pitch == b.pitch || a.rows == 1)) return a.out && b.out;
-    if (a.pitch == b.pitch && a.rows > 1) {
-      const uint64_t d = b.at >= a.at ? (b.at - a.at) % a.pitch : (a.pitch - (a.at - b.at) % a.pitch) % a.pitch;
-      return d < a.width || d + b.width > a.pitch;
-    }
-  }
-  return true;
-}
-
-enum RowType { kF32, kF16, kBF16 };
-
-struct Arguments {
-  RowType type;
-  uint64_t rows, cols;
-  uint32_t flags;
-  Region r[14];
-  int n = 0;
-  bool ok = true, range = true;
-  int t() const { return type == kF32 ? 4 : 2; }
-  int res() const { return flags & TK_RESIDUAL_F32 ? 4 : t(); }
-  int par() const { return flags & TK_PARAMS_F32 ? 4 : t(); }
-  void add(const void *p, uint64_t count, uint64_t ld, uint64_t width, int size, bool out, bool matrix) {
-    if ((uintptr_t)p % size) ok = false;
-    r[n++] = Region{(uintptr_t)p, count, ld * size, width * size, size, out, matrix};
-  }
-  void matrix(const void *p, uint64_t ld, int size, bool out, bool needed) {
-    if (!p) {
-      ok = ok && !needed;
-      return;
-    }
-    if (ld < cols) ok = false;
-    if (ld >= kMaxLd) range = false;
-    else add(p, rows, ld, cols, size, out, true);
-  }
-  void vector(const void *p, uint64_t count, int size, bool out, bool needed) {
-    if (!p) ok = ok && !needed;
-    else add(p, 1, count, count, size, out, false);
-  }
-  // Checks every pair; the caller has added all of a call's arguments.
-  tk_status done() const {
-    if (!ok) return TK_EINVAL;
-    if (!range) return TK_ERANGE;
-    for (int i = 0; i < n; ++i) {
-      // a matrix must end below 2^57, above every address of a process: no sum of clash() wraps
-      const unsigned __int128 end = (unsigned __int128)r[i].at + (unsigned __int128)(r[i].rows - 1) * r[i].pitch + r[i].width;
-      if (end >> 57) return TK_ERANGE;
-    }
-    for (int i = 0; i < n; ++i)
-      for (int j = i + 1; j < n; ++j)
-        if (clash(r[i], r[j])) return TK_EINVAL;
-    return TK_OK;
-  }
-};
-
-static tk_status check_scalars(uint64_t start, uint64_t rows, uint64_t cols, float p, float eps, uint32_t flags) {
-  if (!(p >= 0.0f && p < 1.0f) || !(eps >= 0.0f && eps < INFINITY)) return TK_EINVAL;
-  if (flags & ~(TK_RESIDUAL_F32 | TK_PARAMS_F32)) return TK_EINVAL;
-  if (rows >= kMaxDim || cols >= kMaxDim) return TK_ERANGE;
-  if (p > 0.0f && (start > (1ull << 32) || rows * cols > (1ull << 32) - start)) return TK_ERANGE;
-  return TK_OK;
-}
-
-static Drop drop_of(uint32_t key, uint64_t start, float p) {
-  Drop d{};
-  d.on = p > 0.0f;
-  d.hk = host_lowbias32(key);
-  d.start = (uint32_t)start;
-  d.threshold = (uint32_t)ceilf(p * 0x1p23f);  // the product is exact
-  d.q = 1.0f - p;
-  const double r = 1.0 / (double)d.q;
-  d.rq = (float)r;
-  if (d.rq > r) d.rq = nextafterf(d.rq, 0.0f);
-  // never 0 nor below, also where the reciprocal is a float: infinity times both is infinity
-  d.rl = fmaxf((float)(r - d.rq), d.rq * 0x1p-48f);
-  return d;
-}
+constexpr uint32_t kRowFlags = TK_RESIDUAL_F32 | TK_PARAMS_F32;
 
 static RowTable table_of(RowType t, uint32_t flags) {
   const bool r32 = flags & TK_RESIDUAL_F32;
@@ -258,9 +159,7 @@ static RowTable table_of(RowType t, uint32_t flags) {
   }
 }
 
-static bool params_f32(RowType t, uint32_t flags) { return t == kF32 || (flags & TK_PARAMS_F32); }
-
-static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
+tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_t lines, uint64_t cols, void *a, void *b,
                         void *c, hipStream_t stream) {
   FinishArgs f{partial, {a, b, c}, lines, (uint32_t)cols, 0, params_f32(t, flags) ? 0 : t == kF16 ? 1 : 2};
   const uint64_t wide = lines <= kFewLines || cols > 4096 ? 64 : 32;
@@ -274,11 +173,6 @@ static tk_status finish(RowType t, uint32_t flags, const float *partial, uint64_
     else hipLaunchKernelGGL((k_finish<32, 16>), grid, dim3(1024), 0, stream, f);
   }
   return launch_status();
-}
-
-// Whether a workspace of `have` bytes serves.
-static bool serves(const void *workspace, uint64_t have, uint64_t need) {
-  return need == 0 || (workspace && ((uintptr_t)workspace & 3u) == 0 && have >= need);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -335,7 +229,7 @@ static tk_status run_add(void (*launch)(const AddArgs &, int, hipStream_t), int 
 static tk_status dropout_add(RowType t, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p, uint32_t flags,
                              const void *x, uint64_t ldx, const void *bias, const void *residual, uint64_t ldr, void *y,
                              uint64_t ldy, hipStream_t stream) {
-  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
+  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags, kRowFlags);
   if (st != TK_OK || rows == 0 || cols == 0) return st;
   Arguments c{t, rows, cols, flags};
   c.matrix(x, ldx, c.t(), false, true);
@@ -355,7 +249,7 @@ static tk_status dropout_add(RowType t, uint32_t key, uint64_t start, uint64_t r
 static tk_status dropout_add_backward(RowType t, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p,
                                       uint32_t flags, const void *dy, uint64_t lddy, void *dx, uint64_t lddx, void *dbias,
                                       void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
-  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
+  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags, kRowFlags);
   if (st != TK_OK || cols == 0) return st;
   Arguments c{t, rows, cols, flags};
   if (rows == 0) {
@@ -402,7 +296,7 @@ static tk_status norm_forward(RowType t, bool fused, uint32_t key, uint64_t star
                               float eps, uint32_t flags, const void *x, uint64_t ldx, const void *bias, const void *residual,
                               uint64_t ldr, const void *gamma, const void *beta, void *sum, uint64_t lds, void *y,
                               uint64_t ldy, float *mean, float *rstd, hipStream_t stream) {
-  tk_status st = check_scalars(start, rows, cols, p, eps, flags);
+  tk_status st = check_scalars(start, rows, cols, p, eps, flags, kRowFlags);
   if (st != TK_OK || rows == 0 || cols == 0) return st;
   Arguments c{t, rows, cols, flags};
   if (fused) c.matrix(x, ldx, c.t(), false, true);
@@ -431,7 +325,7 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
                                const void *sum, uint64_t lds, const void *gamma, const float *mean, const float *rstd,
                                void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma, void *dbeta,
                                void *dbias, void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
-  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags);
+  tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags, kRowFlags);
   if (st != TK_OK || cols == 0) return st;
   Arguments c{t, rows, cols, flags};
   const bool sums = dgamma || dbeta || dbias;
