@@ -35,6 +35,7 @@ lib = C.CDLL(LIB_PATH)
 
 TK_OK, TK_EINVAL, TK_ERANGE, TK_ENOMEM, TK_EHIP = 0, 1, 2, 3, 4
 TK_RESIDUAL_F32, TK_PARAMS_F32 = 1, 2  # flags of the row operators
+TK_INDEX_I64, TK_ACCUMULATE, TK_INTERLEAVED = 8, 16, 32  # and of those on tokens and heads
 
 _u32, _u64, _i32, _i64, _f32 = C.c_uint32, C.c_uint64, C.c_int32, C.c_int64, C.c_float
 _p = C.c_void_p
@@ -96,8 +97,23 @@ for _t in ("f32", "f16", "bf16"):
                                             _u64, _p, _u64, _p, _p, _p],
         f"tk_dropout_add_layer_norm_backward_{_t}": [_u32, _u64, _u64, _u64, _f32, _u32, _p, _u64, _p, _u64, _p, _u64, _p,
                                                      _p, _p, _p, _u64, _p, _u64, _p, _p, _p, _p, _u64, _p],
+        f"tk_embedding_{_t}": [_u32, _u64, _u64, _u64, _f32, _f32, _u32, _u64, _p, _p, _u64, _p, _u64, _p],
+        f"tk_embedding_backward_{_t}": [_u32, _u64, _u64, _u64, _f32, _f32, _u32, _u64, _p, _p, _u64, _p, _u64, _p, _u64, _p],
+        f"tk_head_norm_rotate_{_t}": [_u64] * 5 + [_f32, _u32, _p, _u64, _p, _u64, _p, _p, _p, _u64, _p, _p, _p, _u64, _p,
+                                                   _u64, _p],
+        f"tk_head_norm_rotate_backward_{_t}": [_u64] * 5 + [_f32, _u32] + [_p, _u64] * 4 + [_p, _p, _p, _u64, _p, _p]
+        + [_p, _u64] * 2 + [_p, _p, _p, _u64, _p],
+        f"tk_checkpoint_{_t}": [_u32, _u64, _u64, _u64, _u32, _p, _u64, _p, _u64, _p, _p],
+        f"tk_checkpoint_restore_{_t}": [_u64, _u64, _u32, _p, _u64, _p, _p, _u64, _p],
+        f"tk_layer_norm_backward_checkpoint_{_t}": [_u64, _u64, _u32, _p, _u64, _p, _u64, _p, _p, _p, _p, _p, _u64, _p, _p,
+                                                    _p, _u64, _p],
+        f"tk_dropout_add_layer_norm_backward_checkpoint_{_t}": [_u32, _u64, _u64, _u64, _f32, _u32, _p, _u64, _p, _u64, _p,
+                                                                _u64, _p, _p, _p, _p, _p, _u64, _p, _u64, _p, _p, _p, _p,
+                                                                _u64, _p],
     })
 SIGNATURES["tk_backward_workspace_bytes"] = [_u64, _u64, _p]
+SIGNATURES["tk_embedding_workspace_bytes"] = [_u64, _u64, _u64, _p]
+SIGNATURES["tk_head_norm_workspace_bytes"] = [_u64, _u64, _u64, _u64, _p]
 for _name, _args in SIGNATURES.items():
     _fn = getattr(lib, _name)
     _fn.argtypes = _args
@@ -247,6 +263,22 @@ def tk_backward_workspace_bytes(rows, cols):
     return v.value
 
 
+@functools.lru_cache(maxsize=256)
+def tk_embedding_workspace_bytes(rows, cols, vocab):
+    """Device bytes that the embedding's backward calls need."""
+    v = C.c_uint64()
+    _check(lib.tk_embedding_workspace_bytes(rows, cols, vocab, C.byref(v)), "tk_embedding_workspace_bytes")
+    return v.value
+
+
+@functools.lru_cache(maxsize=256)
+def tk_head_norm_workspace_bytes(rows, heads_q, heads_k, dim):
+    """Device bytes that the head norms' backward calls need for their sums."""
+    v = C.c_uint64()
+    _check(lib.tk_head_norm_workspace_bytes(rows, heads_q, heads_k, dim, C.byref(v)), "tk_head_norm_workspace_bytes")
+    return v.value
+
+
 # The current device and its current stream's handle, as torch.cuda.current_device() and
 # torch.cuda.current_stream() give them, without making a Stream object for every call (1.1 of the
 # 8.7 us that one row's layer norm took on the host); by those where torch lacks the names.
@@ -274,6 +306,7 @@ if _get_device is None or _raw_stream is None:
         return torch.cuda.current_stream(dev).cuda_stream
 
 
+_CODE_BLOCK = 128  # columns of a row that share a checkpoint's scale
 _SUMS_ALONE = 8192  # columns up to which a backward call needs its workspace for column sums alone
 
 
@@ -328,16 +361,16 @@ def _on(where, stream, dev):
     return stream.cuda_stream
 
 
-def _workspace(where, dev, x, stream, rows, cols, needed):
+def _workspace(where, dev, x, stream, needed, size, *sizes):
     """(address, bytes, what keeps it alive) of a workspace: a tensor, a pair (address, bytes), or an
-    address of as many bytes as tk_backward_workspace_bytes names.  None allocates it with torch, in
-    the order of the current stream: for a call on another stream the caller passes one."""
+    address of as many bytes as `size` names.  None allocates it with torch, in the order of the
+    current stream: for a call on another stream the caller passes one."""
     if isinstance(x, tuple):
         return x[0], x[1], None
     if isinstance(x, int):
-        return x, tk_backward_workspace_bytes(rows, cols), None
+        return x, size(*sizes), None
     if x is None:
-        n = tk_backward_workspace_bytes(rows, cols) if needed else 0
+        n = size(*sizes) if needed else 0
         if n == 0:
             return None, 0, None
         if stream is not None and _on(where, stream, dev) != _raw_stream(dev):
@@ -376,7 +409,7 @@ def _row_operators(suffix, dtype):
         pdy, lddy = _matrix(w, dev, dy, lddy, rows, cols, res)
         pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, dtype)
         pb = _vector(w, dev, dbias, cols, par)
-        ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols, dbias is not None)
+        ws, n, keep = _workspace(w, dev, workspace, stream, dbias is not None, tk_backward_workspace_bytes, rows, cols)
         _check(add_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pdx, lddx, pb, ws, n, _on(w, stream, dev)), w)
 
     def layer_norm(rows, cols, eps, flags, x, ldx, gamma, beta, y, ldy, mean=None, rstd=None, stream=None):
@@ -397,8 +430,8 @@ def _row_operators(suffix, dtype):
         pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, res)
         pg, pdg, pdb = (_vector(w, dev, v, cols, par) for v in (gamma, dgamma, dbeta))
         pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
-        ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols,
-                                 cols > _SUMS_ALONE or dgamma is not None or dbeta is not None)
+        ws, n, keep = _workspace(w, dev, workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None,
+                                 tk_backward_workspace_bytes, rows, cols)
         _check(norm_bwd(rows, cols, flags, pdy, lddy, px, ldx, pg, pm, ps, pdx, lddx, pdg, pdb, ws, n,
                         _on(w, stream, dev)), w)
 
@@ -426,14 +459,19 @@ def _row_operators(suffix, dtype):
         pdr, lddr = _matrix(w, dev, dresidual, lddr, rows, cols, res)
         pg, pdg, pdb, pdt = (_vector(w, dev, v, cols, par) for v in (gamma, dgamma, dbeta, dbias))
         pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
-        ws, n, keep = _workspace(w, dev, workspace, stream, rows, cols, cols > _SUMS_ALONE or dgamma is not None
-                                 or dbeta is not None or dbias is not None)
+        ws, n, keep = _workspace(w, dev, workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None
+                                 or dbias is not None, tk_backward_workspace_bytes, rows, cols)
         _check(both_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pds, ldds, pv, lds, pg, pm, ps, pdx, lddx, pdr,
                         lddr, pdg, pdb, pdt, ws, n, _on(w, stream, dev)), w)
 
+    return _named(suffix, dropout_add, dropout_add_backward, layer_norm, layer_norm_backward, dropout_add_layer_norm,
+                  dropout_add_layer_norm_backward)
+
+
+def _named(suffix, *functions):
+    """The functions under the names of their C entry points."""
     out = {}
-    for f in (dropout_add, dropout_add_backward, layer_norm, layer_norm_backward, dropout_add_layer_norm,
-              dropout_add_layer_norm_backward):
+    for f in functions:
         f.__name__ = f.__qualname__ = f"tk_{f.__name__}_{suffix}"
         f.__doc__ = (f"{f.__name__}: see include/tk.h.  Matrices are rows x cols tensors (their ld may be None) or raw "
                      "addresses" + (", and a workspace of None is allocated." if "backward" in f.__name__ else "."))
@@ -441,10 +479,138 @@ def _row_operators(suffix, dtype):
     return out
 
 
+def _heads(where, dev, x, ld, rows, heads, dim, dtype):
+    """(address, ld) of a matrix of heads: as _matrix takes it, or a view of rows x heads x dim."""
+    if not (x is None or isinstance(x, int)) and x.dim() == 3 and not x.is_contiguous():
+        if tuple(x.shape) != (rows, heads, dim) or (heads > 1 and x.stride(1) != dim) or (dim > 1 and x.stride(2) != 1):
+            _refuse(where, x, dtype, dev, f"{rows} x {heads} x {dim} with a row's heads one after the other")
+        x = x.as_strided((rows, heads * dim), (x.stride(0), 1))
+    return _matrix(where, dev, x, ld, rows, heads * dim, dtype)
+
+
+def _token_operators(suffix, dtype):
+    """The embedding, the head norms and the checkpoints for one element type, under the names of
+    their C entry points."""
+    emb_fwd, emb_bwd = getattr(lib, "tk_embedding_" + suffix), getattr(lib, "tk_embedding_backward_" + suffix)
+    head_fwd = getattr(lib, "tk_head_norm_rotate_" + suffix)
+    head_bwd = getattr(lib, "tk_head_norm_rotate_backward_" + suffix)
+    pack, unpack = getattr(lib, "tk_checkpoint_" + suffix), getattr(lib, "tk_checkpoint_restore_" + suffix)
+    norm_bwd = getattr(lib, "tk_layer_norm_backward_checkpoint_" + suffix)
+    both_bwd = getattr(lib, "tk_dropout_add_layer_norm_backward_checkpoint_" + suffix)
+    float32, int32, int64, int8 = torch.float32, torch.int32, torch.int64, torch.int8
+    name_embedding, name_embedding_backward = "tk_embedding_" + suffix, "tk_embedding_backward_" + suffix
+    name_head, name_head_backward = "tk_head_norm_rotate_" + suffix, "tk_head_norm_rotate_backward_" + suffix
+    name_checkpoint, name_restore = "tk_checkpoint_" + suffix, "tk_checkpoint_restore_" + suffix
+    name_norm_backward = "tk_layer_norm_backward_checkpoint_" + suffix
+    name_both_backward = "tk_dropout_add_layer_norm_backward_checkpoint_" + suffix
+
+    def embedding(key, start_draw, rows, cols, p, scale, flags, vocab, ids, table, ldt, y, ldy, stream=None):
+        w, dev = name_embedding, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pi = _vector(w, dev, ids, rows, int64 if flags & TK_INDEX_I64 else int32)
+        pt, ldt = _matrix(w, dev, table, ldt, vocab, cols, par)
+        py, ldy = _matrix(w, dev, y, ldy, rows, cols, res)
+        _check(emb_fwd(key, start_draw, rows, cols, p, scale, flags, vocab, pi, pt, ldt, py, ldy, _on(w, stream, dev)), w)
+
+    def embedding_backward(key, start_draw, rows, cols, p, scale, flags, vocab, ids, dy, lddy, dtable, lddt, workspace=None,
+                           stream=None):
+        w, dev = name_embedding_backward, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pi = _vector(w, dev, ids, rows, int64 if flags & TK_INDEX_I64 else int32)
+        pd, lddy = _matrix(w, dev, dy, lddy, rows, cols, res)
+        pt, lddt = _matrix(w, dev, dtable, lddt, vocab, cols, par)
+        ws, n, keep = _workspace(w, dev, workspace, stream, True, tk_embedding_workspace_bytes, rows, cols, vocab)
+        _check(emb_bwd(key, start_draw, rows, cols, p, scale, flags, vocab, pi, pd, lddy, pt, lddt, ws, n,
+                       _on(w, stream, dev)), w)
+
+    def head_norm_rotate(rows, heads_q, heads_k, dim, rotary, eps, flags, q, ldq, k, ldk, gamma_q, gamma_k, positions,
+                         table_rows, cosines, sines, yq, ldyq, yk, ldyk, stream=None):
+        w, dev = name_head, _device()
+        par, turns = float32 if flags & TK_PARAMS_F32 else dtype, table_rows * (rotary // 2)
+        pq, ldq = _heads(w, dev, q, ldq, rows, heads_q, dim, dtype)
+        pk, ldk = _heads(w, dev, k, ldk, rows, heads_k, dim, dtype)
+        pgq, pgk = _vector(w, dev, gamma_q, dim, par), _vector(w, dev, gamma_k, dim, par)
+        pp = _vector(w, dev, positions, rows, int64 if flags & TK_INDEX_I64 else int32)
+        pc, ps = _vector(w, dev, cosines, turns, float32), _vector(w, dev, sines, turns, float32)
+        pyq, ldyq = _heads(w, dev, yq, ldyq, rows, heads_q, dim, dtype)
+        pyk, ldyk = _heads(w, dev, yk, ldyk, rows, heads_k, dim, dtype)
+        _check(head_fwd(rows, heads_q, heads_k, dim, rotary, eps, flags, pq, ldq, pk, ldk, pgq, pgk, pp, table_rows, pc, ps,
+                        pyq, ldyq, pyk, ldyk, _on(w, stream, dev)), w)
+
+    def head_norm_rotate_backward(rows, heads_q, heads_k, dim, rotary, eps, flags, dyq, lddyq, dyk, lddyk, q, ldq, k, ldk,
+                                  gamma_q, gamma_k, positions, table_rows, cosines, sines, dq, lddq, dk, lddk, dgamma_q,
+                                  dgamma_k, workspace=None, stream=None):
+        w, dev = name_head_backward, _device()
+        par, turns = float32 if flags & TK_PARAMS_F32 else dtype, table_rows * (rotary // 2)
+        pdyq, lddyq = _heads(w, dev, dyq, lddyq, rows, heads_q, dim, dtype)
+        pdyk, lddyk = _heads(w, dev, dyk, lddyk, rows, heads_k, dim, dtype)
+        pq, ldq = _heads(w, dev, q, ldq, rows, heads_q, dim, dtype)
+        pk, ldk = _heads(w, dev, k, ldk, rows, heads_k, dim, dtype)
+        pgq, pgk, pdgq, pdgk = (_vector(w, dev, v, dim, par) for v in (gamma_q, gamma_k, dgamma_q, dgamma_k))
+        pp = _vector(w, dev, positions, rows, int64 if flags & TK_INDEX_I64 else int32)
+        pc, ps = _vector(w, dev, cosines, turns, float32), _vector(w, dev, sines, turns, float32)
+        pdq, lddq = _heads(w, dev, dq, lddq, rows, heads_q, dim, dtype)
+        pdk, lddk = _heads(w, dev, dk, lddk, rows, heads_k, dim, dtype)
+        ws, n, keep = _workspace(w, dev, workspace, stream, dgamma_q is not None or dgamma_k is not None,
+                                 tk_head_norm_workspace_bytes, rows, heads_q, heads_k, dim)
+        _check(head_bwd(rows, heads_q, heads_k, dim, rotary, eps, flags, pdyq, lddyq, pdyk, lddyk, pq, ldq, pk, ldk, pgq, pgk,
+                        pp, table_rows, pc, ps, pdq, lddq, pdk, lddk, pdgq, pdgk, ws, n, _on(w, stream, dev)), w)
+
+    def checkpoint(key, start_draw, rows, cols, flags, x, ldx, codes, ldc, scales, stream=None):
+        w, dev = name_checkpoint, _device()
+        px, ldx = _matrix(w, dev, x, ldx, rows, cols, float32 if flags & TK_RESIDUAL_F32 else dtype)
+        pc, ldc = _matrix(w, dev, codes, ldc, rows, cols, int8)
+        ps = _vector(w, dev, scales, rows * -(-cols // _CODE_BLOCK), float32)
+        _check(pack(key, start_draw, rows, cols, flags, px, ldx, pc, ldc, ps, _on(w, stream, dev)), w)
+
+    def checkpoint_restore(rows, cols, flags, codes, ldc, scales, y, ldy, stream=None):
+        w, dev = name_restore, _device()
+        pc, ldc = _matrix(w, dev, codes, ldc, rows, cols, int8)
+        ps = _vector(w, dev, scales, rows * -(-cols // _CODE_BLOCK), float32)
+        py, ldy = _matrix(w, dev, y, ldy, rows, cols, float32 if flags & TK_RESIDUAL_F32 else dtype)
+        _check(unpack(rows, cols, flags, pc, ldc, ps, py, ldy, _on(w, stream, dev)), w)
+
+    def layer_norm_backward_checkpoint(rows, cols, flags, dy, lddy, codes, ldc, scales, gamma, mean, rstd, dx, lddx, dgamma,
+                                       dbeta, workspace=None, stream=None):
+        w, dev = name_norm_backward, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pdy, lddy = _matrix(w, dev, dy, lddy, rows, cols, dtype)
+        pc, ldc = _matrix(w, dev, codes, ldc, rows, cols, int8)
+        pv = _vector(w, dev, scales, rows * -(-cols // _CODE_BLOCK), float32)
+        pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, res)
+        pg, pdg, pdb = (_vector(w, dev, v, cols, par) for v in (gamma, dgamma, dbeta))
+        pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
+        ws, n, keep = _workspace(w, dev, workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None,
+                                 tk_backward_workspace_bytes, rows, cols)
+        _check(norm_bwd(rows, cols, flags, pdy, lddy, pc, ldc, pv, pg, pm, ps, pdx, lddx, pdg, pdb, ws, n,
+                        _on(w, stream, dev)), w)
+
+    def dropout_add_layer_norm_backward_checkpoint(key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, codes, ldc,
+                                                   scales, gamma, mean, rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias,
+                                                   workspace=None, stream=None):
+        w, dev = name_both_backward, _device()
+        res, par = float32 if flags & TK_RESIDUAL_F32 else dtype, float32 if flags & TK_PARAMS_F32 else dtype
+        pdy, lddy = _matrix(w, dev, dy, lddy, rows, cols, dtype)
+        pds, ldds = _matrix(w, dev, dsum, ldds, rows, cols, res)
+        pc, ldc = _matrix(w, dev, codes, ldc, rows, cols, int8)
+        pv = _vector(w, dev, scales, rows * -(-cols // _CODE_BLOCK), float32)
+        pdx, lddx = _matrix(w, dev, dx, lddx, rows, cols, dtype)
+        pdr, lddr = _matrix(w, dev, dresidual, lddr, rows, cols, res)
+        pg, pdg, pdb, pdt = (_vector(w, dev, v, cols, par) for v in (gamma, dgamma, dbeta, dbias))
+        pm, ps = _vector(w, dev, mean, rows, float32), _vector(w, dev, rstd, rows, float32)
+        ws, n, keep = _workspace(w, dev, workspace, stream, cols > _SUMS_ALONE or dgamma is not None or dbeta is not None
+                                 or dbias is not None, tk_backward_workspace_bytes, rows, cols)
+        _check(both_bwd(key, start_draw, rows, cols, p, flags, pdy, lddy, pds, ldds, pc, ldc, pv, pg, pm, ps, pdx, lddx, pdr,
+                        lddr, pdg, pdb, pdt, ws, n, _on(w, stream, dev)), w)
+
+    return _named(suffix, embedding, embedding_backward, head_norm_rotate, head_norm_rotate_backward, checkpoint,
+                  checkpoint_restore, layer_norm_backward_checkpoint, dropout_add_layer_norm_backward_checkpoint)
+
+
 if torch is not None:
-    globals().update(_row_operators("f32", torch.float32))
-    globals().update(_row_operators("f16", torch.float16))
-    globals().update(_row_operators("bf16", torch.bfloat16))
+    for _suffix, _dtype in (("f32", torch.float32), ("f16", torch.float16), ("bf16", torch.bfloat16)):
+        globals().update(_row_operators(_suffix, _dtype))
+        globals().update(_token_operators(_suffix, _dtype))
 
 
 class Alias:

@@ -19,7 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtk.so")
 SOURCES = ["tk_runtime.hip", "tk_fills.hip", "tk_ziggurat.hip", "tk_choice.hip", "tk_rows.hip", "tk_rows_f32.hip",
-           "tk_rows_f16.hip", "tk_rows_f16_r32.hip", "tk_rows_bf16.hip", "tk_rows_bf16_r32.hip"]
+           "tk_rows_f16.hip", "tk_rows_f16_r32.hip", "tk_rows_bf16.hip", "tk_rows_bf16_r32.hip", "tk_embedding.hip",
+           "tk_heads.hip", "tk_checkpoint.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 

@@ -1,0 +1,438 @@
+// tk_heads.hip -- the norm of each query and key head with the position rotation in the same pass,
+// and its gradient.
+#include <type_traits>
+
+#include "tk_row_checks.h"
+#include "tk_rows.h"
+
+namespace tk {
+
+// A side is the queries or the keys: `heads` heads of `dim` elements, one after the other in a row.
+struct Side {
+  const void *x, *dy, *gamma;
+  void *out;  // y, or dx
+  uint64_t ldx, lddy, ldo;
+};
+
+struct HeadArgs {
+  Side side[2];
+  const void *positions;
+  const float *cosines, *sines;
+  float *partial;  // lines of partial sums: dgamma_q's, then dgamma_k's
+  uint64_t rows, table_rows;
+  uint32_t heads_q, heads, dim, half, pair_slots, slots;  // heads: of both sides
+  uint32_t parts;                                         // into which a row's heads are cut
+  float eps;
+  bool i64, params_f32;
+};
+
+// ---- a lane's part of a head ----
+// A lane holds a slot, twice P elements of its head.  The first slots hold pairs: with halves paired,
+// P elements of the first half and their partners, and with neighbours paired 2 P in a row.  The rest
+// of the head, which does not turn, follows in slots of 2 P in a row.  So a pair never leaves its
+// lane, and with a head's width a multiple of 4 P every access is a whole vector.
+struct Slot {
+  uint32_t at1, at2, angle;  // first elements of its two vectors, and the first pair's angle
+  int n1, n2, pairs;         // how many elements count; pairs: 0 in the slots that do not turn
+};
+
+template <int P, bool kNeighbours>
+__device__ __forceinline__ Slot slot_of(const HeadArgs &a, uint32_t s) {
+  const auto upto = [](int n) { return n < 0 ? 0 : n < P ? n : P; };
+  Slot t{};
+  if (s >= a.slots) return t;
+  if (s >= a.pair_slots) {
+    t.at1 = 2 * a.half + (s - a.pair_slots) * 2 * P;
+    t.at2 = t.at1 + P;
+    t.n1 = upto((int)a.dim - (int)t.at1);
+    t.n2 = upto((int)a.dim - (int)t.at2);
+    return t;
+  }
+  t.angle = s * P;
+  t.pairs = upto((int)a.half - (int)t.angle);
+  if (kNeighbours) {
+    t.at1 = 2 * t.angle;
+    t.at2 = t.at1 + P;
+    t.n1 = upto(2 * t.pairs);
+    t.n2 = 2 * t.pairs - t.n1;
+  } else {
+    t.at1 = t.angle;
+    t.at2 = a.half + t.angle;
+    t.n1 = t.n2 = t.pairs;
+  }
+  return t;
+}
+
+// n of P elements as floats, the others 0.  Fewer than P are loaded one by one: a vector would reach
+// into what the call need not own.
+template <int P, class T>
+__device__ __forceinline__ void load_some(const T *p, int n, float *v) {
+  if (n == P) {
+    const Chunk<T, P> t = *(const Chunk<T, P> *)p;
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = (float)t[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = e < n ? (float)p[e] : 0.0f;
+  }
+}
+
+// Both vectors of a slot, at a head's first element.
+template <int P, class T>
+__device__ __forceinline__ void load_slot(const void *head, const Slot &s, float *v) {
+  load_some<P, T>((const T *)head + s.at1, s.n1, v);
+  load_some<P, T>((const T *)head + s.at2, s.n2, v + P);
+}
+
+template <int P, class T>
+__device__ __forceinline__ void store_slot(void *head, const Slot &s, const float *v) {
+  store_chunk<P>((T *)head + s.at1, s.n1, v);
+  store_chunk<P>((T *)head + s.at2, s.n2, v + P);
+}
+
+template <int P, class T>
+__device__ __forceinline__ void load_gamma(const HeadArgs &a, const void *gamma, const Slot &s, float *v) {
+  if (!gamma) {
+#pragma unroll
+    for (int e = 0; e < 2 * P; ++e) v[e] = 1.0f;
+  } else if (a.params_f32) {
+    load_slot<P, float>(gamma, s, v);
+  } else {
+    load_slot<P, T>(gamma, s, v);
+  }
+}
+
+// The angles of a row for a slot.  A row whose position is none of the tables' does not turn.
+template <int P>
+struct Angles {
+  float c[P], s[P];
+  bool turns;
+  __device__ __forceinline__ void load(const HeadArgs &a, uint64_t row, const Slot &t) {
+    uint64_t at = row;
+    if (a.positions)
+      at = a.i64 ? (uint64_t)((const int64_t *)a.positions)[row] : (uint64_t)(int64_t)((const int32_t *)a.positions)[row];
+    turns = t.pairs > 0 && at < a.table_rows;
+    const uint64_t from = turns ? at * a.half + t.angle : 0;
+    const int n = turns ? t.pairs : 0;
+    load_some<P, float>(a.cosines + from, n, c);
+    load_some<P, float>(a.sines + from, n, s);
+  }
+  // v's pairs turned by the angles, or back.
+  template <bool kNeighbours, bool kBack>
+  __device__ __forceinline__ void turn(float *v) const {
+    if (!turns) return;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      float &x = kNeighbours ? v[2 * e] : v[e], &y = kNeighbours ? v[2 * e + 1] : v[P + e];
+      const float sine = kBack ? -s[e] : s[e], u = x;
+      x = __builtin_fmaf(-y, sine, u * c[e]);
+      y = __builtin_fmaf(u, sine, y * c[e]);
+    }
+  }
+};
+
+// ---- kernels ----
+// A wave takes some heads of one row: 64 / kLanes of them at a time, kLanes lanes each, with the
+// row's angles in registers.
+template <class T, int P, int kLanes, bool kNeighbours>
+__global__ __launch_bounds__(256) void k_heads(HeadArgs a) {
+  constexpr uint32_t kGroups = 64 / kLanes;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = (threadIdx.x & 63) / kLanes;
+  const Slot slot = slot_of<P, kNeighbours>(a, threadIdx.x % kLanes);
+  const float inv = 1.0f / (float)a.dim;
+  const uint64_t units = a.rows * a.parts;
+  for (uint64_t unit = blockIdx.x * 4ull + wave; unit < units; unit += gridDim.x * 4ull) {
+    const uint64_t row = unit / a.parts;
+    const uint32_t part = (uint32_t)(unit - row * a.parts);
+    Angles<P> angles;
+    angles.load(a, row, slot);
+    for (uint32_t h = part * kGroups + group; h < a.heads; h += a.parts * kGroups) {
+      const bool key = h >= a.heads_q;
+      const Side &side = a.side[key];
+      const uint32_t at = (key ? h - a.heads_q : h) * a.dim;
+      float v[2 * P], g[2 * P], sum = 0.0f;
+      load_slot<P, T>((const T *)side.x + row * side.ldx + at, slot, v);
+      load_gamma<P, T>(a, side.gamma, slot, g);
+#pragma unroll
+      for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(v[e], v[e], sum);
+      const float rstd = rsqrt_any(__builtin_fmaf(lanes_sum<kLanes>(sum), inv, a.eps));
+#pragma unroll
+      for (int e = 0; e < 2 * P; ++e) v[e] = v[e] * rstd * g[e];
+      angles.template turn<kNeighbours, false>(v);
+      store_slot<P, T>((T *)side.out + row * side.ldo + at, slot, v);
+    }
+  }
+}
+
+// The sum over a wave's lanes that hold the same slot, in all of them.
+template <int kLanes>
+__device__ __forceinline__ float slots_sum(float x) {
+  if (kLanes <= 1) x += dpp<0x121>(x);  // row_ror:1, 2, 4, 8
+  if (kLanes <= 2) x += dpp<0x122>(x);
+  if (kLanes <= 4) x += dpp<0x124>(x);
+  if (kLanes <= 8) x += dpp<0x128>(x);
+  if (kLanes <= 16) x = swap_sum16(x);
+  if (kLanes <= 32) x = swap_sum32(x);
+  return x;
+}
+
+constexpr int kBackWaves = 8;
+
+// The gradient: one pass over x and dy, the statistics made anew.  A wave keeps the sums for both
+// gammas in registers over all its rows; a work-group's go to the workspace as one line each.
+template <class T, int P, int kLanes, bool kNeighbours>
+__global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
+  constexpr uint32_t kGroups = 64 / kLanes;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = (threadIdx.x & 63) / kLanes;
+  const Slot slot = slot_of<P, kNeighbours>(a, threadIdx.x % kLanes);
+  const float inv = 1.0f / (float)a.dim;
+  const uint64_t units = a.rows * a.parts;
+  float acc[2][2 * P];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 2 * P; ++e) acc[k][e] = 0.0f;
+  for (uint64_t unit = blockIdx.x * (uint64_t)kBackWaves + wave; unit < units; unit += gridDim.x * (uint64_t)kBackWaves) {
+    const uint64_t row = unit / a.parts;
+    const uint32_t part = (uint32_t)(unit - row * a.parts);
+    Angles<P> angles;
+    angles.load(a, row, slot);
+    for (uint32_t h = part * kGroups + group; h < a.heads; h += a.parts * kGroups) {
+      const bool key = h >= a.heads_q;
+      const Side &side = a.side[key];
+      const uint32_t at = (key ? h - a.heads_q : h) * a.dim;
+      float x[2 * P], d[2 * P], g[2 * P], s[2] = {0.0f, 0.0f};
+      load_slot<P, T>((const T *)side.x + row * side.ldx + at, slot, x);
+      load_slot<P, T>((const T *)side.dy + row * side.lddy + at, slot, d);
+      load_gamma<P, T>(a, side.gamma, slot, g);
+      angles.template turn<kNeighbours, true>(d);
+#pragma unroll
+      for (int e = 0; e < 2 * P; ++e) s[0] = __builtin_fmaf(x[e], x[e], s[0]);
+      const float rstd = rsqrt_any(__builtin_fmaf(lanes_sum<kLanes>(s[0]), inv, a.eps));
+#pragma unroll
+      for (int e = 0; e < 2 * P; ++e) {
+        x[e] *= rstd;  // h
+        const float t = d[e] * x[e];
+        acc[0][e] += key ? 0.0f : t;
+        acc[1][e] += key ? t : 0.0f;
+        d[e] *= g[e];
+        s[1] = __builtin_fmaf(d[e], x[e], s[1]);
+      }
+      const float m = lanes_sum<kLanes>(s[1]) * inv;
+#pragma unroll
+      for (int e = 0; e < 2 * P; ++e) d[e] = rstd * __builtin_fmaf(-x[e], m, d[e]);
+      store_slot<P, T>((T *)side.out + row * side.ldo + at, slot, d);
+    }
+  }
+  if (!a.partial) return;
+  __shared__ float tile[kBackWaves][kLanes * 2 * P];
+  for (int k = 0; k < 2; ++k) {
+    if (k) __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 2 * P; ++e) {
+      const float v = slots_sum<kLanes>(k ? acc[1][e] : acc[0][e]);
+      if ((threadIdx.x & 63) < kLanes) tile[wave][(threadIdx.x & 63) * 2 * P + e] = v;
+    }
+    __syncthreads();
+    float *line = a.partial + ((uint64_t)k * gridDim.x + blockIdx.x) * line_pitch(a.dim);
+    for (uint32_t i = threadIdx.x; i < kLanes * 2 * P; i += 64 * kBackWaves) {
+      const Slot t = slot_of<P, kNeighbours>(a, i / (2 * P));
+      const int e = (int)(i % (2 * P));
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBackWaves; ++w) v += tile[w][i];
+      if (e < P) {
+        if (e < t.n1) line[t.at1 + e] = v;
+      } else if (e - P < t.n2) {
+        line[t.at2 + e - P] = v;
+      }
+    }
+  }
+}
+
+// ---- launches ----
+constexpr uint64_t kMostDim = 512;  // 64 lanes of 8 f32 elements
+
+template <class T>
+struct Heads {
+  template <int P, int kLanes, bool kNeighbours>
+  static uint32_t go(HeadArgs a, bool back, hipStream_t s) {
+    constexpr uint32_t kGroups = 64 / kLanes;
+    // A wave goes through as many of a row's heads as leaves enough waves.
+    const uint32_t most = (a.heads + kGroups - 1) / kGroups;
+    uint64_t parts = 4096 / a.rows + 1;
+    a.parts = (uint32_t)(parts < most ? parts : most);
+    const uint64_t units = a.rows * a.parts, waves = back ? kBackWaves : 4, sets = (units + waves - 1) / waves;
+    const uint64_t cap = back ? kMaxLines : 1u << 16;
+    const uint32_t grid = (uint32_t)(sets < cap ? sets : cap);
+    if (back) hipLaunchKernelGGL((k_heads_bwd<T, P, kLanes, kNeighbours>), dim3(grid), dim3(64 * kBackWaves), 0, s, a);
+    else hipLaunchKernelGGL((k_heads<T, P, kLanes, kNeighbours>), dim3(grid), dim3(256), 0, s, a);
+    return grid;
+  }
+  template <int P, bool kNeighbours>
+  static uint32_t lanes(const HeadArgs &a, bool back, hipStream_t s) {
+    if (a.slots <= 2) return go<P, 2, kNeighbours>(a, back, s);
+    if (a.slots <= 4) return go<P, 4, kNeighbours>(a, back, s);
+    if (a.slots <= 8) return go<P, 8, kNeighbours>(a, back, s);
+    if (a.slots <= 16) return go<P, 16, kNeighbours>(a, back, s);
+    if (a.slots <= 32) return go<P, 32, kNeighbours>(a, back, s);
+    return go<P, 64, kNeighbours>(a, back, s);
+  }
+  template <int P>
+  static uint32_t launch(HeadArgs a, bool neighbours, bool back, hipStream_t s) {
+    return neighbours ? lanes<P, true>(a, back, s) : lanes<P, false>(a, back, s);
+  }
+  static void set_slots(HeadArgs &a, uint32_t P) {
+    a.pair_slots = (a.half + P - 1) / P;
+    a.slots = a.pair_slots + (a.dim - 2 * a.half + 2 * P - 1) / (2 * P);
+  }
+  // The work-groups that ran.
+  static uint32_t run(HeadArgs a, bool neighbours, bool back, hipStream_t s) {
+    if constexpr (sizeof(T) == 4) {
+      set_slots(a, 4);
+      if (a.slots <= 64) return launch<4>(a, neighbours, back, s);
+    }
+    set_slots(a, 8);
+    return launch<8>(a, neighbours, back, s);
+  }
+};
+
+constexpr uint32_t kHeadFlags = TK_PARAMS_F32 | TK_INDEX_I64 | TK_INTERLEAVED;
+constexpr int kQueries = 1, kKeys = 2;  // Region's kinds
+
+struct HeadCall {
+  RowType type;
+  uint64_t rows, heads_q, heads_k, dim, rotary;
+  float eps;
+  uint32_t flags;
+  HeadArgs a{};
+
+  uint64_t width(int k) const { return (k ? heads_k : heads_q) * dim; }
+  tk_status check_numbers() const {
+    if (!(eps >= 0.0f && eps < INFINITY) || (flags & ~kHeadFlags) || rotary % 2 || rotary > dim) return TK_EINVAL;
+    if (rows >= kMaxDim || dim > kMostDim || heads_q >= kMaxDim || heads_k >= kMaxDim) return TK_ERANGE;
+    if ((heads_q + heads_k) * dim >= kMaxDim) return TK_ERANGE;
+    return TK_OK;
+  }
+  bool empty() const { return rows == 0 || dim == 0 || heads_q + heads_k == 0; }
+  // The arguments that both directions have.
+  tk_status angles(Arguments &c, const void *positions, uint64_t table_rows, const float *cosines, const float *sines) {
+    if (table_rows >= kMaxDim) return TK_ERANGE;
+    c.vector(positions, rows, flags & TK_INDEX_I64 ? 8 : 4, false, false);
+    if (rotary && table_rows) {
+      c.vector(cosines, table_rows * (rotary / 2), 4, false, true);
+      c.vector(sines, table_rows * (rotary / 2), 4, false, true);
+    }
+    a.positions = positions; a.table_rows = table_rows; a.cosines = cosines; a.sines = sines;
+    a.rows = rows; a.heads_q = (uint32_t)heads_q; a.heads = (uint32_t)(heads_q + heads_k);
+    a.dim = (uint32_t)dim; a.half = (uint32_t)(rotary / 2); a.eps = eps;
+    a.i64 = flags & TK_INDEX_I64; a.params_f32 = params_f32(type, flags);
+    return TK_OK;
+  }
+  uint32_t run(bool back, hipStream_t s) const {
+    const bool n = flags & TK_INTERLEAVED;
+    return type == kF32 ? Heads<float>::run(a, n, back, s) : type == kF16 ? Heads<f16_t>::run(a, n, back, s)
+                                                                           : Heads<bf16_t>::run(a, n, back, s);
+  }
+};
+
+static tk_status head_forward(HeadCall h, const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q,
+                              const void *gamma_k, const void *positions, uint64_t table_rows, const float *cosines,
+                              const float *sines, void *yq, uint64_t ldyq, void *yk, uint64_t ldyk, hipStream_t stream) {
+  tk_status st = h.check_numbers();
+  if (st != TK_OK || h.empty()) return st;
+  Arguments c{h.type, h.rows, h.dim, h.flags};
+  const void *x[2] = {q, k}, *gamma[2] = {gamma_q, gamma_k};
+  void *y[2] = {yq, yk};
+  const uint64_t ldx[2] = {ldq, ldk}, ldy[2] = {ldyq, ldyk};
+  for (int i = 0; i < 2; ++i) {
+    if (!h.width(i)) continue;
+    c.matrix_of(x[i], h.rows, h.width(i), ldx[i], c.t(), false, true, i ? kKeys : kQueries);
+    c.matrix_of(y[i], h.rows, h.width(i), ldy[i], c.t(), true, true, i ? kKeys : kQueries);
+    c.vector(gamma[i], h.dim, c.par(), false, false);
+    h.a.side[i] = Side{x[i], nullptr, gamma[i], y[i], ldx[i], 0, ldy[i]};
+  }
+  if ((st = h.angles(c, positions, table_rows, cosines, sines)) != TK_OK || (st = c.done()) != TK_OK) return st;
+  h.run(false, stream);
+  return launch_status();
+}
+
+static uint64_t head_bytes(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim) {
+  return rows * (heads_q + heads_k) * dim ? 8 * kMaxLines * line_pitch(dim) : 0;
+}
+
+static tk_status head_backward(HeadCall h, const void *dyq, uint64_t lddyq, const void *dyk, uint64_t lddyk, const void *q,
+                               uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q, const void *gamma_k,
+                               const void *positions, uint64_t table_rows, const float *cosines, const float *sines,
+                               void *dq, uint64_t lddq, void *dk, uint64_t lddk, void *dgamma_q, void *dgamma_k,
+                               void *workspace, uint64_t bytes, hipStream_t stream) {
+  tk_status st = h.check_numbers();
+  if (st != TK_OK || h.dim == 0) return st;
+  Arguments c{h.type, h.rows, h.dim, h.flags};
+  const bool sums = dgamma_q || dgamma_k;
+  c.vector(dgamma_q, h.dim, c.par(), true, false);
+  c.vector(dgamma_k, h.dim, c.par(), true, false);
+  if (h.empty()) {
+    if ((st = c.done()) != TK_OK || !sums) return st;
+    return finish(h.type, h.flags, nullptr, 0, h.dim, dgamma_q, dgamma_k, nullptr, stream);
+  }
+  const void *x[2] = {q, k}, *dy[2] = {dyq, dyk}, *gamma[2] = {gamma_q, gamma_k};
+  void *dx[2] = {dq, dk};
+  const uint64_t ldx[2] = {ldq, ldk}, lddy[2] = {lddyq, lddyk}, lddx[2] = {lddq, lddk};
+  for (int i = 0; i < 2; ++i) {
+    if (!h.width(i)) continue;
+    const int kind = i ? kKeys : kQueries;
+    c.matrix_of(x[i], h.rows, h.width(i), ldx[i], c.t(), false, true, kind);
+    c.matrix_of(dy[i], h.rows, h.width(i), lddy[i], c.t(), false, true, kind);
+    c.matrix_of(dx[i], h.rows, h.width(i), lddx[i], c.t(), true, true, kind);
+    c.vector(gamma[i], h.dim, c.par(), false, false);
+    h.a.side[i] = Side{x[i], dy[i], gamma[i], dx[i], ldx[i], lddy[i], lddx[i]};
+  }
+  const uint64_t need = sums ? head_bytes(h.rows, h.heads_q, h.heads_k, h.dim) : 0;
+  if (!serves(workspace, bytes, need)) return TK_EINVAL;
+  if (need) c.vector(workspace, need / 4, 4, true, true);
+  if ((st = h.angles(c, positions, table_rows, cosines, sines)) != TK_OK || (st = c.done()) != TK_OK) return st;
+  h.a.partial = sums ? (float *)workspace : nullptr;
+  const uint32_t lines = h.run(true, stream);
+  if ((st = launch_status()) != TK_OK || !sums) return st;
+  return finish(h.type, h.flags, h.a.partial, lines, h.dim, dgamma_q, dgamma_k, nullptr, stream);
+}
+
+}  // namespace tk
+
+extern "C" {
+
+tk_status tk_head_norm_workspace_bytes(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t *bytes) {
+  if (!bytes) return TK_EINVAL;
+  if (rows >= tk::kMaxDim || heads_q >= tk::kMaxDim || heads_k >= tk::kMaxDim || dim > tk::kMostDim ||
+      (heads_q + heads_k) * dim >= tk::kMaxDim)
+    return TK_ERANGE;
+  *bytes = tk::head_bytes(rows, heads_q, heads_k, dim);
+  return TK_OK;
+}
+
+#define TK_HEADS(SUFFIX, TYPE)                                                                                            \
+  tk_status tk_head_norm_rotate_##SUFFIX(                                                                                 \
+      uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t rotary, float eps, uint32_t flags,        \
+      const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q, const void *gamma_k,                 \
+      const void *positions, uint64_t table_rows, const float *cosines, const float *sines, void *yq, uint64_t ldyq,      \
+      void *yk, uint64_t ldyk, hipStream_t stream) {                                                                      \
+    return tk::head_forward(tk::HeadCall{TYPE, rows, heads_q, heads_k, dim, rotary, eps, flags}, q, ldq, k, ldk, gamma_q, \
+                            gamma_k, positions, table_rows, cosines, sines, yq, ldyq, yk, ldyk, stream);                  \
+  }                                                                                                                       \
+  tk_status tk_head_norm_rotate_backward_##SUFFIX(                                                                        \
+      uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t rotary, float eps, uint32_t flags,        \
+      const void *dyq, uint64_t lddyq, const void *dyk, uint64_t lddyk, const void *q, uint64_t ldq, const void *k,       \
+      uint64_t ldk, const void *gamma_q, const void *gamma_k, const void *positions, uint64_t table_rows,                 \
+      const float *cosines, const float *sines, void *dq, uint64_t lddq, void *dk, uint64_t lddk, void *dgamma_q,         \
+      void *dgamma_k, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {                                    \
+    return tk::head_backward(tk::HeadCall{TYPE, rows, heads_q, heads_k, dim, rotary, eps, flags}, dyq, lddyq, dyk, lddyk, \
+                             q, ldq, k, ldk, gamma_q, gamma_k, positions, table_rows, cosines, sines, dq, lddq, dk, lddk, \
+                             dgamma_q, dgamma_k, workspace, workspace_bytes, stream);                                     \
+  }
+
+TK_HEADS(f32, tk::kF32)
+TK_HEADS(f16, tk::kF16)
+TK_HEADS(bf16, tk::kBF16)
+
+}  // extern "C"

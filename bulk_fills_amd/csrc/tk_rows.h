@@ -148,6 +148,31 @@ __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) 
   }
 }
 
+// The words themselves, for draws other than dropout's.
+template <int CH>
+__device__ __forceinline__ void chunk_words(uint32_t hk, uint32_t c, uint32_t *w) {
+  if (CH > 1 && (c & (CH - 1)) == 0) {
+    uint32_t k = c ^ hk;
+    k ^= k >> 16;
+    uint32_t x[CH];
+    x[0] = k * kHashMul1;
+#pragma unroll
+    for (int b = 1; b < CH; b <<= 1) {
+      const uint32_t step = k & b ? 0u - b * kHashMul1 : b * kHashMul1;
+#pragma unroll
+      for (int e = 0; e < b; ++e) x[b + e] = x[e] + step;
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) {
+      const uint32_t y = (x[e] ^ (x[e] >> 15)) * kHashMul2;
+      w[e] = y ^ (y >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < CH; ++e) w[e] = tk_word(hk, c + e);
+  }
+}
+
 // ---- sums over a row's lanes -----------------------------------------------------------
 template <int kCtrl>
 __device__ __forceinline__ float dpp(float x) {
@@ -484,22 +509,33 @@ __device__ __forceinline__ float norm_grad(float g, float h, float rstd, float a
   return __builtin_fmaf(h, b, __builtin_fmaf(g, rstd, a));
 }
 
-// A chunk of a row's inputs as loaded.  dy is of type D: T, or R for dropout-add's gradient.
-template <class T, class R, class D, bool kNorm, bool kOnce, int CH>
+// The scale of a checkpoint's codes at column c of a row (past the row's end its last one's).
+__device__ __forceinline__ float code_scale(const BwdArgs &a, uint64_t row, uint32_t c) {
+  return a.scales[row * a.blocks + (c < a.cols ? c / kCodeBlock : a.blocks - 1)];
+}
+
+// A chunk of a row's inputs as loaded.  dy is of type D: T, or R for dropout-add's gradient; the sum
+// of type S: R, or the 8-bit codes of a checkpoint with their scale (a chunk's elements that count
+// lie in one block).
+template <class T, class R, class S, class D, bool kNorm, bool kOnce, int CH>
 struct BwdIn {
+  static constexpr bool kCodes = std::is_same<S, int8_t>::value;
   Chunk<D, CH> dy;
-  Chunk<R, CH> sum, dsum;
+  Chunk<S, CH> sum;
+  Chunk<R, CH> dsum;
+  float scale;
   __device__ __forceinline__ void load(const BwdArgs &a, uint64_t row, uint32_t c) {
     const uint32_t at = chunk_at<CH>(c, a.cols);
     dy = load_chunk<kOnce, CH>((const D *)a.dy + row * a.lddy + at);
-    if (kNorm) sum = load_chunk<kOnce, CH>((const R *)a.sum + row * a.lds + at);
+    if (kNorm) sum = load_chunk<kOnce, CH>((const S *)a.sum + row * a.lds + at);
+    if (kNorm && kCodes) scale = code_scale(a, row, c);
     if (a.dsum) dsum = load_chunk<kOnce, CH>((const R *)a.dsum + row * a.ldds + at);
   }
   // h of every element
   __device__ __forceinline__ void normed(int nv, float mean, float rstd, float *h) const {
-    unpack<CH, R>(sum, nv, h);
+    unpack<CH, S>(sum, nv, h);
 #pragma unroll
-    for (int e = 0; e < CH; ++e) h[e] = (h[e] - mean) * rstd;
+    for (int e = 0; e < CH; ++e) h[e] = ((kCodes ? h[e] * scale : h[e]) - mean) * rstd;
   }
   // Outputs: dresidual = v + dsum and dx = drop(dresidual), which comes back in v.
   template <bool kX>
@@ -555,7 +591,7 @@ __device__ __forceinline__ void put_sums(float *p, int nv, const float *v, bool 
 // of partial sums per work-group, which k_finish adds up in order.  Sixteen waves have 128
 // registers; with three sums, the f32 kernels and those of whole waves with a float stream spill 2
 // (9 with 32 lanes to a row), 12 to 16 bytes a lane.
-template <class T, class R, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
+template <class T, class R, class S, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
 __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
   constexpr int kSums = kBias ? 3 : 2;
   __shared__ float slot[2][16][2];
@@ -564,7 +600,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
   uint64_t base = (uint64_t)blockIdx.x * team.groups, row = base + team.group;
   const float inv = 1.0f / (float)a.cols;
   float acc[kSums][V][CH], gamma[V][CH], mean = 0.0f, rstd = 0.0f;
-  BwdIn<T, R, T, true, kOnce, CH> next[V];
+  BwdIn<T, R, S, T, true, kOnce, CH> next[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const uint32_t c = (j * team.threads + team.t) * CH;
@@ -583,7 +619,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
   for (; base < a.rows; base += step, row += step, par ^= 1) {
     const bool here = row < a.rows;
     const float m = mean, rs = rstd;
-    BwdIn<T, R, T, true, kOnce, CH> in[V];
+    BwdIn<T, R, S, T, true, kOnce, CH> in[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) in[j] = next[j];
     if (row + step < a.rows) {
@@ -671,7 +707,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(BwdArgs a) {
 // Rows wider than k_norm_bwd's registers hold with their column sums: first norm_grad's two
 // numbers for every row, then k_cols_bwd over columns, which reads dy and sum again (here they
 // are read through the caches).
-template <class T, class R>
+template <class T, class R, class S>
 __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
   constexpr int CH = kChunk<T, R>, kTpr = 1024;
   __shared__ float slot[2][kTpr / 64][2];
@@ -680,27 +716,31 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s[2] = {0.0f, 0.0f};
     const T *dy = (const T *)a.dy + row * a.lddy;
-    const R *sum = (const R *)a.sum + row * a.lds;
+    const S *sum = (const S *)a.sum + row * a.lds;
+    constexpr bool kCodes = std::is_same<S, int8_t>::value;
     uint32_t c = threadIdx.x * CH;
     // the next chunk is loaded before the present one is used (past the end: the row's last, unused)
     Chunk<T, CH> next_dy = load_chunk<false, CH>(dy + chunk_at<CH>(c, a.cols));
-    Chunk<R, CH> next_sum = load_chunk<false, CH>(sum + chunk_at<CH>(c, a.cols));
+    Chunk<S, CH> next_sum = load_chunk<false, CH>(sum + chunk_at<CH>(c, a.cols));
+    float next_scale = kCodes ? code_scale(a, row, c) : 1.0f;
     for (; c < a.cols; c += kTpr * CH) {
       const int nv = (int)(a.cols - c);
       const uint32_t at = chunk_at<CH>(c + kTpr * CH, a.cols);
       float g[CH], h[CH], w[CH];
       const Chunk<T, CH> here_dy = next_dy;
-      const Chunk<R, CH> here_sum = next_sum;
+      const Chunk<S, CH> here_sum = next_sum;
+      const float scale = next_scale;
       next_dy = load_chunk<false, CH>(dy + at);
       next_sum = load_chunk<false, CH>(sum + at);
+      if (kCodes) next_scale = code_scale(a, row, c + kTpr * CH);
       load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, w);
       unpack<CH, T>(here_dy, nv, g);
-      unpack<CH, R>(here_sum, nv, h);
+      unpack<CH, S>(here_sum, nv, h);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         const float x = g[e] * w[e];
         s[0] += x;
-        s[1] = __builtin_fmaf(x, (h[e] - mean) * rstd, s[1]);
+        s[1] = __builtin_fmaf(x, ((kCodes ? h[e] * scale : h[e]) - mean) * rstd, s[1]);
       }
     }
     row_sums<64>(s, slot[par], 0, kTpr / 64);
@@ -721,7 +761,7 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
 // us for dropout-add's backward bf16 8192x4096, by where the buffers lay).  Sixteen waves to a
 // work-group keep the lines of partial sums few: 32768x512 takes 14.7 us, with four waves and
 // 2048 lines 20.5; 65536x64, eight rows to a wave, 7.4 us, with one row to a wave 24.
-template <class T, class R, bool kNorm, bool kX, bool kBias, bool kOnce, int CH, int kLanes>
+template <class T, class R, class S, bool kNorm, bool kX, bool kBias, bool kOnce, int CH, int kLanes>
 __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
   constexpr int kSums = (kNorm ? 2 : 0) + (kBias ? 1 : 0), kGroups = 64 / kLanes;
   typedef typename std::conditional<kNorm, T, R>::type D;
@@ -737,11 +777,11 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
   if (nv > 0) {
     float w[CH];
     if (kNorm) load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, w);
-    BwdIn<T, R, D, kNorm, kOnce, CH> next;
+    BwdIn<T, R, S, D, kNorm, kOnce, CH> next;
     uint64_t row = ((uint64_t)blockIdx.y * 16 + wave) * kGroups + (kGroups > 1 ? lane / kLanes : 0);
     if (row < a.rows) next.load(a, row, c);
     for (; row < a.rows; row += step) {
-      const BwdIn<T, R, D, kNorm, kOnce, CH> in = next;
+      const BwdIn<T, R, S, D, kNorm, kOnce, CH> in = next;
       if (row + step < a.rows) next.load(a, row + step, c);
       float v[CH];
       unpack<CH, D>(in.dy, nv, v);
@@ -791,9 +831,7 @@ __global__ __launch_bounds__(1024) void k_cols_bwd(BwdArgs a) {
 // scalar unit and its lanes' rows from there, a few rows further: one product a matrix.  The
 // quotient is a product with the rounded-up reciprocal: exact below 2^31 chunks, which a launch
 // stays under.
-__device__ __forceinline__ uint32_t row_of(const AddArgs &a, uint32_t n) {
-  return a.div_shift < 0 ? n : __umulhi(n, a.div_mul) >> a.div_shift;
-}
+__device__ __forceinline__ uint32_t row_of(const AddArgs &a, uint32_t n) { return a.per_row.of(n); }
 
 template <class TI, class TO, bool kDivide, bool kOnce, bool kFlat, int CH, class TP>
 __global__ __launch_bounds__(256) void k_drop_add(AddArgs a) {
@@ -875,31 +913,31 @@ static void norm_fwd_of(const FwdArgs &a, hipStream_t s) {
   else hipLaunchKernelGGL((k_norm_fwd_wide<T, R, kX>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
 }
 
-template <class T, class R, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
+template <class T, class R, class S, bool kX, bool kBias, bool kOnce, int CH, int kLanes, int V>
 static void launch_bwd(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
   const uint32_t lds = (uint32_t)p.waves * kLanes * V * CH * 4;
-  hipLaunchKernelGGL((k_norm_bwd<T, R, kX, kBias, kOnce, CH, kLanes, V>), dim3((uint32_t)p.lines), dim3(64 * p.waves), lds, s,
+  hipLaunchKernelGGL((k_norm_bwd<T, R, S, kX, kBias, kOnce, CH, kLanes, V>), dim3((uint32_t)p.lines), dim3(64 * p.waves), lds, s,
                      a);
 }
 
-template <class T, class R, bool kX, bool kBias, bool kOnce>
+template <class T, class R, class S, bool kX, bool kBias, bool kOnce>
 static void norm_bwd_as(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
   constexpr int CH = kChunk<T, R>, K = 8 / CH;
-  if (a.cols < CH) launch_bwd<T, R, kX, kBias, kOnce, 1, 8, 1>(a, p, s);
-  else if (p.lanes == 8) launch_bwd<T, R, kX, kBias, kOnce, CH, 8, K>(a, p, s);
-  else if (p.lanes == 16) launch_bwd<T, R, kX, kBias, kOnce, CH, 16, K>(a, p, s);
-  else if (p.lanes == 32) launch_bwd<T, R, kX, kBias, kOnce, CH, 32, K>(a, p, s);
-  else launch_bwd<T, R, kX, kBias, kOnce, CH, 64, K>(a, p, s);
+  if (a.cols < CH) launch_bwd<T, R, S, kX, kBias, kOnce, 1, 8, 1>(a, p, s);
+  else if (p.lanes == 8) launch_bwd<T, R, S, kX, kBias, kOnce, CH, 8, K>(a, p, s);
+  else if (p.lanes == 16) launch_bwd<T, R, S, kX, kBias, kOnce, CH, 16, K>(a, p, s);
+  else if (p.lanes == 32) launch_bwd<T, R, S, kX, kBias, kOnce, CH, 32, K>(a, p, s);
+  else launch_bwd<T, R, S, kX, kBias, kOnce, CH, 64, K>(a, p, s);
 }
 
-template <class T, class R, bool kNorm, bool kX, bool kBias, bool kOnce, int CH, int kLanes>
+template <class T, class R, class S, bool kNorm, bool kX, bool kBias, bool kOnce, int CH, int kLanes>
 static void launch_cols(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
   // a launch holds fewer than 2^32 threads to a dimension
   constexpr uint64_t kMost = 1u << 20;
   BwdArgs b = a;
   for (uint64_t strip = 0; strip < p.strips; strip += kMost) {
     b.strip0 = (uint32_t)strip;
-    hipLaunchKernelGGL((k_cols_bwd<T, R, kNorm, kX, kBias, kOnce, CH, kLanes>),
+    hipLaunchKernelGGL((k_cols_bwd<T, R, S, kNorm, kX, kBias, kOnce, CH, kLanes>),
                        dim3((uint32_t)(p.strips - strip < kMost ? p.strips - strip : kMost), (uint32_t)p.lines), dim3(1024), 0,
                        s, b);
   }
@@ -908,23 +946,23 @@ static void launch_cols(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
 template <class T, class R, bool kOnce>
 static void add_bwd_as(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
   constexpr int CH = kChunk<T, R>;
-  if (a.cols < CH) launch_cols<T, R, false, true, true, kOnce, 1, 8>(a, p, s);
-  else if (p.lanes == 8) launch_cols<T, R, false, true, true, kOnce, CH, 8>(a, p, s);
-  else if (p.lanes == 16) launch_cols<T, R, false, true, true, kOnce, CH, 16>(a, p, s);
-  else if (p.lanes == 32) launch_cols<T, R, false, true, true, kOnce, CH, 32>(a, p, s);
-  else launch_cols<T, R, false, true, true, kOnce, CH, 64>(a, p, s);
+  if (a.cols < CH) launch_cols<T, R, R, false, true, true, kOnce, 1, 8>(a, p, s);
+  else if (p.lanes == 8) launch_cols<T, R, R, false, true, true, kOnce, CH, 8>(a, p, s);
+  else if (p.lanes == 16) launch_cols<T, R, R, false, true, true, kOnce, CH, 16>(a, p, s);
+  else if (p.lanes == 32) launch_cols<T, R, R, false, true, true, kOnce, CH, 32>(a, p, s);
+  else launch_cols<T, R, R, false, true, true, kOnce, CH, 64>(a, p, s);
 }
 
-template <class T, class R, bool kX, bool kBias>
+template <class T, class R, class S, bool kX, bool kBias>
 static void norm_bwd_of(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
   if (p.strips) {  // wide rows
-    hipLaunchKernelGGL((k_row_stats<T, R>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
-    if (a.once) launch_cols<T, R, true, kX, kBias, true, kChunk<T, R>, 64>(a, p, s);
-    else launch_cols<T, R, true, kX, kBias, false, kChunk<T, R>, 64>(a, p, s);
+    hipLaunchKernelGGL((k_row_stats<T, R, S>), dim3(row_grid(a.rows, 1u << 16)), dim3(1024), 0, s, a);
+    if (a.once) launch_cols<T, R, S, true, kX, kBias, true, kChunk<T, R>, 64>(a, p, s);
+    else launch_cols<T, R, S, true, kX, kBias, false, kChunk<T, R>, 64>(a, p, s);
   } else if (a.once) {
-    norm_bwd_as<T, R, kX, kBias, true>(a, p, s);
+    norm_bwd_as<T, R, S, kX, kBias, true>(a, p, s);
   } else {
-    norm_bwd_as<T, R, kX, kBias, false>(a, p, s);
+    norm_bwd_as<T, R, S, kX, kBias, false>(a, p, s);
   }
 }
 
@@ -954,10 +992,15 @@ struct RowKernels {
       else norm_fwd_of<T, R, false, false>(a, s);
     }
   }
+  template <class S>
+  static void norm_bwd_from(const BwdArgs &a, const BwdPlan &p, bool bias, hipStream_t s) {
+    if (!a.dx) norm_bwd_of<T, R, S, false, false>(a, p, s);
+    else if (!bias) norm_bwd_of<T, R, S, true, false>(a, p, s);
+    else norm_bwd_of<T, R, S, true, true>(a, p, s);
+  }
   static void norm_bwd(const BwdArgs &a, const BwdPlan &p, bool bias, hipStream_t s) {
-    if (!a.dx) norm_bwd_of<T, R, false, false>(a, p, s);
-    else if (!bias) norm_bwd_of<T, R, true, false>(a, p, s);
-    else norm_bwd_of<T, R, true, true>(a, p, s);
+    if (a.scales) norm_bwd_from<int8_t>(a, p, bias, s);
+    else norm_bwd_from<R>(a, p, bias, s);
   }
   static void add_bwd_sums(const BwdArgs &a, const BwdPlan &p, hipStream_t s) {
     if (a.once) add_bwd_as<T, R, true>(a, p, s);

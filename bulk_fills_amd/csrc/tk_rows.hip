@@ -187,13 +187,9 @@ static tk_status run_add(void (*launch)(const AddArgs &, int, hipStream_t), int 
   if (!a.flat && cols < (uint64_t)chunk) chunk = 1;  // no row holds a whole chunk
   const uint64_t per_row = (cols + chunk - 1) / chunk, most = 1ull << 30;  // chunks
   a.bias_cols = cols;
-  // n / d for n < 2^31: n ceil(2^(31 + l) / d) >> (31 + l), l = ceil(log2 d)
   if (!a.flat || a.bias) {
-    int l = 0;
-    while ((1ull << l) < per_row) ++l;
     a.chunks_per_row = (uint32_t)per_row;
-    a.div_shift = l - 1;
-    a.div_mul = (uint32_t)(((1ull << (31 + l)) + per_row - 1) / per_row);
+    a.per_row = Divisor(per_row);
   }
   if (a.flat) {
     // pieces of whole rows where there is a bias, and none shorter than a chunk
@@ -320,11 +316,13 @@ static tk_status norm_forward(RowType t, bool fused, uint32_t key, uint64_t star
   return launch_status();
 }
 
+// `kept`: `sum` is a checkpoint's codes, and `scales` theirs.
 static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t start, uint64_t rows, uint64_t cols, float p,
                                uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds,
-                               const void *sum, uint64_t lds, const void *gamma, const float *mean, const float *rstd,
-                               void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma, void *dbeta,
-                               void *dbias, void *workspace, uint64_t workspace_bytes_, hipStream_t stream) {
+                               const void *sum, uint64_t lds, bool kept, const float *scales, const void *gamma,
+                               const float *mean, const float *rstd, void *dx, uint64_t lddx, void *dresidual,
+                               uint64_t lddr, void *dgamma, void *dbeta, void *dbias, void *workspace,
+                               uint64_t workspace_bytes_, hipStream_t stream) {
   tk_status st = check_scalars(start, rows, cols, p, 0.0f, flags, kRowFlags);
   if (st != TK_OK || cols == 0) return st;
   Arguments c{t, rows, cols, flags};
@@ -338,7 +336,9 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   }
   c.matrix(dy, lddy, c.t(), false, true);
   c.matrix(dsum, ldds, c.res(), false, false);
-  c.matrix(sum, lds, c.res(), false, true);
+  const uint64_t blocks = (cols + kCodeBlock - 1) / kCodeBlock;
+  c.matrix(sum, lds, kept ? 1 : c.res(), false, true);
+  if (kept) c.vector(scales, rows * blocks, 4, false, true);
   c.vector(gamma, cols, c.par(), false, false);
   c.vector(mean, rows, 4, false, true);
   c.vector(rstd, rows, 4, false, true);
@@ -355,6 +355,7 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   const BwdPlan plan = norm_plan(k.chunk, rows, cols, sums);
   BwdArgs a{};
   a.dy = dy; a.lddy = lddy; a.dsum = dsum; a.ldds = ldds; a.sum = sum; a.lds = lds;
+  a.scales = kept ? scales : nullptr; a.blocks = (uint32_t)blocks;
   a.gamma = gamma; a.mean = mean; a.rstd = rstd;
   a.dx = dx; a.lddx = lddx; a.dresidual = dresidual; a.lddr = lddr;
   a.rows = rows; a.cols = (uint32_t)cols; a.waves = (uint32_t)plan.row_waves;
@@ -365,7 +366,7 @@ static tk_status norm_backward(RowType t, bool fused, uint32_t key, uint64_t sta
   a.stats = !plan.strips ? nullptr : (float *)((char *)workspace + need - 8 * rows);
   a.params_f32 = params_f32(t, flags);
   a.drop = drop_of(key, start, p);
-  a.once = rows * cols * (c.t() + (dsum ? 2 : 1) * c.res()) > kCachedReads;
+  a.once = rows * cols * (c.t() + (dsum ? c.res() : 0) + (kept ? 1 : c.res())) > kCachedReads;
   k.norm_bwd(a, plan, dbias != nullptr, stream);
   if ((st = launch_status()) != TK_OK || !sums || a.alone) return st;
   return finish(t, flags, a.partial, plan.lines, cols, dgamma, dbeta, dbias, stream);
@@ -405,8 +406,9 @@ tk_status tk_backward_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t *by
                                             const void *x, uint64_t ldx, const void *gamma, const float *mean,           \
                                             const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta,       \
                                             void *workspace, uint64_t workspace_bytes, hipStream_t stream) {             \
-    return tk::norm_backward(TYPE, false, 0, 0, rows, cols, 0.0f, flags, dy, lddy, nullptr, 0, x, ldx, gamma, mean,      \
-                             rstd, nullptr, 0, dx, lddx, dgamma, dbeta, nullptr, workspace, workspace_bytes, stream);    \
+    return tk::norm_backward(TYPE, false, 0, 0, rows, cols, 0.0f, flags, dy, lddy, nullptr, 0, x, ldx, false, nullptr,   \
+                             gamma, mean, rstd, nullptr, 0, dx, lddx, dgamma, dbeta, nullptr, workspace,                 \
+                             workspace_bytes, stream);                                                                   \
   }                                                                                                                      \
   tk_status tk_dropout_add_layer_norm_##SUFFIX(                                                                          \
       uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float eps, uint32_t flags,               \
@@ -420,13 +422,35 @@ tk_status tk_backward_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t *by
       uint64_t lddy, const void *dsum, uint64_t ldds, const void *sum, uint64_t lds, const void *gamma,                  \
       const float *mean, const float *rstd, void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma,       \
       void *dbeta, void *dbias, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {                         \
-    return tk::norm_backward(TYPE, true, key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, gamma,   \
-                             mean, rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace, workspace_bytes,    \
-                             stream);                                                                                    \
+    return tk::norm_backward(TYPE, true, key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, sum, lds, false,   \
+                             nullptr, gamma, mean, rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace,     \
+                             workspace_bytes, stream);                                                                   \
+  }
+
+#define TK_BACKWARD_FROM_CHECKPOINT(SUFFIX, TYPE)                                                                        \
+  tk_status tk_layer_norm_backward_checkpoint_##SUFFIX(                                                                  \
+      uint64_t rows, uint64_t cols, uint32_t flags, const void *dy, uint64_t lddy, const int8_t *codes, uint64_t ldc,    \
+      const float *scales, const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx,             \
+      void *dgamma, void *dbeta, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {                        \
+    return tk::norm_backward(TYPE, false, 0, 0, rows, cols, 0.0f, flags, dy, lddy, nullptr, 0, codes, ldc, true, scales, \
+                             gamma, mean, rstd, nullptr, 0, dx, lddx, dgamma, dbeta, nullptr, workspace,                 \
+                             workspace_bytes, stream);                                                                   \
+  }                                                                                                                      \
+  tk_status tk_dropout_add_layer_norm_backward_checkpoint_##SUFFIX(                                                      \
+      uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, uint32_t flags, const void *dy,          \
+      uint64_t lddy, const void *dsum, uint64_t ldds, const int8_t *codes, uint64_t ldc, const float *scales,            \
+      const void *gamma, const float *mean, const float *rstd, void *dx, uint64_t lddx, void *dresidual, uint64_t lddr,  \
+      void *dgamma, void *dbeta, void *dbias, void *workspace, uint64_t workspace_bytes, hipStream_t stream) {           \
+    return tk::norm_backward(TYPE, true, key, start_draw, rows, cols, p, flags, dy, lddy, dsum, ldds, codes, ldc, true,  \
+                             scales, gamma, mean, rstd, dx, lddx, dresidual, lddr, dgamma, dbeta, dbias, workspace,      \
+                             workspace_bytes, stream);                                                                   \
   }
 
 TK_ROW_OPERATORS(f32, tk::kF32)
 TK_ROW_OPERATORS(f16, tk::kF16)
 TK_ROW_OPERATORS(bf16, tk::kBF16)
+TK_BACKWARD_FROM_CHECKPOINT(f32, tk::kF32)
+TK_BACKWARD_FROM_CHECKPOINT(f16, tk::kF16)
+TK_BACKWARD_FROM_CHECKPOINT(bf16, tk::kBF16)
 
 }  // extern "C"

@@ -16,6 +16,20 @@ struct Drop {
   float rq, rl;        // its reciprocal rounded down, and the rest
 };
 
+// Quotients of n < 2^31 by d: n ceil(2^(31 + l) / d) >> (31 + l), l = ceil(log2 d), exact for them.
+struct Divisor {
+  uint32_t mul = 0;
+  int shift = -1;  // below 0: d is 1
+  Divisor() = default;
+  explicit Divisor(uint64_t d) {
+    int l = 0;
+    while ((1ull << l) < d) ++l;
+    shift = l - 1;
+    mul = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return shift < 0 ? n : __umulhi(n, mul) >> shift; }
+};
+
 // Forward of the layer norm (x null: its input is `residual`) and of the fused operator.
 struct FwdArgs {
   const void *x, *bias, *residual, *gamma, *beta;
@@ -37,8 +51,9 @@ struct BwdArgs {
   float *partial;  // lines of partial column sums: dgamma's, dbeta's, then dbias's
   void *sums[3];   // those gradients (null: not wanted), written by the kernel where `alone`
   float *stats;    // -rstd mean(g), -rstd mean(g h) of every row (wide rows)
+  const float *scales;  // `sum` is a checkpoint's codes, these their scales, `blocks` to a row (null: it is not)
   uint64_t rows, lddy, ldds, lds, lddx, lddr;
-  uint32_t cols, waves, strip0;  // strip0: the launch's first strip of columns
+  uint32_t cols, waves, blocks, strip0;  // strip0: the launch's first strip of columns
   bool alone;                    // one line of sums: they are the gradients
   bool past;                     // the lines are written past the caches
   bool params_f32, once;  // once: the call's reads go past the caches
@@ -49,12 +64,15 @@ struct AddArgs {
   const void *x, *bias, *residual;
   void *y;
   uint64_t row0, ldx, ldr, ldy, cols64, bias_cols;
-  uint32_t chunks, chunks_per_row, div_mul;
-  int div_shift;
+  uint32_t chunks, chunks_per_row;
+  Divisor per_row;  // chunks_per_row
   bool flat;  // the call's matrices are one row of cols64 elements; a bias repeats in it
   bool params_f32, once;  // once: the call's reads go past the caches
   Drop drop;
 };
+
+// Columns of a row that share a checkpoint's scale.
+constexpr uint32_t kCodeBlock = 128;
 
 // Floats from one line of partial sums to the next: a multiple of 128 bytes, so that no two
 // work-groups write to one cache line (layer norm backward bf16 1000x1500: 10.1 us, packed 10.7).

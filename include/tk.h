@@ -289,6 +289,176 @@ tk_status tk_dropout_add_layer_norm_backward_bf16(uint32_t key, uint64_t start_d
         void *dresidual, uint64_t lddr, void *dgamma, void *dbeta, void *dbias, void *workspace,
         uint64_t workspace_bytes, hipStream_t stream);
 
+/* ---- Embedding lookup ----------------------------------------------------------------
+ * The rows' way into a model, and the table's gradient, with the dropout that follows the lookup.
+ * Types, flags, strides, rounding and drop() are the row operators'; the counter of an element is
+ * start_draw + r * cols + c:
+ *   tk_embedding     y[r] = drop(scale * table[ids[r]])
+ *     _backward      dtable[v] = scale * (sum of drop(dy[r]) over the rows r with ids[r] = v)
+ * ids are `rows` int32 numbers, or int64 with TK_INDEX_I64.  table and dtable are vocab x cols.  A row
+ * whose id is no row of the table (below 0, as padding often is, or vocab and above) gives a y of
+ * +0.0 and goes into no gradient; its dy is not read.
+ *   flags: TK_RESIDUAL_F32  y and dy are float       TK_PARAMS_F32  table and dtable are float
+ *          TK_INDEX_I64     ids are int64
+ *          TK_ACCUMULATE    (backward) the sums are added to what dtable holds, rounded once; rows of
+ *                           it whose token does not occur are neither read nor written.  Without it
+ *                           every row is written, with zeros where its token does not occur.
+ * The gradient's sums are float, over the rows in their order: equal arguments give equal bits.
+ * Nothing is updated concurrently, so a token of every row costs no more than others.
+ *   scale must be finite, else TK_EINVAL; rows, cols, vocab and the lds are below 2^31, else TK_ERANGE.
+ *   rows == 0 or cols == 0 is TK_OK, as is vocab == 0 (y is then zeros; the table may be NULL);
+ *   a gradient over rows == 0 is zeros, or with TK_ACCUMULATE stays as it is.
+ *   No output may share bytes with any other argument.
+ *   workspace (backward): at least the bytes that tk_embedding_workspace_bytes names, 4-byte aligned;
+ *   as for the row operators it holds nothing between calls, one for the most rows serves fewer, and
+ *   calls that may overlap in time need one each.                                              */
+#define TK_INDEX_I64 8u
+#define TK_ACCUMULATE 16u
+tk_status tk_embedding_workspace_bytes(uint64_t rows, uint64_t cols, uint64_t vocab, uint64_t *bytes);
+
+tk_status tk_embedding_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float scale,
+        uint32_t flags, uint64_t vocab, const void *ids, const void *table, uint64_t ldt, void *y, uint64_t ldy,
+        hipStream_t stream);
+tk_status tk_embedding_backward_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float scale,
+        uint32_t flags, uint64_t vocab, const void *ids, const void *dy, uint64_t lddy, void *dtable, uint64_t lddt,
+        void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+tk_status tk_embedding_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float scale,
+        uint32_t flags, uint64_t vocab, const void *ids, const void *table, uint64_t ldt, void *y, uint64_t ldy,
+        hipStream_t stream);
+tk_status tk_embedding_backward_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float scale,
+        uint32_t flags, uint64_t vocab, const void *ids, const void *dy, uint64_t lddy, void *dtable, uint64_t lddt,
+        void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+tk_status tk_embedding_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float scale,
+        uint32_t flags, uint64_t vocab, const void *ids, const void *table, uint64_t ldt, void *y, uint64_t ldy,
+        hipStream_t stream);
+tk_status tk_embedding_backward_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, float p, float scale,
+        uint32_t flags, uint64_t vocab, const void *ids, const void *dy, uint64_t lddy, void *dtable, uint64_t lddt,
+        void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/* ---- Norms of queries and keys for each head, with the position rotation -------------
+ * A row is a token: heads_q query heads and heads_k key heads of `dim` elements each, one after the
+ * other in q's row and in k's (slices of one projection's output, by their ld, as well as matrices of
+ * their own).  For each head x:
+ *   n = x rstd gamma, rstd = 1 / sqrt(mean(x^2) + eps), with gamma_q or gamma_k of dim elements;
+ *   the first `rotary` elements of n turn in pairs (a, b), i < rotary / 2:
+ *     (a cos - b sin, b cos + a sin),  cos = cosines[pos][i], sin = sines[pos][i],
+ *   where a and b are elements i and rotary / 2 + i, or with TK_INTERLEAVED 2 i and 2 i + 1; the rest
+ *   of the head stays as it is.
+ * pos is positions[r], int32 or with TK_INDEX_I64 int64 (NULL: r).  cosines and sines are table_rows x
+ * (rotary / 2) contiguous floats that the caller makes once.  A row whose position is not in
+ * [0, table_rows), padding for instance, is normed and does not turn.
+ *   _backward: g = dy turned back, h = x rstd: dgamma = sums of g h over rows and heads,
+ *              dx = rstd (g gamma - h mean(g gamma h)); the statistics are made anew from x.
+ * All matrices are of the operator's type; sums and angles are float, outputs are rounded once.
+ *   flags: TK_PARAMS_F32 (gammas and their gradients are float), TK_INDEX_I64, TK_INTERLEAVED.
+ *   Nullable: gammas (1), positions, dgammas, q's or k's arguments where their number of heads is 0,
+ *          and the tables where rotary or table_rows is 0.
+ *   In place: yq may be q and yk k; dq may be q or dyq, dk k or dyk (same address and ld).  No other
+ *          output may share bytes with any other argument.
+ *   rotary must be even and at most dim, else TK_EINVAL; dim is at most 512, and rows, a row's
+ *   elements, table_rows and the lds are below 2^31, else TK_ERANGE.  rows == 0, dim == 0 or no head at
+ *   all is TK_OK with nothing to write but gradients of gammas, which are zeros.
+ *   workspace (backward with dgamma_q or dgamma_k): at least the bytes that
+ *   tk_head_norm_workspace_bytes names, 4-byte aligned; rules as above.                        */
+#define TK_INTERLEAVED 32u
+tk_status tk_head_norm_workspace_bytes(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t *bytes);
+
+tk_status tk_head_norm_rotate_f32(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t rotary,
+        float eps, uint32_t flags, const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q,
+        const void *gamma_k, const void *positions, uint64_t table_rows, const float *cosines, const float *sines,
+        void *yq, uint64_t ldyq, void *yk, uint64_t ldyk, hipStream_t stream);
+tk_status tk_head_norm_rotate_backward_f32(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim,
+        uint64_t rotary, float eps, uint32_t flags, const void *dyq, uint64_t lddyq, const void *dyk, uint64_t lddyk,
+        const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q, const void *gamma_k,
+        const void *positions, uint64_t table_rows, const float *cosines, const float *sines, void *dq, uint64_t lddq,
+        void *dk, uint64_t lddk, void *dgamma_q, void *dgamma_k, void *workspace, uint64_t workspace_bytes,
+        hipStream_t stream);
+
+tk_status tk_head_norm_rotate_f16(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t rotary,
+        float eps, uint32_t flags, const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q,
+        const void *gamma_k, const void *positions, uint64_t table_rows, const float *cosines, const float *sines,
+        void *yq, uint64_t ldyq, void *yk, uint64_t ldyk, hipStream_t stream);
+tk_status tk_head_norm_rotate_backward_f16(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim,
+        uint64_t rotary, float eps, uint32_t flags, const void *dyq, uint64_t lddyq, const void *dyk, uint64_t lddyk,
+        const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q, const void *gamma_k,
+        const void *positions, uint64_t table_rows, const float *cosines, const float *sines, void *dq, uint64_t lddq,
+        void *dk, uint64_t lddk, void *dgamma_q, void *dgamma_k, void *workspace, uint64_t workspace_bytes,
+        hipStream_t stream);
+
+tk_status tk_head_norm_rotate_bf16(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t rotary,
+        float eps, uint32_t flags, const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q,
+        const void *gamma_k, const void *positions, uint64_t table_rows, const float *cosines, const float *sines,
+        void *yq, uint64_t ldyq, void *yk, uint64_t ldyk, hipStream_t stream);
+tk_status tk_head_norm_rotate_backward_bf16(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim,
+        uint64_t rotary, float eps, uint32_t flags, const void *dyq, uint64_t lddyq, const void *dyk, uint64_t lddyk,
+        const void *q, uint64_t ldq, const void *k, uint64_t ldk, const void *gamma_q, const void *gamma_k,
+        const void *positions, uint64_t table_rows, const float *cosines, const float *sines, void *dq, uint64_t lddq,
+        void *dk, uint64_t lddk, void *dgamma_q, void *dgamma_k, void *workspace, uint64_t workspace_bytes,
+        hipStream_t stream);
+
+/* ---- Activation checkpoints in 8 bits --------------------------------------------------
+ * What the backward pass needs of the forward one, kept in a byte an element: a row's columns in blocks
+ * of 128, each with a float scale.  With m = the block's largest |x|:
+ *   scale = m / 127, inverse = 127 / m and t = |x| inverse, each rounded to float;
+ *   code = sign(x) min(127, floor(t) + (u < t - floor(t))),  u = the f32 uniform of word
+ *   start_draw + r * cols + c (Phobos, uniform): rounded up with the chance of its fraction, so that
+ *   code * scale is x on average.  The comparison is exact: equal arguments give equal codes on
+ *   any device.
+ * A block whose m is below 2^-100 is kept as zeros (scale 0); one that holds an infinity or a NaN comes
+ * back as NaN throughout (scale NaN, codes 0).
+ *   tk_checkpoint          x (float with TK_RESIDUAL_F32, the only flag) to codes, rows x cols bytes
+ *                          `ldc` apart, and scales, rows x ceil(cols / 128) contiguous floats
+ *   tk_checkpoint_restore  y = code * scale, rounded once
+ *   tk_layer_norm_backward_checkpoint, tk_dropout_add_layer_norm_backward_checkpoint
+ *                          the backward passes of the row operators with the checkpoint in place of x or
+ *                          sum, its values float; mean and rstd are the forward's
+ * Overlaps, limits and the backward passes' workspace (tk_backward_workspace_bytes) are the row
+ * operators'; codes and scales are in no place of another argument.  start_draw + rows * cols <= 2^32
+ * (tk_checkpoint always), else TK_ERANGE.                                                      */
+tk_status tk_checkpoint_f32(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, uint32_t flags, const void *x,
+        uint64_t ldx, int8_t *codes, uint64_t ldc, float *scales, hipStream_t stream);
+tk_status tk_checkpoint_restore_f32(uint64_t rows, uint64_t cols, uint32_t flags, const int8_t *codes, uint64_t ldc,
+        const float *scales, void *y, uint64_t ldy, hipStream_t stream);
+tk_status tk_layer_norm_backward_checkpoint_f32(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy,
+        uint64_t lddy, const int8_t *codes, uint64_t ldc, const float *scales, const void *gamma, const float *mean,
+        const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_backward_checkpoint_f32(uint32_t key, uint64_t start_draw, uint64_t rows,
+        uint64_t cols, float p, uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds,
+        const int8_t *codes, uint64_t ldc, const float *scales, const void *gamma, const float *mean,
+        const float *rstd, void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma, void *dbeta,
+        void *dbias, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+tk_status tk_checkpoint_f16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, uint32_t flags, const void *x,
+        uint64_t ldx, int8_t *codes, uint64_t ldc, float *scales, hipStream_t stream);
+tk_status tk_checkpoint_restore_f16(uint64_t rows, uint64_t cols, uint32_t flags, const int8_t *codes, uint64_t ldc,
+        const float *scales, void *y, uint64_t ldy, hipStream_t stream);
+tk_status tk_layer_norm_backward_checkpoint_f16(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy,
+        uint64_t lddy, const int8_t *codes, uint64_t ldc, const float *scales, const void *gamma, const float *mean,
+        const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_backward_checkpoint_f16(uint32_t key, uint64_t start_draw, uint64_t rows,
+        uint64_t cols, float p, uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds,
+        const int8_t *codes, uint64_t ldc, const float *scales, const void *gamma, const float *mean,
+        const float *rstd, void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma, void *dbeta,
+        void *dbias, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+tk_status tk_checkpoint_bf16(uint32_t key, uint64_t start_draw, uint64_t rows, uint64_t cols, uint32_t flags, const void *x,
+        uint64_t ldx, int8_t *codes, uint64_t ldc, float *scales, hipStream_t stream);
+tk_status tk_checkpoint_restore_bf16(uint64_t rows, uint64_t cols, uint32_t flags, const int8_t *codes, uint64_t ldc,
+        const float *scales, void *y, uint64_t ldy, hipStream_t stream);
+tk_status tk_layer_norm_backward_checkpoint_bf16(uint64_t rows, uint64_t cols, uint32_t flags, const void *dy,
+        uint64_t lddy, const int8_t *codes, uint64_t ldc, const float *scales, const void *gamma, const float *mean,
+        const float *rstd, void *dx, uint64_t lddx, void *dgamma, void *dbeta, void *workspace,
+        uint64_t workspace_bytes, hipStream_t stream);
+tk_status tk_dropout_add_layer_norm_backward_checkpoint_bf16(uint32_t key, uint64_t start_draw, uint64_t rows,
+        uint64_t cols, float p, uint32_t flags, const void *dy, uint64_t lddy, const void *dsum, uint64_t ldds,
+        const int8_t *codes, uint64_t ldc, const float *scales, const void *gamma, const float *mean,
+        const float *rstd, void *dx, uint64_t lddx, void *dresidual, uint64_t lddr, void *dgamma, void *dbeta,
+        void *dbias, void *workspace, uint64_t workspace_bytes, hipStream_t stream);
+
 /* ---- Weighted choice through an alias table -----------------------------------------
  * tandem-sycl, "Design", §Fills: the choice fill maps each 64-bit draw through an alias
  * table.  tk_alias_create builds the table on the host from n >= 1 finite, non-negative
