@@ -53,6 +53,7 @@ __global__ __launch_bounds__(256) void k_embedding(LookupArgs a) {
 struct SortArgs {
   const void *ids;
   uint32_t *order;  // the rows with a token, by token and then by row
+  uint32_t *run;    // at a token's first place in `order` the number of its rows, else 0
   uint32_t *first;  // where each token's rows begin in `order`, and at [vocab] where they end
   uint32_t rows, vocab, ranges;
   bool ids64;
@@ -61,15 +62,42 @@ struct SortArgs {
 constexpr uint32_t kNoToken = ~0u;
 constexpr int kSortWaves = 16, kAhead = 8;
 
+// The lanes whose number below kRange is this lane's, among those of `mask`: a vote for each bit.
+template <int kRange>
+__device__ __forceinline__ uint64_t same_lanes(uint32_t n, uint64_t mask) {
+  uint32_t lo = (uint32_t)mask, hi = (uint32_t)(mask >> 32);
+#pragma unroll
+  for (int b = 0; (1 << b) < kRange; ++b) {
+    const uint64_t set = __ballot((n >> b) & 1);
+    const uint32_t mine = (uint32_t)((int)(n << (31 - b)) >> 31);  // this lane's bit in all of them
+    lo &= ~((uint32_t)set ^ mine);
+    hi &= ~((uint32_t)(set >> 32) ^ mine);
+  }
+  return (uint64_t)hi << 32 | lo;
+}
+
+// Counts that a wave's lanes read and its first lanes of each token write, in this order: a wave's LDS
+// accesses are not reordered.
+__device__ __forceinline__ uint32_t get_count(uint32_t *p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+}
+__device__ __forceinline__ void set_count(uint32_t *p, uint32_t n) {
+  __hip_atomic_store(p, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+}
+
 // A work-group takes a range of kRange tokens and reads all rows' tokens, which lie in the L2s:
 // it needs nothing from the other ones, since the rows of lower tokens that it passes say where its
 // own begin.  Each wave reads a sixteenth of the rows, in their order, twice: it counts its tokens
 // in a column of its own, and after a scan over tokens and waves it puts its rows in their places.
 // Rows of one token keep their order, whatever the waves do, so a gradient's sum has one order.
+// The lanes of one token find each other by votes, and the first of them counts for all: texts have
+// half of their tokens in the range of the lowest ones (16384 rows: with a turn of a loop for each of
+// a wave's tokens 82 us).
 template <int kRange>
 __global__ __launch_bounds__(64 * kSortWaves) void k_sort_tokens(SortArgs a) {
-  __shared__ uint32_t count[kSortWaves][kRange], part[kSortWaves], under[kSortWaves];
+  __shared__ uint32_t count[kSortWaves][kRange], begin_of[kRange], total_of[kRange], part[kSortWaves], under[kSortWaves];
   const uint32_t lane = threadIdx.x & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint64_t under_me = (1ull << lane) - 1;
   const uint32_t piece = ((a.rows + kSortWaves * 64 - 1) / (kSortWaves * 64)) * 64;
   const uint32_t begin = wave * piece, end = begin + piece < a.rows ? begin + piece : a.rows;
   const auto load = [&](uint32_t i) -> uint32_t {  // the token of row i, or none
@@ -109,6 +137,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort_tokens(SortArgs a) {
     for (int w = 0; w < kSortWaves; ++w) base += under[w] + (w < (int)wave ? part[w] : 0);
     if (threadIdx.x < kRange) {
       uint32_t at = base + upto - total;
+      begin_of[threadIdx.x] = at;
+      total_of[threadIdx.x] = total;
       if (lo + threadIdx.x < a.vocab) a.first[lo + threadIdx.x] = at;
       if (lo + threadIdx.x + 1 == a.vocab) a.first[a.vocab] = at + total;
       for (int w = 0; w < kSortWaves; ++w) {
@@ -124,16 +154,16 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort_tokens(SortArgs a) {
       for (int k = 0; k < kAhead; ++k) t[k] = load(at + 64 * k + lane);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        uint64_t left = __ballot(t[k] - lo < kRange);
-        while (left) {  // the rows of one token at a time, the first lane's
-          const int leader = __ffsll((unsigned long long)left) - 1;
-          const uint32_t mine = (uint32_t)__builtin_amdgcn_readlane((int)t[k], leader);
-          const uint64_t same = __ballot(t[k] == mine);
-          uint32_t put = 0;
-          if (lane == (uint32_t)leader) put = atomicAdd(&count[wave][mine - lo], (uint32_t)__popcll(same));
-          put = (uint32_t)__builtin_amdgcn_readlane((int)put, leader);
-          if (t[k] == mine) a.order[put + __popcll(same & ((1ull << lane) - 1))] = at + 64 * k + lane;
-          left &= ~same;
+        const uint32_t own = t[k] - lo;
+        const uint64_t mine = __ballot(own < kRange);
+        if (mine) {
+          const uint64_t same = same_lanes<kRange>(own, mine);
+          if (own < kRange) {
+            const uint32_t put = get_count(&count[wave][own]), place = put + (uint32_t)__popcll(same & under_me);
+            if ((same & under_me) == 0) set_count(&count[wave][own], put + (uint32_t)__popcll(same));
+            a.order[place] = at + 64 * k + lane;
+            a.run[place] = place == begin_of[own] ? total_of[own] : 0;
+          }
         }
       }
     }
@@ -146,54 +176,36 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_sort_tokens(SortArgs a) {
 // ---------------------------------------------------------------------------------------
 struct GradArgs {
   const void *ids, *dy;
-  const uint32_t *order, *first;
+  const uint32_t *order, *run, *first;
   void *dtable;
   float *partial;  // two lines to a tile of `order`
-  uint64_t lddy, lddt;
-  uint32_t rows, vocab, cols, tile, tiles, strips, hot_groups;
+  uint64_t lddy, lddt, units, strips, blocks;  // units: tiles times strips; blocks: work-groups' worth of work
+  uint32_t rows, vocab, cols, tile, tiles;
+  uint32_t clear_lanes;  // lanes that clear a row whose token does not occur (0: none are cleared)
   float scale;
   bool ids64;
   Drop drop;
 };
 
-// A token of up to `tile` rows is summed by the group of lanes that writes its gradient.  Of one with
-// more, its parts between the multiples of `tile` in `order` are summed by a group each, to a line of
-// the workspace, and k_join adds the lines: a text's most frequent token has a tenth of the rows.
-// A tile holds at most two such parts: of a token that begins before it (its first line) and of one
-// that begins in it (its second).
+// A group of lanes takes a tile, `tile` places of `order` after each other, and a strip of columns: all
+// have the same work, whether a text's most frequent token has a tenth of the rows or every row has
+// a token of its own.  It reads the rows ahead of adding them, and where a token ends writes its
+// gradient.  Of a token that goes past an end of the tile it writes the sum so far, to a line of the
+// workspace: the tile's first line if the token begins before the tile, else its second.  k_join adds
+// those lines up in the order of the tiles.
 template <class W, class R, bool kDivide, bool kAdd, int CH, int kLanes>
-struct Sums {
+struct Tile {
+  static constexpr int kDeep = 4;
   const GradArgs &a;
   uint32_t c, lane;  // this lane's first column, and its place in the group
   int nv;
 
-  // drop(dy) of the rows order[from .. to), added up in that order
-  __device__ __forceinline__ void rows(uint32_t from, uint32_t to, float *acc) const {
-    constexpr int kDeep = 4;
-#pragma unroll
-    for (int e = 0; e < CH; ++e) acc[e] = 0.0f;
-    const uint32_t at = chunk_at<CH>(c, a.cols);
-    for (uint32_t i = from; i < to; i += kDeep) {
-      Chunk<R, CH> x[kDeep];
-      uint32_t r[kDeep];
-#pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        r[k] = a.order[i + k < to ? i + k : to - 1];
-        if (kLanes == 64) r[k] = (uint32_t)__builtin_amdgcn_readfirstlane(r[k]);
-      }
-#pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        if (i + k < to) x[k] = load_chunk<false, CH>((const R *)a.dy + r[k] * a.lddy + at);
-#pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        if (i + k < to) {
-          float v[CH];
-          unpack<CH, R>(x[k], nv, v);
-          if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + r[k] * a.cols + c, v);
-#pragma unroll
-          for (int e = 0; e < CH; ++e) acc[e] += v[e];
-        }
-    }
+  // A value that the lane of place i holds.
+  __device__ __forceinline__ uint32_t of_place(uint32_t v, uint32_t i) const {
+    return kLanes == 64 ? (uint32_t)__builtin_amdgcn_readlane((int)v, (int)i) : (uint32_t)__shfl((int)v, (int)i, kLanes);
+  }
+  __device__ __forceinline__ Chunk<R, CH> load(uint32_t row) const {
+    return load_chunk<false, CH>((const R *)a.dy + row * a.lddy + chunk_at<CH>(c, a.cols));
   }
   __device__ __forceinline__ void write(uint32_t id, float *acc) const {
     W *p = (W *)a.dtable + id * a.lddt;
@@ -207,104 +219,151 @@ struct Sums {
     }
     store_chunk<CH>(p + c, nv, acc);
   }
-  // One of the vocabulary's tokens, or (adding to what is there) the token that begins at a place
-  // of `order`, so that nothing is looked up for the tokens that do not occur.
-  __device__ __forceinline__ void cold(uint32_t n) const {
-    uint32_t id = n;
-    if (kAdd) {
-      if (n >= a.first[a.vocab]) return;
-      id = (uint32_t)token(a.ids, a.ids64, a.order[n]);
-    }
-    const uint32_t s = a.rows ? a.first[id] : 0, e = a.rows ? a.first[id + 1] : 0;
-    if (e - s > a.tile || (kAdd && s != n)) return;
-    float acc[CH];
-    rows(s, e, acc);
-    write(id, acc);
+  __device__ __forceinline__ void put_line(uint32_t t, int line, const float *acc) const {
+    put_sums<CH>(a.partial + (2ull * t + line) * line_pitch(a.cols) + c, nv, acc);
   }
-  __device__ __forceinline__ void hot(uint32_t t) const {
-    const uint32_t all = a.first[a.vocab], from = t * a.tile;
-    if (from >= all) return;
-    const uint32_t to = all - from < a.tile ? all : from + a.tile;
+  __device__ __forceinline__ void run(uint32_t t) const {
+    const uint32_t all = a.first[a.vocab], t0 = t * a.tile;
+    if (t0 >= all) return;
+    const uint32_t n = all - t0 < a.tile ? all - t0 : a.tile, place = t0 + (lane < n ? lane : n - 1);
+    const uint32_t row = a.order[place];
+    const bool ends = place + 1 == all || a.run[place + 1] != 0;
+    bool whole = a.run[t0] != 0;  // the token began in this tile
+    const uint32_t id = (uint32_t)token(a.ids, a.ids64, row);
+    const uint64_t end_mask = __ballot(ends);
+    Chunk<R, CH> x[kDeep];
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k)
+      if ((uint32_t)k < n) x[k] = load(of_place(row, k));
     float acc[CH];
-    const auto part = [&](uint32_t id, int line) {
-      const uint32_t s = a.first[id], e = a.first[id + 1];
-      if (e - s <= a.tile || (s < from) != (line == 0)) return;
-      rows(s < from ? from : s, e < to ? e : to, acc);
-      put_sums<CH>(a.partial + (2ull * t + line) * line_pitch(a.cols) + c, nv, acc);
-    };
-    part((uint32_t)token(a.ids, a.ids64, a.order[from]), 0);
-    part((uint32_t)token(a.ids, a.ids64, a.order[to - 1]), 1);
+#pragma unroll
+    for (int e = 0; e < CH; ++e) acc[e] = 0.0f;
+    for (uint32_t i0 = 0; i0 < n; i0 += kDeep) {
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const uint32_t i = i0 + k;
+        if (i >= n) break;
+        float v[CH];
+        unpack<CH, R>(x[k], nv, v);
+        if (i + kDeep < n) x[k] = load(of_place(row, i + kDeep));
+        if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + of_place(row, i) * a.cols + c, v);
+#pragma unroll
+        for (int e = 0; e < CH; ++e) acc[e] += v[e];
+        const bool end = kLanes == 64 ? (end_mask >> i) & 1 : of_place(ends, i) != 0;
+        if (!end) continue;
+        if (whole) write(of_place(id, i), acc);
+        else put_line(t, 0, acc);
+        whole = true;
+#pragma unroll
+        for (int e = 0; e < CH; ++e) acc[e] = 0.0f;
+      }
+    }
+    if (!(kLanes == 64 ? (end_mask >> (n - 1)) & 1 : of_place(ends, n - 1) != 0)) put_line(t, whole ? 1 : 0, acc);
   }
 };
 
+// `lanes` lanes clear n bytes, whole elements of `size`: vectors between the 16-byte boundaries.
+__device__ __forceinline__ void clear_row(char *p, uint64_t n, uint32_t size, uint32_t lane, uint32_t lanes) {
+  typedef uint32_t V4 __attribute__((ext_vector_type(4)));
+  uint64_t head = (16 - ((uintptr_t)p & 15)) & 15;
+  head = head < n ? head : n;
+  const uint64_t vectors = (n - head) / 16, tail = head + vectors * 16;
+  const auto one = [&](uint64_t at) {
+    if (size == 4) *(uint32_t *)(p + at) = 0;
+    else *(uint16_t *)(p + at) = 0;
+  };
+  if (lane * size < head) one(lane * size);
+  if (tail + lane * size < n) one(tail + lane * size);
+  for (uint64_t i = lane; i < vectors; i += lanes) __builtin_nontemporal_store(V4(0), (V4 *)(p + head) + i);
+}
+
+// Work-groups of four waves.  The tiles come first: the rows to clear, whose stores wait for nothing,
+// fill the time that the tiles wait for their loads.
 template <class W, class R, bool kDivide, bool kAdd, int CH, int kLanes>
 __global__ __launch_bounds__(256) void k_token_sums(GradArgs a) {
   constexpr uint32_t kGroups = 256 / kLanes;
   uint32_t group = threadIdx.x / kLanes;
   if (kLanes == 64) group = (uint32_t)__builtin_amdgcn_readfirstlane(group);
-  const uint32_t lane = threadIdx.x % kLanes, units = kAdd ? a.rows : a.vocab, groups = (units + kGroups - 1) / kGroups;
-  for (uint32_t strip = blockIdx.x; strip < a.strips; strip += gridDim.x) {
-    const uint32_t c = (strip * kLanes + lane) * CH;
-    if (c >= a.cols) continue;
-    const Sums<W, R, kDivide, kAdd, CH, kLanes> sums{a, c, lane, (int)(a.cols - c)};
-    for (uint32_t g = blockIdx.y; g < a.hot_groups + groups; g += gridDim.y) {
-      if (g < a.hot_groups) {
-        const uint32_t t = g * kGroups + group;
-        if (t < a.tiles) sums.hot(t);
-      } else {
-        const uint32_t n = (g - a.hot_groups) * kGroups + group;
-        if (n < units) sums.cold(n);
-      }
+  const uint64_t sums = (a.units + kGroups - 1) / kGroups;
+  for (uint64_t block = blockIdx.x; block < a.blocks; block += gridDim.x) {
+    if (block < sums) {
+      const uint64_t unit = block * kGroups + group;
+      if (unit >= a.units) continue;
+      const uint32_t t = (uint32_t)(unit / a.strips), strip = (uint32_t)(unit - t * a.strips), lane = threadIdx.x % kLanes;
+      const uint32_t c = (strip * kLanes + lane) * CH;
+      Tile<W, R, kDivide, kAdd, CH, kLanes>{a, c, lane, (int)(a.cols - c)}.run(t);
+    } else {
+      const uint32_t lane = threadIdx.x % a.clear_lanes;
+      const uint64_t id = (block - sums) * (256 / a.clear_lanes) + threadIdx.x / a.clear_lanes;
+      if (id < a.vocab && (!a.first || a.first[id] == a.first[id + 1]))
+        clear_row((char *)((W *)a.dtable + id * a.lddt), (uint64_t)a.cols * sizeof(W), sizeof(W), lane, a.clear_lanes);
     }
   }
 }
 
-// The tokens of more than `tile` rows: their lines, in order.  blockIdx.y: the tile where one begins.
+// The tokens that go past the end of the tile where they begin, blockIdx.y: their lines, in order.
 template <class W, bool kAdd>
 __global__ __launch_bounds__(256) void k_join(GradArgs a) {
-  const uint32_t all = a.first[a.vocab], t = blockIdx.y, from = t * a.tile;
-  if (from >= all) return;
-  const uint32_t to = all - from < a.tile ? all : from + a.tile;
-  const uint32_t id = (uint32_t)token(a.ids, a.ids64, a.order[to - 1]), s = a.first[id], e = a.first[id + 1];
-  if (e - s <= a.tile || s < from) return;
   const uint64_t pitch = line_pitch(a.cols);
-  const uint32_t last = (e - 1) / a.tile;
-  for (uint64_t c = blockIdx.x * 256ull + threadIdx.x; c < a.cols; c += gridDim.x * 256ull) {
-    const float *p = a.partial + 2ull * t * pitch + c;
-    float sum = p[pitch];
-    for (uint32_t k = t + 1; k <= last; k += 8) {
-      float v[8];
+  const uint32_t all = a.first[a.vocab], lane = threadIdx.x & 63;
+  for (uint32_t t = blockIdx.y; t < a.tiles; t += gridDim.y) {
+    const uint32_t t0 = t * a.tile, t1 = t0 + a.tile;
+    if (t1 >= all) return;
+    const uint64_t begins = __ballot(lane < a.tile && a.run[t0 + (lane < a.tile ? lane : 0)] != 0);
+    if (!begins) continue;
+    const uint32_t begin = t0 + 63 - (uint32_t)__clzll((long long)begins), end = begin + a.run[begin];
+    if (end <= t1) continue;
+    const uint32_t last = (end - 1) / a.tile;
+    W *out = (W *)a.dtable + (uint32_t)token(a.ids, a.ids64, a.order[begin]) * a.lddt;
+    for (uint64_t c = blockIdx.x * 256ull + threadIdx.x; c < a.cols; c += gridDim.x * 256ull) {
+      const float *p = a.partial + 2ull * t * pitch + c;
+      float sum = p[pitch];
+      for (uint32_t k = t + 1; k <= last; k += 8) {
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[2ull * ((k + j < last ? k + j : last) - t) * pitch];
+        for (int j = 0; j < 8; ++j) v[j] = p[2ull * ((k + j < last ? k + j : last) - t) * pitch];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum += k + j <= last ? v[j] : 0.0f;
+        for (int j = 0; j < 8; ++j) sum += k + j <= last ? v[j] : 0.0f;
+      }
+      sum *= a.scale;
+      out[c] = (W)(kAdd ? sum + (float)out[c] : sum);
     }
-    W *out = (W *)a.dtable + id * a.lddt + c;
-    sum *= a.scale;
-    *out = (W)(kAdd ? sum + (float)*out : sum);
   }
 }
 
 // ---------------------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------------------
-// Rows of `order` to a tile: 64, and more where that makes over 1024 tiles.
-constexpr uint64_t kLeastTile = 64, kMostTiles = 1024;
+// Places to a tile: 8, 16, 32 or 64, the most that leave kUnits waves' work (and no more than the lanes of
+// a strip, which hold them).
+constexpr uint64_t kUnits = 4096;
 
-static uint32_t tile_of(uint64_t rows) {
-  uint64_t t = kLeastTile;
-  while ((rows + t - 1) / t > kMostTiles) t *= 2;
-  return (uint32_t)t;
-}
-
-static uint64_t most_tiles(uint64_t rows) {
-  const uint64_t t = (rows + kLeastTile - 1) / kLeastTile;
-  return rows <= kLeastTile ? 0 : t < kMostTiles ? t : kMostTiles;  // a single tile has no token of more rows
-}
+struct TilePlan {
+  uint64_t tile = 8, strips, least;  // least: tiles that make kUnits
+  uint32_t lanes;
+  TilePlan(uint64_t rows, uint64_t cols, uint64_t chunk) {
+    const uint64_t ch = cols < chunk ? 1 : chunk;
+    lanes = cols <= 8 * ch ? 8 : cols <= 16 * ch ? 16 : cols <= 32 * ch ? 32 : 64;
+    strips = (cols + lanes * ch - 1) / (lanes * ch);
+    least = (kUnits * 64 / lanes + strips - 1) / strips;
+    while (tile < lanes && rows >= 2 * tile * least) tile *= 2;
+  }
+  uint64_t tiles(uint64_t rows) const { return (rows + tile - 1) / tile; }
+  // The most tiles that any number of rows up to this one makes: below 2 * least where a wider tile follows.
+  uint64_t room(uint64_t rows) const {
+    const uint64_t n = tiles(rows);
+    return tile > 8 && n < 2 * least ? 2 * least : n;
+  }
+};
 
 static uint64_t embedding_bytes(uint64_t rows, uint64_t cols, uint64_t vocab) {
   if (rows == 0 || cols == 0 || vocab == 0) return 0;
-  return 4 * (rows + vocab + 1) + 8 * most_tiles(rows) * line_pitch(cols) + 12;  // 12: the lines are aligned to 16 bytes
+  uint64_t room = 0;
+  for (uint64_t chunk = 4; chunk <= 8; chunk += 4) {  // one size serves every type
+    const uint64_t n = TilePlan(rows, cols, chunk).room(rows);
+    room = n > room ? n : room;
+  }
+  return 4 * (2 * rows + vocab + 1) + 8 * room * line_pitch(cols) + 12;  // 12: the lines are aligned to 16 bytes
 }
 
 template <class W, class R, bool kDivide>
@@ -331,24 +390,34 @@ struct Embedding {
   template <bool kAdd, int ch, int kLanes>
   static void launch_sums(GradArgs a, hipStream_t s) {
     constexpr uint32_t kGroups = 256 / kLanes;
-    const uint64_t units = kAdd ? a.rows : a.vocab, groups = (units + kGroups - 1) / kGroups;
-    a.strips = (uint32_t)(((uint64_t)a.cols + kLanes * ch - 1) / (kLanes * ch));
-    a.hot_groups = (a.tiles + kGroups - 1) / kGroups;
-    const uint64_t g = a.hot_groups + groups;
-    hipLaunchKernelGGL((k_token_sums<W, R, kDivide, kAdd, ch, kLanes>),
-                       dim3(a.strips < 1u << 16 ? a.strips : 1u << 16, (uint32_t)(g < 32768 ? g : 32768)), dim3(256), 0, s, a);
+    a.blocks = (a.units + kGroups - 1) / kGroups;
+    if (!kAdd) {
+      // two vectors to a lane, where a row is that long
+      const uint64_t vectors = (uint64_t)a.cols * sizeof(W) / 16;
+      a.clear_lanes = 8;
+      while (a.clear_lanes < 256 && a.clear_lanes * 2 < vectors) a.clear_lanes *= 2;
+      a.blocks += ((uint64_t)a.vocab + 256 / a.clear_lanes - 1) / (256 / a.clear_lanes);
+    }
+    const uint64_t most = 1ull << 23;  // a launch holds fewer than 2^32 threads
+    hipLaunchKernelGGL((k_token_sums<W, R, kDivide, kAdd, ch, kLanes>), dim3((uint32_t)(a.blocks < most ? a.blocks : most)),
+                       dim3(256), 0, s, a);
   }
   template <bool kAdd>
-  static tk_status sums(const GradArgs &a, hipStream_t s) {
+  static tk_status sums(GradArgs a, hipStream_t s) {
+    const TilePlan p(a.rows, a.cols, CH);
+    a.tile = (uint32_t)p.tile;
+    a.tiles = (uint32_t)p.tiles(a.rows);
+    a.strips = p.strips;
+    a.units = a.tiles * p.strips;
     if (a.cols < (uint32_t)CH) launch_sums<kAdd, 1, 8>(a, s);
-    else if (a.cols <= 8u * CH) launch_sums<kAdd, CH, 8>(a, s);
-    else if (a.cols <= 16u * CH) launch_sums<kAdd, CH, 16>(a, s);
-    else if (a.cols <= 32u * CH) launch_sums<kAdd, CH, 32>(a, s);
+    else if (p.lanes == 8) launch_sums<kAdd, CH, 8>(a, s);
+    else if (p.lanes == 16) launch_sums<kAdd, CH, 16>(a, s);
+    else if (p.lanes == 32) launch_sums<kAdd, CH, 32>(a, s);
     else launch_sums<kAdd, CH, 64>(a, s);
-    tk_status st = launch_status();
-    if (st != TK_OK || a.tiles == 0) return st;
+    const tk_status st = launch_status();
+    if (st != TK_OK || a.tiles <= 1) return st;
     const uint32_t blocks = (a.cols + 255) / 256;
-    hipLaunchKernelGGL((k_join<W, kAdd>), dim3(blocks < 1024 ? blocks : 1024, a.tiles), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_join<W, kAdd>), dim3(blocks < 1024 ? blocks : 1024, a.tiles < 8192 ? a.tiles : 8192), dim3(256), 0, s, a);
     return launch_status();
   }
   static tk_status backward(const GradArgs &a, bool add, hipStream_t s) { return add ? sums<true>(a, s) : sums<false>(a, s); }
@@ -432,13 +501,10 @@ static tk_status embedding_backward(RowType t, uint32_t key, uint64_t start, uin
   a.rows = (uint32_t)rows; a.vocab = (uint32_t)vocab; a.cols = (uint32_t)cols; a.scale = scale;
   a.drop = drop_of(key, start, p);
   if (rows) {
-    uint32_t *order = (uint32_t *)workspace, *first = order + rows;
-    a.order = order;
-    a.first = first;
+    uint32_t *order = (uint32_t *)workspace, *run = order + rows, *first = run + rows;
+    a.order = order; a.run = run; a.first = first;
     a.partial = (float *)(((uintptr_t)(first + vocab + 1) + 15) & ~(uintptr_t)15);
-    a.tile = tile_of(rows);
-    a.tiles = rows <= a.tile ? 0 : (uint32_t)((rows + a.tile - 1) / a.tile);
-    if ((st = sort_tokens(SortArgs{ids, order, first, a.rows, a.vocab, 0, a.ids64}, stream)) != TK_OK) return st;
+    if ((st = sort_tokens(SortArgs{ids, order, run, first, a.rows, a.vocab, 0, a.ids64}, stream)) != TK_OK) return st;
   }
   return with_types(t, flags, [&](auto k) { return k.backward(a, add, stream); });
 }
