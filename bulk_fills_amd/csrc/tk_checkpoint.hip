@@ -15,16 +15,17 @@ struct CodeArgs {
   Divisor per_row;  // chunks_per_row
 };
 
-constexpr int kCodes = 8;  // codes of a lane, so that sixteen lanes hold a block
+constexpr int kCodes = 8;  // codes of a lane of k_restore
+constexpr int kPack = 16;  // elements of a lane of k_checkpoint: eight lanes hold a block
 
-// nv of a lane's elements, the others 0: fewer than all are loaded one by one.
-template <class R>
+// nv of a lane's N elements, the others 0: fewer than all are loaded one by one.
+template <int N, class R>
 __device__ __forceinline__ void load_lane(const R *p, int nv, float *v) {
-  if (nv >= kCodes) {
-    unpack<kCodes, R>(load_chunk<true, kCodes>(p), kCodes, v);
+  if (nv >= N) {
+    unpack<N, R>(load_chunk<true, N>(p), N, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < kCodes; ++e) v[e] = e < nv ? (float)p[e] : 0.0f;
+    for (int e = 0; e < N; ++e) v[e] = e < nv ? (float)p[e] : 0.0f;
   }
 }
 
@@ -32,50 +33,130 @@ __device__ __forceinline__ void load_lane(const R *p, int nv, float *v) {
 // scale normal.
 constexpr float kLeastHeld = 0x1p-100f;
 
+// m / 127 to the nearest: a product with the rounded reciprocal and one correction, which is enough
+// for a reciprocal that is itself the nearest (m at least kLeastHeld: nothing is subnormal).
+__device__ __forceinline__ float over_127(float m) {
+  const float r = 1.0f / 127.0f, q = m * r;
+  return __builtin_fmaf(__builtin_fmaf(-q, 127.0f, m), r, q);
+}
+
+// floor(-x), and a << 1 plus b.
+__device__ __forceinline__ int floor_of_negative(float x) {
+  int n;
+  asm("v_cvt_flr_i32_f32_e64 %0, -%1" : "=v"(n) : "v"(x));
+  return n;
+}
+__device__ __forceinline__ uint32_t twice_and(uint32_t a, uint32_t b) {
+  uint32_t n;
+  asm("v_lshl_add_u32 %0, %1, 1, %2" : "=v"(n) : "v"(a), "v"(b));
+  return n;
+}
+
+// Four codes from numbers that hold -|code| in their highest byte: those of negative elements (0xFF in
+// `sign`) are the bytes themselves.  With the sign bit turned a byte is 128 - |code|, so that four are
+// subtracted from 128 at once and none borrows.
+__device__ __forceinline__ uint32_t four_codes(const uint32_t *n, uint32_t sign) {
+  const uint32_t low = __builtin_amdgcn_perm(n[1], n[0], 0x0C0C0703), high = __builtin_amdgcn_perm(n[3], n[2], 0x07030C0C);
+  const uint32_t negative = low | high, positive = 0x80808080u - (negative ^ 0x80808080u);
+  return (negative & sign) | (positive & ~sign);
+}
+
+// A lane's elements as they are kept: their values, the largest magnitude's bits as a float's, and
+// 0xFF in the byte of each negative one of four.
+template <class R>
+struct Lane {
+  float x[kPack];
+  __device__ __forceinline__ void load(const R *p, int nv) { load_lane<kPack, R>(p, nv, x); }
+  __device__ __forceinline__ float value(int e) const { return x[e]; }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int e = 0; e < kPack; ++e) {
+      const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+      t = b > t ? b : t;
+    }
+    return t;
+  }
+  __device__ __forceinline__ uint32_t signs(int e) const {
+    const uint32_t low = __builtin_amdgcn_perm(__float_as_uint(x[e + 1]), __float_as_uint(x[e]), 0x0C0C0B09);
+    return low | __builtin_amdgcn_perm(__float_as_uint(x[e + 3]), __float_as_uint(x[e + 2]), 0x0B090C0C);
+  }
+};
+
+// bfloat16: two elements to a register, whose magnitudes compare as 16-bit numbers.
+template <>
+struct Lane<bf16_t> {
+  typedef uint32_t Pairs __attribute__((ext_vector_type(kPack / 2), aligned(2)));
+  Pairs x;
+  __device__ __forceinline__ void load(const bf16_t *p, int nv) {
+    if (nv >= kPack) {
+      x = __builtin_nontemporal_load((const Pairs *)p);
+    } else {
+      const uint16_t *q = (const uint16_t *)p;
+#pragma unroll
+      for (int e = 0; e < kPack; e += 2) x[e / 2] = (e < nv ? (uint32_t)q[e] : 0u) | (e + 1 < nv ? (uint32_t)q[e + 1] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ float value(int e) const {
+    return __uint_as_float(e % 2 ? x[e / 2] & 0xFFFF0000u : x[e / 2] << 16);
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    typedef uint16_t Two __attribute__((ext_vector_type(2)));
+    Two t = 0;
+#pragma unroll
+    for (int i = 0; i < kPack / 2; ++i) t = __builtin_elementwise_max(t, __builtin_bit_cast(Two, x[i] & 0x7FFF7FFFu));
+    return (uint32_t)(t[0] > t[1] ? t[0] : t[1]) << 16;
+  }
+  __device__ __forceinline__ uint32_t signs(int e) const {
+    return __builtin_amdgcn_perm(x[e / 2 + 1], x[e / 2], 0x0B0A0908);
+  }
+};
+
 // The float |x| times the float 127 / m lies on a grid that t - floor(t) is exact on, so a code is a
-// comparison of two exact numbers: any evaluation of the definition gives the same one.  The largest
-// magnitude is taken among the bit patterns, where NaN is above infinity.
+// comparison of two exact numbers: any evaluation of the definition gives the same one.  Here, with
+// k = u 2^23 and N = floor(-t 2^24), -|code| = floor((N + 2 k) / 2^24): that is -floor(t) - 1 where 2 k is
+// below ceil(t 2^24) - 2^24 floor(t), so below t's fraction, and -floor(t) elsewhere.
+// The largest magnitude is taken among the bit patterns, where NaN is above infinity.
+//
+// Bound by its instructions: 3 bytes move for every element.  Sixteen elements to a lane share what
+// a lane does once.
 template <class R>
 __global__ __launch_bounds__(256) void k_checkpoint(CodeArgs a) {
   const uint32_t n = blockIdx.x * 256u + threadIdx.x;
-  if (n >= a.chunks) return;  // whole blocks of sixteen lanes
-  const uint32_t r = a.per_row.of(n), k = n - r * a.chunks_per_row, c = k * kCodes;
+  if (n >= a.chunks) return;  // whole blocks of eight lanes
+  const uint32_t r = a.per_row.of(n), k = n - r * a.chunks_per_row, c = k * kPack;
   const uint64_t row = a.row0 + r;
   const int nv = (int)(a.cols - c);
-  float x[kCodes];
-  load_lane<R>((const R *)a.x + row * a.ldx + c, nv, x);
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < kCodes; ++e) {
-    const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-    top = b > top ? b : top;
-  }
+  Lane<R> x;
+  x.load((const R *)a.x + row * a.ldx + c, nv);
+  uint32_t top = x.top();
   const auto larger = [&](uint32_t o) { top = o > top ? o : top; };
   larger(__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));   // quad_perm 1,0,3,2
   larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));   // quad_perm 2,3,0,1
   larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xF, 0xF, true));  // row_half_mirror
-  larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x140, 0xF, 0xF, true));  // row_mirror
   const float m = __uint_as_float(top);
   const bool finite = top < 0x7F800000u, held = finite && m >= kLeastHeld;
-  const float inverse = held ? __fdiv_rn(127.0f, m) : 0.0f;
-  if (k % 16 == 0) a.scales[row * a.blocks + k / 16] = !finite ? __uint_as_float(0x7FC00000u) : held ? __fdiv_rn(m, 127.0f) : 0.0f;
+  if (k % 8 == 0) a.scales[row * a.blocks + k / 8] = !finite ? __uint_as_float(0x7FC00000u) : held ? over_127(m) : 0.0f;
   if (nv <= 0) return;
-  uint32_t w[kCodes];
-  chunk_words<kCodes>(a.hk, a.start + (uint32_t)row * a.cols + c, w);
-  Chunk<int8_t, kCodes> code;
+  const float inverse = held ? __fdiv_rn(127.0f, m) : 0.0f;
+  uint32_t w[kPack];
+  chunk_words<kPack>(a.hk, a.start + (uint32_t)row * a.cols + c, w);
 #pragma unroll
-  for (int e = 0; e < kCodes; ++e) {
-    const float t = held ? __builtin_fabsf(x[e]) * inverse : 0.0f, down = __builtin_floorf(t);
-    const float up = tk_unit23(w[e]) < t - down ? 1.0f : 0.0f;
-    code[e] = (int8_t)__builtin_copysignf(fminf(down + up, 127.0f), x[e]);
+  for (int e = 0; e < kPack; ++e) {
+    const float t = __builtin_fabsf(x.value(e)) * inverse;
+    w[e] = twice_and(w[e] & 0x7FFFFFu, (uint32_t)floor_of_negative(fminf(t * 0x1p24f, 127.0f * 0x1p24f)));
   }
+  typedef uint32_t Codes __attribute__((ext_vector_type(kPack / 4), aligned(1)));
+  Codes code;
+#pragma unroll
+  for (int e = 0; e < kPack; e += 4) code[e / 4] = finite ? four_codes(w + e, x.signs(e)) : 0;
   int8_t *out = a.codes + row * a.ldc + c;
-  if (nv >= kCodes) {
-    __builtin_nontemporal_store(code, (Chunk<int8_t, kCodes> *)out);
+  if (nv >= kPack) {
+    __builtin_nontemporal_store(code, (Codes *)out);
   } else {
 #pragma unroll
-    for (int e = 0; e < kCodes; ++e)
-      if (e < nv) out[e] = code[e];
+    for (int e = 0; e < kPack; ++e)
+      if (e < nv) out[e] = (int8_t)(code[e / 4] >> (8 * (e % 4)));
   }
 }
 
@@ -87,7 +168,7 @@ __global__ __launch_bounds__(256) void k_restore(CodeArgs a) {
   const uint64_t row = a.row0 + r;
   const int nv = (int)(a.cols - c);
   float v[kCodes];
-  load_lane<int8_t>(a.codes + row * a.ldc + c, nv, v);
+  load_lane<kCodes, int8_t>(a.codes + row * a.ldc + c, nv, v);
   const float scale = a.scales[row * a.blocks + c / kCodeBlock];
 #pragma unroll
   for (int e = 0; e < kCodes; ++e) v[e] *= scale;
@@ -98,7 +179,7 @@ __global__ __launch_bounds__(256) void k_restore(CodeArgs a) {
 static tk_status run_codes(CodeArgs a, uint64_t rows, RowType t, bool r32, hipStream_t s) {
   const bool pack = a.x != nullptr;
   a.blocks = (a.cols + kCodeBlock - 1) / kCodeBlock;
-  a.chunks_per_row = pack ? a.blocks * (kCodeBlock / kCodes) : (a.cols + kCodes - 1) / kCodes;
+  a.chunks_per_row = pack ? a.blocks * (kCodeBlock / kPack) : (a.cols + kCodes - 1) / kCodes;
   a.per_row = Divisor(a.chunks_per_row);
   const uint64_t rows_each = (1ull << 30) / a.chunks_per_row;
   for (uint64_t r = 0; r < rows; r += rows_each) {

@@ -148,28 +148,60 @@ __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) 
   }
 }
 
-// The words themselves, for draws other than dropout's.
-template <int CH>
+// The arguments of the hash's second step for N counters from c, in groups of up to eight counters
+// as above: where c lies within a group (a start draw that is no multiple of eight, an odd width), they
+// come from one group more, whose products are shared the same way.  The offset is nearly always the
+// same in a wave's lanes; then each of its values has code of its own, in which no element chooses its group.
+template <int N, int kOffset>
+__device__ __forceinline__ void offset_products(const uint32_t (&p)[N / (N < 8 ? N : 8) + 1],
+                                                const uint32_t (&step)[N / (N < 8 ? N : 8) + 1][3], uint32_t *x) {
+  constexpr int G = N < 8 ? N : 8;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int g = (kOffset + e) / G, t = (kOffset + e) % G;
+    uint32_t v = p[g];
+#pragma unroll
+    for (int b = 2; b >= 0; --b)
+      if (t >> b & 1) v += step[g][b];
+    x[e] = v;
+  }
+}
+
+template <int N>
 __device__ __forceinline__ void chunk_words(uint32_t hk, uint32_t c, uint32_t *w) {
-  if (CH > 1 && (c & (CH - 1)) == 0) {
-    uint32_t k = c ^ hk;
-    k ^= k >> 16;
-    uint32_t x[CH];
-    x[0] = k * kHashMul1;
+  constexpr int G = N < 8 ? N : 8, kGroups = N / G + 1;
+  const uint32_t offset = c & (G - 1), one = (uint32_t)__builtin_amdgcn_readfirstlane((int)offset);
+  if (__all(offset == one)) {
+    uint32_t p[kGroups], step[kGroups][3];
+    const auto group = [&](int g) {
+      uint32_t k = (c - offset + g * G) ^ hk;
+      k ^= k >> 16;
+      p[g] = k * kHashMul1;
 #pragma unroll
-    for (int b = 1; b < CH; b <<= 1) {
-      const uint32_t step = k & b ? 0u - b * kHashMul1 : b * kHashMul1;
+      for (int b = 0; 1 << b < G; ++b) step[g][b] = k >> b & 1 ? 0u - (kHashMul1 << b) : kHashMul1 << b;
+    };
 #pragma unroll
-      for (int e = 0; e < b; ++e) x[b + e] = x[e] + step;
+    for (int g = 0; g + 1 < kGroups; ++g) group(g);
+    if (one == 0) {
+      offset_products<N, 0>(p, step, w);
+    } else {
+      group(kGroups - 1);
+      if (one == 1) offset_products<N, 1>(p, step, w);
+      else if (one == 2) offset_products<N, 2>(p, step, w);
+      else if (one == 3) offset_products<N, 3>(p, step, w);
+      else if (G == 8 && one == 4) offset_products<N, 4 % G>(p, step, w);
+      else if (G == 8 && one == 5) offset_products<N, 5 % G>(p, step, w);
+      else if (G == 8 && one == 6) offset_products<N, 6 % G>(p, step, w);
+      else offset_products<N, G - 1>(p, step, w);
     }
 #pragma unroll
-    for (int e = 0; e < CH; ++e) {
-      const uint32_t y = (x[e] ^ (x[e] >> 15)) * kHashMul2;
+    for (int e = 0; e < N; ++e) {
+      const uint32_t y = (w[e] ^ (w[e] >> 15)) * kHashMul2;
       w[e] = y ^ (y >> 16);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < CH; ++e) w[e] = tk_word(hk, c + e);
+    for (int e = 0; e < N; ++e) w[e] = tk_word(hk, c + e);
   }
 }
 
