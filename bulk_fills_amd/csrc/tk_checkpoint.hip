@@ -17,6 +17,7 @@ struct CodeArgs {
 
 constexpr int kCodes = 8;  // codes of a lane of k_restore
 constexpr int kPack = 16;  // elements of a lane of k_checkpoint: eight lanes hold a block
+constexpr int kBlockLanes = kCodeBlock / kPack;
 
 // nv of a lane's N elements, the others 0: fewer than all are loaded one by one.
 template <int N, class R>
@@ -52,13 +53,25 @@ __device__ __forceinline__ uint32_t twice_and(uint32_t a, uint32_t b) {
   return n;
 }
 
+// The number whose highest byte is a code's magnitude below 0, from its word and t 2^24.
+__device__ __forceinline__ uint32_t numbered(uint32_t word, float t) {
+  return twice_and(word & 0x7FFFFFu, (uint32_t)floor_of_negative(t));
+}
+
 // Four codes from numbers that hold -|code| in their highest byte: those of negative elements (0xFF in
 // `sign`) are the bytes themselves.  With the sign bit turned a byte is 128 - |code|, so that four are
-// subtracted from 128 at once and none borrows.
-__device__ __forceinline__ uint32_t four_codes(const uint32_t *n, uint32_t sign) {
+// subtracted from 128 at once and none borrows.  A magnitude of 128 sets a highest bit in `over`.
+__device__ __forceinline__ uint32_t four_codes(const uint32_t *n, uint32_t sign, uint32_t &over) {
   const uint32_t low = __builtin_amdgcn_perm(n[1], n[0], 0x0C0C0703), high = __builtin_amdgcn_perm(n[3], n[2], 0x07030C0C);
   const uint32_t negative = low | high, positive = 0x80808080u - (negative ^ 0x80808080u);
+  over |= positive;
   return (negative & sign) | (positive & ~sign);
+}
+
+// Codes of 0x80, which no other magnitude than 128 gives, to 127 of their sign.
+__device__ __forceinline__ uint32_t down_to_127(uint32_t codes, uint32_t sign) {
+  const uint32_t x = codes ^ 0x80808080u, one = (~(((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | x) & 0x80808080u) >> 7;
+  return codes + (one & sign) - (one & ~sign);
 }
 
 // A lane's elements as they are kept: their values, the largest magnitude's bits as a float's, and
@@ -120,36 +133,60 @@ struct Lane<bf16_t> {
 //
 // Bound by its instructions: 3 bytes move for every element.  Sixteen elements to a lane share what
 // a lane does once.
-template <class R>
+//
+// kWide: a wave takes 64 chunks of one row, so that rows and their addresses are the scalar unit's;
+// else the chunks of all rows follow each other.
+template <class R, bool kWide>
 __global__ __launch_bounds__(256) void k_checkpoint(CodeArgs a) {
-  const uint32_t n = blockIdx.x * 256u + threadIdx.x;
-  if (n >= a.chunks) return;  // whole blocks of eight lanes
-  const uint32_t r = a.per_row.of(n), k = n - r * a.chunks_per_row, c = k * kPack;
+  uint32_t n = blockIdx.x * 256u + threadIdx.x, r, k;
+  if constexpr (kWide) {
+    n = blockIdx.x * 4u + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (n >= a.chunks) return;  // here waves' worth of chunks
+    r = a.per_row.of(n);
+    k = (n - r * a.chunks_per_row) * 64 + (threadIdx.x & 63);
+  } else {
+    if (n >= a.chunks) return;  // whole blocks of a row's lanes
+    r = a.per_row.of(n);
+    k = n - r * a.chunks_per_row;
+  }
   const uint64_t row = a.row0 + r;
+  const uint32_t c = k * kPack;
   const int nv = (int)(a.cols - c);
   Lane<R> x;
   x.load((const R *)a.x + row * a.ldx + c, nv);
   uint32_t top = x.top();
   const auto larger = [&](uint32_t o) { top = o > top ? o : top; };
-  larger(__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));   // quad_perm 1,0,3,2
-  larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));   // quad_perm 2,3,0,1
-  larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xF, 0xF, true));  // row_half_mirror
+  larger(__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true));  // quad_perm 1,0,3,2
+  larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true));  // quad_perm 2,3,0,1
+  if (kBlockLanes == 8) larger(__builtin_amdgcn_update_dpp(0, (int)top, 0x141, 0xF, 0xF, true));  // row_half_mirror
+  if (nv <= 0) return;
   const float m = __uint_as_float(top);
   const bool finite = top < 0x7F800000u, held = finite && m >= kLeastHeld;
-  if (k % 8 == 0) a.scales[row * a.blocks + k / 8] = !finite ? __uint_as_float(0x7FC00000u) : held ? over_127(m) : 0.0f;
-  if (nv <= 0) return;
+  if (k % kBlockLanes == 0)
+    a.scales[row * a.blocks + k / kBlockLanes] = !finite ? __uint_as_float(0x7FC00000u) : held ? over_127(m) : 0.0f;
   const float inverse = held ? __fdiv_rn(127.0f, m) : 0.0f;
   uint32_t w[kPack];
   chunk_words<kPack>(a.hk, a.start + (uint32_t)row * a.cols + c, w);
+  // One product gives t 2^24 where 2^24 inverse is finite and no t is rounded to 0: where t is subnormal
+  // the product may differ from t 2^24, but both are above 0 and below 1.
+  if (__all(!held || (m >= 0x1p-96f && m < 127.0f))) {
 #pragma unroll
-  for (int e = 0; e < kPack; ++e) {
-    const float t = __builtin_fabsf(x.value(e)) * inverse;
-    w[e] = twice_and(w[e] & 0x7FFFFFu, (uint32_t)floor_of_negative(fminf(t * 0x1p24f, 127.0f * 0x1p24f)));
+    for (int e = 0; e < kPack; ++e)
+      w[e] = numbered(w[e], __builtin_fabsf(x.value(e)) * (inverse * 0x1p24f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPack; ++e) w[e] = numbered(w[e], __builtin_fabsf(x.value(e)) * inverse * 0x1p24f);
   }
   typedef uint32_t Codes __attribute__((ext_vector_type(kPack / 4), aligned(1)));
   Codes code;
+  uint32_t over = 0;
 #pragma unroll
-  for (int e = 0; e < kPack; e += 4) code[e / 4] = finite ? four_codes(w + e, x.signs(e)) : 0;
+  for (int e = 0; e < kPack; e += 4) code[e / 4] = four_codes(w + e, x.signs(e), over);
+  // The largest t lies up to two units of its last place above 127, and is rounded up then once in 2^16.
+  if (__any(over & 0x80808080u))
+#pragma unroll
+    for (int e = 0; e < kPack; e += 4) code[e / 4] = down_to_127(code[e / 4], x.signs(e));
+  if (!__all(finite)) code = finite ? code : Codes(0);
   int8_t *out = a.codes + row * a.ldc + c;
   if (nv >= kPack) {
     __builtin_nontemporal_store(code, (Codes *)out);
@@ -175,20 +212,30 @@ __global__ __launch_bounds__(256) void k_restore(CodeArgs a) {
   store_chunk<kCodes>((R *)a.y + row * a.ldy + c, nv, v);
 }
 
-// A call of more than 2^30 chunks is cut.
+// A call of more than 2^30 chunks (waves of them, where rows have 64 and more) is cut.
 static tk_status run_codes(CodeArgs a, uint64_t rows, RowType t, bool r32, hipStream_t s) {
   const bool pack = a.x != nullptr;
   a.blocks = (a.cols + kCodeBlock - 1) / kCodeBlock;
-  a.chunks_per_row = pack ? a.blocks * (kCodeBlock / kPack) : (a.cols + kCodes - 1) / kCodes;
+  a.chunks_per_row = pack ? a.blocks * kBlockLanes : (a.cols + kCodes - 1) / kCodes;
+  const bool wide = pack && a.chunks_per_row >= 64;
+  if (wide) a.chunks_per_row = (a.chunks_per_row + 63) / 64;
   a.per_row = Divisor(a.chunks_per_row);
-  const uint64_t rows_each = (1ull << 30) / a.chunks_per_row;
+  const uint64_t rows_each = (wide ? 1ull << 25 : 1ull << 30) / a.chunks_per_row;
   for (uint64_t r = 0; r < rows; r += rows_each) {
     a.row0 = r;
     a.chunks = (uint32_t)((rows - r < rows_each ? rows - r : rows_each) * a.chunks_per_row);
-    const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((a.chunks + 255) / 256), dim3(256), 0, s, a); };
-    if (t == kF32 || r32) go(pack ? k_checkpoint<float> : k_restore<float>);
-    else if (t == kF16) go(pack ? k_checkpoint<f16_t> : k_restore<f16_t>);
-    else go(pack ? k_checkpoint<bf16_t> : k_restore<bf16_t>);
+    const auto go = [&](auto kernel, uint32_t each) {
+      hipLaunchKernelGGL(kernel, dim3((a.chunks + each - 1) / each), dim3(256), 0, s, a);
+    };
+    const auto type = [&](auto h) {
+      typedef decltype(h) R;
+      if (wide) go(k_checkpoint<R, true>, 4);
+      else if (pack) go(k_checkpoint<R, false>, 256);
+      else go(k_restore<R>, 256);
+    };
+    if (t == kF32 || r32) type(float());
+    else if (t == kF16) type(f16_t());
+    else type(bf16_t());
     const tk_status st = launch_status();
     if (st != TK_OK) return st;
   }

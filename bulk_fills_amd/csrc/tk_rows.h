@@ -148,51 +148,55 @@ __device__ __forceinline__ void drop_chunk(const Drop &d, uint32_t c, float *v) 
   }
 }
 
-// The arguments of the hash's second step for N counters from c, in groups of up to eight counters
-// as above: where c lies within a group (a start draw that is no multiple of eight, an odd width), they
-// come from one group more, whose products are shared the same way.  The offset is nearly always the
-// same in a wave's lanes; then each of its values has code of its own, in which no element chooses its group.
+// The arguments of the hash's second step for N counters that begin kOffset behind a multiple of N:
+// (k ^ t) K = k K + ((k ^ t) - k) K, where the last is a number of the scalar unit, as the low bits of
+// both multiples' k are the same in all lanes.
 template <int N, int kOffset>
-__device__ __forceinline__ void offset_products(const uint32_t (&p)[N / (N < 8 ? N : 8) + 1],
-                                                const uint32_t (&step)[N / (N < 8 ? N : 8) + 1][3], uint32_t *x) {
-  constexpr int G = N < 8 ? N : 8;
+__device__ __forceinline__ void offset_products(const uint32_t (&p)[2], const uint32_t (&low)[2], uint32_t *x) {
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const int g = (kOffset + e) / G, t = (kOffset + e) % G;
-    uint32_t v = p[g];
-#pragma unroll
-    for (int b = 2; b >= 0; --b)
-      if (t >> b & 1) v += step[g][b];
-    x[e] = v;
+    const int g = (kOffset + e) / N, t = (kOffset + e) % N;
+    uint32_t more = ((low[g] ^ t) - low[g]) * kHashMul1;
+    __asm__("" : "+s"(more));  // else the sum becomes a product for every word again
+    x[e] = p[g] + more;
   }
 }
 
+// One of the offsets kFrom to kTo - 1.
+template <int N, int kFrom, int kTo>
+__device__ __forceinline__ void products_at(uint32_t offset, const uint32_t (&p)[2], const uint32_t (&low)[2], uint32_t *x) {
+  constexpr int kMid = (kFrom + kTo) / 2;
+  if constexpr (kTo - kFrom == 1) offset_products<N, kFrom>(p, low, x);
+  else if (offset < kMid) products_at<N, kFrom, kMid>(offset, p, low, x);
+  else products_at<N, kMid, kTo>(offset, p, low, x);
+}
+
+// The words of N counters from c (N a power of two up to 16).  The lanes of a wave nearly always begin
+// the same way behind a multiple of N, and have the same bits 16 to 19 there: any start draw does that
+// with widths that are multiples of N, but where the wave passes a multiple of 2^16.  The hash's first
+// step then takes one product, or two at an offset, and an addition for each word; every offset has
+// code of its own, so that no word chooses its product.  Packing bf16 16384x8192 into 8 bits, which is
+// bound by its instructions, at an odd start draw: WWW us, with a first step for every word 99.
 template <int N>
 __device__ __forceinline__ void chunk_words(uint32_t hk, uint32_t c, uint32_t *w) {
-  constexpr int G = N < 8 ? N : 8, kGroups = N / G + 1;
-  const uint32_t offset = c & (G - 1), one = (uint32_t)__builtin_amdgcn_readfirstlane((int)offset);
-  if (__all(offset == one)) {
-    uint32_t p[kGroups], step[kGroups][3];
-    const auto group = [&](int g) {
-      uint32_t k = (c - offset + g * G) ^ hk;
-      k ^= k >> 16;
-      p[g] = k * kHashMul1;
+  uint32_t p[2], low[2], k[2];
+  const uint32_t offset = c & (N - 1);
 #pragma unroll
-      for (int b = 0; 1 << b < G; ++b) step[g][b] = k >> b & 1 ? 0u - (kHashMul1 << b) : kHashMul1 << b;
-    };
-#pragma unroll
-    for (int g = 0; g + 1 < kGroups; ++g) group(g);
-    if (one == 0) {
-      offset_products<N, 0>(p, step, w);
+  for (int g = 0; g < 2; ++g) {
+    k[g] = (c - offset + g * N) ^ hk;
+    k[g] ^= k[g] >> 16;
+  }
+  const uint32_t same = offset | (k[0] & (N - 1)) << 8 | (k[1] & (N - 1)) << 16;
+  const uint32_t one = (uint32_t)__builtin_amdgcn_readfirstlane((int)same);
+  if (__all(same == one)) {
+    low[0] = one >> 8 & (N - 1);
+    low[1] = one >> 16;
+    p[0] = k[0] * kHashMul1;
+    if ((one & (N - 1)) == 0) {
+      offset_products<N, 0>(p, low, w);
     } else {
-      group(kGroups - 1);
-      if (one == 1) offset_products<N, 1>(p, step, w);
-      else if (one == 2) offset_products<N, 2>(p, step, w);
-      else if (one == 3) offset_products<N, 3>(p, step, w);
-      else if (G == 8 && one == 4) offset_products<N, 4 % G>(p, step, w);
-      else if (G == 8 && one == 5) offset_products<N, 5 % G>(p, step, w);
-      else if (G == 8 && one == 6) offset_products<N, 6 % G>(p, step, w);
-      else offset_products<N, G - 1>(p, step, w);
+      p[1] = k[1] * kHashMul1;
+      products_at<N, 1, N>(one & (N - 1), p, low, w);
     }
 #pragma unroll
     for (int e = 0; e < N; ++e) {
