@@ -12,6 +12,8 @@ struct Side {
   const void *x, *dy, *gamma;
   void *out;  // y, or dx
   uint64_t ldx, lddy, ldo;
+  uint32_t heads, units, steps;  // a row's units of work, and the steps of one
+  Divisor by_units;
 };
 
 struct HeadArgs {
@@ -20,8 +22,8 @@ struct HeadArgs {
   const float *cosines, *sines;
   float *partial;  // lines of partial sums: dgamma_q's, then dgamma_k's
   uint64_t rows, table_rows;
-  uint32_t heads_q, heads, dim, half, pair_slots, slots;  // heads: of both sides
-  uint32_t parts;                                         // into which a row's heads are cut
+  uint32_t dim, half, pair_slots, slots;
+  uint32_t waves_q;  // of a backward work-group's waves those for the queries
   float eps;
   bool i64, params_f32;
 };
@@ -131,35 +133,70 @@ struct Angles {
   }
 };
 
+// A slot's two vectors as loaded, and their elements as floats.  Fewer than P are loaded one by one.
+template <int P, class T>
+struct Raw {
+  Chunk<T, P> v[2];
+  __device__ __forceinline__ void load(const void *head, const Slot &s) {
+    load_one((const T *)head + s.at1, s.n1, v[0]);
+    load_one((const T *)head + s.at2, s.n2, v[1]);
+  }
+  __device__ __forceinline__ void floats(float *x) const {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      x[e] = (float)v[0][e];
+      x[P + e] = (float)v[1][e];
+    }
+  }
+
+ private:
+  static __device__ __forceinline__ void load_one(const T *p, int n, Chunk<T, P> &t) {
+    if (n == P) {
+      t = *(const Chunk<T, P> *)p;
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e) t[e] = e < n ? p[e] : (T)0.0f;
+    }
+  }
+};
+
 // ---- kernels ----
-// A wave takes some heads of one row: 64 / kLanes of them at a time, kLanes lanes each, with the
-// row's angles in registers.
-template <class T, int P, int kLanes, bool kNeighbours>
+// A wave takes up to S steps of one row's queries or keys, a step being 64 / kLanes heads of kLanes lanes
+// each: all of its loads are on their way before the first value is used, and the angles and gamma serve
+// all steps.  blockIdx.y counts the queries' steps of a row by S, then the keys'.
+template <class T, int P, int kLanes, bool kNeighbours, int S>
 __global__ __launch_bounds__(256) void k_heads(HeadArgs a) {
   constexpr uint32_t kGroups = 64 / kLanes;
-  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = (threadIdx.x & 63) / kLanes;
+  const uint32_t group = (threadIdx.x & 63) / kLanes;
   const Slot slot = slot_of<P, kNeighbours>(a, threadIdx.x % kLanes);
   const float inv = 1.0f / (float)a.dim;
-  const uint64_t units = a.rows * a.parts;
-  for (uint64_t unit = blockIdx.x * 4ull + wave; unit < units; unit += gridDim.x * 4ull) {
-    const uint64_t row = unit / a.parts;
-    const uint32_t part = (uint32_t)(unit - row * a.parts);
-    Angles<P> angles;
-    angles.load(a, row, slot);
-    for (uint32_t h = part * kGroups + group; h < a.heads; h += a.parts * kGroups) {
-      const bool key = h >= a.heads_q;
-      const Side &side = a.side[key];
-      const uint32_t at = (key ? h - a.heads_q : h) * a.dim;
-      float v[2 * P], g[2 * P], sum = 0.0f;
-      load_slot<P, T>((const T *)side.x + row * side.ldx + at, slot, v);
-      load_gamma<P, T>(a, side.gamma, slot, g);
+  const uint64_t first = blockIdx.x * 4ull + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  for (uint32_t unit = blockIdx.y; unit < a.side[0].units + a.side[1].units; unit += gridDim.y) {
+    const bool key = unit >= a.side[0].units;
+    const Side &side = a.side[key];
+    const uint32_t h0 = (key ? unit - a.side[0].units : unit) * (S * kGroups) + group;
+    float g[2 * P];
+    load_gamma<P, T>(a, side.gamma, slot, g);
+    for (uint64_t row = first; row < a.rows; row += gridDim.x * 4ull) {
+      Raw<P, T> x[S];
+      Angles<P> angles;
 #pragma unroll
-      for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(v[e], v[e], sum);
-      const float rstd = rsqrt_any(__builtin_fmaf(lanes_sum<kLanes>(sum), inv, a.eps));
+      for (int s = 0; s < S; ++s)
+        if (h0 + s * kGroups < side.heads) x[s].load((const T *)side.x + row * side.ldx + (h0 + s * kGroups) * a.dim, slot);
+      angles.load(a, row, slot);
 #pragma unroll
-      for (int e = 0; e < 2 * P; ++e) v[e] = v[e] * rstd * g[e];
-      angles.template turn<kNeighbours, false>(v);
-      store_slot<P, T>((T *)side.out + row * side.ldo + at, slot, v);
+      for (int s = 0; s < S; ++s) {
+        if (h0 + s * kGroups >= side.heads) break;
+        float v[2 * P], sum = 0.0f;
+        x[s].floats(v);
+#pragma unroll
+        for (int e = 0; e < 2 * P; ++e) sum = __builtin_fmaf(v[e], v[e], sum);
+        const float rstd = rsqrt_any(__builtin_fmaf(lanes_sum<kLanes>(sum), inv, a.eps));
+#pragma unroll
+        for (int e = 0; e < 2 * P; ++e) v[e] = v[e] * rstd * g[e];
+        angles.template turn<kNeighbours, false>(v);
+        store_slot<P, T>((T *)side.out + row * side.ldo + (h0 + s * kGroups) * a.dim, slot, v);
+      }
     }
   }
 }
@@ -176,35 +213,65 @@ __device__ __forceinline__ float slots_sum(float x) {
   return x;
 }
 
-constexpr int kBackWaves = 8;
+constexpr int kBackWaves = 16;
 
-// The gradient: one pass over x and dy, the statistics made anew.  A wave keeps the sums for both
-// gammas in registers over all its rows; a work-group's go to the workspace as one line each.
+// The gradient: one pass over x and dy, the statistics made anew.  The waves of a work-group are shared
+// out between queries and keys, a.waves_q for those, so that each keeps one gamma and its gradient's sums
+// in registers over all its rows; at the end a work-group's sums go to the workspace as one line for each.
+// A wave's unit is `steps` steps of one row, or all of them where there are rows enough; the next step's
+// elements are loaded before the present one's are used.
 template <class T, int P, int kLanes, bool kNeighbours>
 __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
   constexpr uint32_t kGroups = 64 / kLanes;
-  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = (threadIdx.x & 63) / kLanes;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), group = (threadIdx.x & 63) / kLanes;
   const Slot slot = slot_of<P, kNeighbours>(a, threadIdx.x % kLanes);
   const float inv = 1.0f / (float)a.dim;
-  const uint64_t units = a.rows * a.parts;
-  float acc[2][2 * P];
+  const bool key = wave >= a.waves_q;
+  const Side &side = a.side[key];
+  const uint32_t waves = key ? kBackWaves - a.waves_q : a.waves_q, stride = gridDim.x * waves;
+  float acc[2 * P], g[2 * P];
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int e = 0; e < 2 * P; ++e) acc[k][e] = 0.0f;
-  for (uint64_t unit = blockIdx.x * (uint64_t)kBackWaves + wave; unit < units; unit += gridDim.x * (uint64_t)kBackWaves) {
-    const uint64_t row = unit / a.parts;
-    const uint32_t part = (uint32_t)(unit - row * a.parts);
-    Angles<P> angles;
-    angles.load(a, row, slot);
-    for (uint32_t h = part * kGroups + group; h < a.heads; h += a.parts * kGroups) {
-      const bool key = h >= a.heads_q;
-      const Side &side = a.side[key];
-      const uint32_t at = (key ? h - a.heads_q : h) * a.dim;
-      float x[2 * P], d[2 * P], g[2 * P], s[2] = {0.0f, 0.0f};
-      load_slot<P, T>((const T *)side.x + row * side.ldx + at, slot, x);
-      load_slot<P, T>((const T *)side.dy + row * side.lddy + at, slot, d);
-      load_gamma<P, T>(a, side.gamma, slot, g);
+  for (int e = 0; e < 2 * P; ++e) acc[e] = 0.0f;
+  load_gamma<P, T>(a, side.gamma, slot, g);
+  uint32_t unit = blockIdx.x * waves + (key ? wave - a.waves_q : wave);
+  const uint32_t units = (uint32_t)a.rows * side.units;
+  uint64_t row = side.by_units.of(unit);
+  uint32_t step = (unit - (uint32_t)row * side.units) * side.steps, end = step + side.steps;
+  Raw<P, T> next_x, next_d;
+  Angles<P> next_angles, angles;
+  const auto load = [&] {  // the head of this lane's group at (row, step), if there is one
+    const uint32_t h = step * kGroups + group;
+    if (h >= side.heads) return;
+    next_x.load((const T *)side.x + row * side.ldx + h * a.dim, slot);
+    next_d.load((const T *)side.dy + row * side.lddy + h * a.dim, slot);
+  };
+  bool more = unit < units;
+  if (more) {
+    load();
+    next_angles.load(a, row, slot);
+  }
+  bool turn_page = true;  // the step is a unit's first
+  while (more) {
+    const Raw<P, T> in_x = next_x, in_d = next_d;
+    if (turn_page) angles = next_angles;
+    const uint64_t at_row = row;
+    const uint32_t h = step * kGroups + group;
+    turn_page = ++step == end || step * kGroups >= side.heads;
+    if (turn_page) {
+      unit += stride;
+      more = unit < units;
+      row = side.by_units.of(unit);
+      step = (unit - (uint32_t)row * side.units) * side.steps;
+      end = step + side.steps;
+    }
+    if (more) {
+      load();
+      if (turn_page) next_angles.load(a, row, slot);
+    }
+    if (h < side.heads) {
+      float x[2 * P], d[2 * P], s[2] = {0.0f, 0.0f};
+      in_x.floats(x);
+      in_d.floats(d);
       angles.template turn<kNeighbours, true>(d);
 #pragma unroll
       for (int e = 0; e < 2 * P; ++e) s[0] = __builtin_fmaf(x[e], x[e], s[0]);
@@ -212,88 +279,108 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
 #pragma unroll
       for (int e = 0; e < 2 * P; ++e) {
         x[e] *= rstd;  // h
-        const float t = d[e] * x[e];
-        acc[0][e] += key ? 0.0f : t;
-        acc[1][e] += key ? t : 0.0f;
+        acc[e] = __builtin_fmaf(d[e], x[e], acc[e]);
         d[e] *= g[e];
         s[1] = __builtin_fmaf(d[e], x[e], s[1]);
       }
       const float m = lanes_sum<kLanes>(s[1]) * inv;
 #pragma unroll
       for (int e = 0; e < 2 * P; ++e) d[e] = rstd * __builtin_fmaf(-x[e], m, d[e]);
-      store_slot<P, T>((T *)side.out + row * side.ldo + at, slot, d);
+      store_slot<P, T>((T *)side.out + at_row * side.ldo + h * a.dim, slot, d);
     }
   }
   if (!a.partial) return;
   __shared__ float tile[kBackWaves][kLanes * 2 * P];
-  for (int k = 0; k < 2; ++k) {
-    if (k) __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 2 * P; ++e) {
-      const float v = slots_sum<kLanes>(k ? acc[1][e] : acc[0][e]);
-      if ((threadIdx.x & 63) < kLanes) tile[wave][(threadIdx.x & 63) * 2 * P + e] = v;
-    }
-    __syncthreads();
+  for (int e = 0; e < 2 * P; ++e) {
+    const float v = slots_sum<kLanes>(acc[e]);
+    if ((threadIdx.x & 63) < kLanes) tile[wave][(threadIdx.x & 63) * 2 * P + e] = v;
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < 2 * kLanes * 2 * P; i += 64 * kBackWaves) {
+    const uint32_t k = i / (kLanes * 2 * P), n = i % (kLanes * 2 * P), from = k ? a.waves_q : 0, to = k ? kBackWaves : a.waves_q;
+    const Slot t = slot_of<P, kNeighbours>(a, n / (2 * P));
+    const int e = (int)(n % (2 * P));
+    float v = 0.0f;
+    for (uint32_t w = from; w < to; ++w) v += tile[w][n];
     float *line = a.partial + ((uint64_t)k * gridDim.x + blockIdx.x) * line_pitch(a.dim);
-    for (uint32_t i = threadIdx.x; i < kLanes * 2 * P; i += 64 * kBackWaves) {
-      const Slot t = slot_of<P, kNeighbours>(a, i / (2 * P));
-      const int e = (int)(i % (2 * P));
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kBackWaves; ++w) v += tile[w][i];
-      if (e < P) {
-        if (e < t.n1) line[t.at1 + e] = v;
-      } else if (e - P < t.n2) {
-        line[t.at2 + e - P] = v;
-      }
+    if (e < P) {
+      if (e < t.n1) line[t.at1 + e] = v;
+    } else if (e - P < t.n2) {
+      line[t.at2 + e - P] = v;
     }
   }
 }
 
 // ---- launches ----
+constexpr int kSteps = 4, kForwardP = 8;
 constexpr uint64_t kMostDim = 512;  // 64 lanes of 8 f32 elements
 
 template <class T>
 struct Heads {
+  template <int P, int kLanes, bool kNeighbours, int S>
+  static void forward(HeadArgs a, hipStream_t s) {
+    for (Side &side : a.side) side.units = (side.heads + S * (64 / kLanes) - 1) / (S * (64 / kLanes));
+    const uint64_t x = (a.rows + 3) / 4, y = (uint64_t)a.side[0].units + a.side[1].units;
+    hipLaunchKernelGGL((k_heads<T, P, kLanes, kNeighbours, S>),
+                       dim3((uint32_t)(x < 1u << 20 ? x : 1u << 20), (uint32_t)(y < 4096 ? y : 4096)), dim3(256), 0, s, a);
+  }
   template <int P, int kLanes, bool kNeighbours>
-  static uint32_t go(HeadArgs a, bool back, hipStream_t s) {
+  static uint32_t backward(HeadArgs a, hipStream_t s) {
     constexpr uint32_t kGroups = 64 / kLanes;
-    // A wave goes through as many of a row's heads as leaves enough waves.
-    const uint32_t most = (a.heads + kGroups - 1) / kGroups;
-    uint64_t parts = 4096 / a.rows + 1;
-    a.parts = (uint32_t)(parts < most ? parts : most);
-    const uint64_t units = a.rows * a.parts, waves = back ? kBackWaves : 4, sets = (units + waves - 1) / waves;
-    const uint64_t cap = back ? kMaxLines : 1u << 16;
-    const uint32_t grid = (uint32_t)(sets < cap ? sets : cap);
-    if (back) hipLaunchKernelGGL((k_heads_bwd<T, P, kLanes, kNeighbours>), dim3(grid), dim3(64 * kBackWaves), 0, s, a);
-    else hipLaunchKernelGGL((k_heads<T, P, kLanes, kNeighbours>), dim3(grid), dim3(256), 0, s, a);
-    return grid;
+    const uint64_t steps[2] = {(a.side[0].heads + kGroups - 1) / kGroups, (a.side[1].heads + kGroups - 1) / kGroups};
+    // the waves by the steps, at least one for a side that has any
+    const uint64_t both = steps[0] + steps[1];
+    uint64_t q = (kBackWaves * steps[0] + both / 2) / both;
+    if (q == 0 && steps[0]) q = 1;
+    if (q == kBackWaves && steps[1]) --q;
+    a.waves_q = (uint32_t)q;
+    uint64_t grid = 1;
+    for (int k = 0; k < 2; ++k) {
+      if (!steps[k]) continue;
+      // a whole row to a wave where that leaves none without work
+      const uint64_t waves = k ? kBackWaves - q : q;
+      Side &side = a.side[k];
+      side.steps = a.rows >= 256 * waves ? (uint32_t)steps[k] : 1;
+      side.units = (uint32_t)((steps[k] + side.steps - 1) / side.steps);
+      side.by_units = Divisor(side.units);
+      const uint64_t sets = (a.rows * side.units + waves - 1) / waves;
+      grid = sets > grid ? sets : grid;
+    }
+    if (grid > kMaxLines) grid = kMaxLines;
+    hipLaunchKernelGGL((k_heads_bwd<T, P, kLanes, kNeighbours>), dim3((uint32_t)grid), dim3(64 * kBackWaves), 0, s, a);
+    return (uint32_t)grid;
   }
-  template <int P, bool kNeighbours>
-  static uint32_t lanes(const HeadArgs &a, bool back, hipStream_t s) {
-    if (a.slots <= 2) return go<P, 2, kNeighbours>(a, back, s);
-    if (a.slots <= 4) return go<P, 4, kNeighbours>(a, back, s);
-    if (a.slots <= 8) return go<P, 8, kNeighbours>(a, back, s);
-    if (a.slots <= 16) return go<P, 16, kNeighbours>(a, back, s);
-    if (a.slots <= 32) return go<P, 32, kNeighbours>(a, back, s);
-    return go<P, 64, kNeighbours>(a, back, s);
-  }
-  template <int P>
-  static uint32_t launch(HeadArgs a, bool neighbours, bool back, hipStream_t s) {
-    return neighbours ? lanes<P, true>(a, back, s) : lanes<P, false>(a, back, s);
+  // Four steps to a wave where that leaves enough waves.
+  template <int P, int kLanes, bool kNeighbours>
+  static void forward_by(const HeadArgs &a, hipStream_t s) {
+    constexpr uint64_t kGroups = 64 / kLanes;
+    const uint64_t steps = (a.side[0].heads + kGroups - 1) / kGroups + (a.side[1].heads + kGroups - 1) / kGroups;
+    if (a.rows * steps >= 8192) forward<P, kLanes, kNeighbours, kSteps>(a, s);
+    else forward<P, kLanes, kNeighbours, 1>(a, s);
   }
   static void set_slots(HeadArgs &a, uint32_t P) {
     a.pair_slots = (a.half + P - 1) / P;
     a.slots = a.pair_slots + (a.dim - 2 * a.half + 2 * P - 1) / (2 * P);
   }
-  // The work-groups that ran.
-  static uint32_t run(HeadArgs a, bool neighbours, bool back, hipStream_t s) {
-    if constexpr (sizeof(T) == 4) {
-      set_slots(a, 4);
-      if (a.slots <= 64) return launch<4>(a, neighbours, back, s);
+  // The work-groups that ran (backward), with the lanes that a head's slots need.
+  template <int P, bool kNeighbours, bool kBack, int kLanes = 2>
+  static uint32_t lanes(const HeadArgs &a, hipStream_t s) {
+    if constexpr (kLanes < 64)
+      if (a.slots > kLanes) return lanes<P, kNeighbours, kBack, 2 * kLanes>(a, s);
+    if constexpr (kBack) return backward<P, kLanes, kNeighbours>(a, s);
+    else forward_by<P, kLanes, kNeighbours>(a, s);
+    return 0;
+  }
+  template <bool kNeighbours, bool kBack>
+  static uint32_t run(HeadArgs a, hipStream_t s) {
+    constexpr int P = kBack || sizeof(T) == 4 ? 4 : kForwardP;
+    set_slots(a, P);
+    if (P < 8 && a.slots > 64) {  // the widest heads, of which some elements turn and some do not
+      set_slots(a, 8);
+      return lanes<8, kNeighbours, kBack, 64>(a, s);
     }
-    set_slots(a, 8);
-    return launch<8>(a, neighbours, back, s);
+    return lanes<P, kNeighbours, kBack>(a, s);
   }
 };
 
@@ -324,15 +411,18 @@ struct HeadCall {
       c.vector(sines, table_rows * (rotary / 2), 4, false, true);
     }
     a.positions = positions; a.table_rows = table_rows; a.cosines = cosines; a.sines = sines;
-    a.rows = rows; a.heads_q = (uint32_t)heads_q; a.heads = (uint32_t)(heads_q + heads_k);
+    a.rows = rows; a.side[0].heads = (uint32_t)heads_q; a.side[1].heads = (uint32_t)heads_k;
     a.dim = (uint32_t)dim; a.half = (uint32_t)(rotary / 2); a.eps = eps;
     a.i64 = flags & TK_INDEX_I64; a.params_f32 = params_f32(type, flags);
     return TK_OK;
   }
   uint32_t run(bool back, hipStream_t s) const {
-    const bool n = flags & TK_INTERLEAVED;
-    return type == kF32 ? Heads<float>::run(a, n, back, s) : type == kF16 ? Heads<f16_t>::run(a, n, back, s)
-                                                                           : Heads<bf16_t>::run(a, n, back, s);
+    const auto by_type = [&](auto h) {
+      typedef Heads<decltype(h)> K;
+      if (flags & TK_INTERLEAVED) return back ? K::template run<true, true>(a, s) : K::template run<true, false>(a, s);
+      return back ? K::template run<false, true>(a, s) : K::template run<false, false>(a, s);
+    };
+    return type == kF32 ? by_type(float()) : type == kF16 ? by_type(f16_t()) : by_type(bf16_t());
   }
 };
 
@@ -350,7 +440,7 @@ static tk_status head_forward(HeadCall h, const void *q, uint64_t ldq, const voi
     c.matrix_of(x[i], h.rows, h.width(i), ldx[i], c.t(), false, true, i ? kKeys : kQueries);
     c.matrix_of(y[i], h.rows, h.width(i), ldy[i], c.t(), true, true, i ? kKeys : kQueries);
     c.vector(gamma[i], h.dim, c.par(), false, false);
-    h.a.side[i] = Side{x[i], nullptr, gamma[i], y[i], ldx[i], 0, ldy[i]};
+    h.a.side[i] = Side{x[i], nullptr, gamma[i], y[i], ldx[i], 0, ldy[i], 0, 0, 0, {}};
   }
   if ((st = h.angles(c, positions, table_rows, cosines, sines)) != TK_OK || (st = c.done()) != TK_OK) return st;
   h.run(false, stream);
@@ -386,7 +476,7 @@ static tk_status head_backward(HeadCall h, const void *dyq, uint64_t lddyq, cons
     c.matrix_of(dy[i], h.rows, h.width(i), lddy[i], c.t(), false, true, kind);
     c.matrix_of(dx[i], h.rows, h.width(i), lddx[i], c.t(), true, true, kind);
     c.vector(gamma[i], h.dim, c.par(), false, false);
-    h.a.side[i] = Side{x[i], dy[i], gamma[i], dx[i], ldx[i], lddy[i], lddx[i]};
+    h.a.side[i] = Side{x[i], dy[i], gamma[i], dx[i], ldx[i], lddy[i], lddx[i], 0, 0, 0, {}};
   }
   const uint64_t need = sums ? head_bytes(h.rows, h.heads_q, h.heads_k, h.dim) : 0;
   if (!serves(workspace, bytes, need)) return TK_EINVAL;
