@@ -24,27 +24,56 @@ __device__ __forceinline__ uint64_t token(const void *ids, bool ids64, uint64_t 
   return ids64 ? (uint64_t)((const int64_t *)ids)[row] : (uint64_t)(int64_t)((const int32_t *)ids)[row];
 }
 
-// A thread takes one chunk: rows come from anywhere in the table, so nothing is gained by keeping a
-// row's lanes together, and many waves hide the two loads that wait for each other (the token, then
-// its row).
-template <class W, class R, bool kDivide, int CH>
+// A lane takes V chunks, 64 apart.  Rows come from anywhere in the table, so nothing is gained by going
+// on from one to the next: many waves hide the two loads that wait for each other (the token, then its
+// row).  kWide: a wave takes 64 V chunks of one row, whose token and address are the scalar unit's; else
+// (V = 1) the chunks of all rows follow each other.
+template <class W, class R, bool kDivide, int CH, bool kWide, int V>
 __global__ __launch_bounds__(256) void k_embedding(LookupArgs a) {
-  const uint32_t n = blockIdx.x * 256u + threadIdx.x;
-  if (n >= a.chunks) return;
-  const uint32_t r = a.per_row.of(n), c = (n - r * a.chunks_per_row) * CH;
-  const uint64_t row = a.row0 + r, id = token(a.ids, a.ids64, row);
-  const int nv = (int)(a.cols - c);
-  float v[CH];
-  if (id < a.vocab) {
-    unpack<CH, W>(load_chunk<false, CH>((const W *)a.table + id * a.ldt + chunk_at<CH>(c, a.cols)), nv, v);
-#pragma unroll
-    for (int e = 0; e < CH; ++e) v[e] *= a.scale;
-    if (a.drop.on) drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)row * a.cols + c, v);
+  uint32_t n, r, c;
+  if constexpr (kWide) {
+    n = blockIdx.x * 4u + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (n >= a.chunks) return;  // here waves' worth of chunks
+    r = a.per_row.of(n);
+    c = ((n - r * a.chunks_per_row) * (64 * V) + (threadIdx.x & 63)) * CH;
   } else {
-#pragma unroll
-    for (int e = 0; e < CH; ++e) v[e] = 0.0f;
+    n = blockIdx.x * 256u + threadIdx.x;
+    if (n >= a.chunks) return;
+    r = a.per_row.of(n);
+    c = (n - r * a.chunks_per_row) * CH;
   }
-  store_chunk<CH>((R *)a.y + row * a.ldy + c, nv, v);
+  const uint64_t row = a.row0 + r, id = token(a.ids, a.ids64, row);
+  const bool there = id < a.vocab;
+  Chunk<W, CH> x[V];
+  if (there)
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      x[j] = load_chunk<false, CH>((const W *)a.table + id * a.ldt + chunk_at<CH>(c + j * 64 * CH, a.cols));
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t at = c + j * 64 * CH;
+    const int nv = (int)(a.cols - at);
+    float v[CH];
+    if (there) {
+      unpack<CH, W>(x[j], nv, v);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) v[e] *= a.scale;
+      if (a.drop.on) {
+        if constexpr (CH > 1) {
+          uint32_t w[CH];
+          chunk_words<CH>(a.drop.hk, a.drop.start + (uint32_t)row * a.cols + at, w);
+#pragma unroll
+          for (int e = 0; e < CH; ++e) v[e] = drop_one<kDivide>(a.drop, w[e], v[e]);
+        } else {
+          drop_chunk<kDivide, CH>(a.drop, a.drop.start + (uint32_t)row * a.cols + at, v);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < CH; ++e) v[e] = 0.0f;
+    }
+    if (nv > 0) store_chunk<CH>((R *)a.y + row * a.ldy + at, nv, v);
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -366,21 +395,29 @@ static uint64_t embedding_bytes(uint64_t rows, uint64_t cols, uint64_t vocab) {
   return 4 * (2 * rows + vocab + 1) + 8 * room * line_pitch(cols) + 12;  // 12: the lines are aligned to 16 bytes
 }
 
+constexpr int kLookupChunks = 2;
+
 template <class W, class R, bool kDivide>
 struct Embedding {
   static constexpr int CH = kChunk<W, R>;
 
   static tk_status forward(LookupArgs a, uint64_t rows, hipStream_t s) {
+    constexpr int V = kLookupChunks;
     const int ch = a.cols < (uint32_t)CH ? 1 : CH;
+    const bool wide = a.cols >= 64u * CH;
     a.chunks_per_row = (a.cols + ch - 1) / ch;
+    if (wide) a.chunks_per_row = (a.chunks_per_row + 64 * V - 1) / (64 * V);
     a.per_row = Divisor(a.chunks_per_row);
-    const uint64_t rows_each = (1ull << 30) / a.chunks_per_row;
+    const uint64_t rows_each = (wide ? 1ull << 25 : 1ull << 30) / a.chunks_per_row;
     for (uint64_t r = 0; r < rows; r += rows_each) {
       a.row0 = r;
       a.chunks = (uint32_t)((rows - r < rows_each ? rows - r : rows_each) * a.chunks_per_row);
-      const dim3 grid((a.chunks + 255) / 256);
-      if (ch == 1) hipLaunchKernelGGL((k_embedding<W, R, kDivide, 1>), grid, dim3(256), 0, s, a);
-      else hipLaunchKernelGGL((k_embedding<W, R, kDivide, CH>), grid, dim3(256), 0, s, a);
+      const auto go = [&](auto kernel, uint32_t each) {
+        hipLaunchKernelGGL(kernel, dim3((a.chunks + each - 1) / each), dim3(256), 0, s, a);
+      };
+      if (ch == 1) go(k_embedding<W, R, kDivide, 1, false, 1>, 256);
+      else if (wide) go(k_embedding<W, R, kDivide, CH, true, V>, 4);
+      else go(k_embedding<W, R, kDivide, CH, false, 1>, 256);
       const tk_status st = launch_status();
       if (st != TK_OK) return st;
     }

@@ -25,7 +25,7 @@ struct HeadArgs {
   uint32_t dim, half, pair_slots, slots;
   uint32_t waves_q;  // of a backward work-group's waves those for the queries
   float eps;
-  bool i64, params_f32;
+  bool i64, params_f32, once;  // once: the call's reads go past the caches
 };
 
 // ---- a lane's part of a head ----
@@ -134,7 +134,7 @@ struct Angles {
 };
 
 // A slot's two vectors as loaded, and their elements as floats.  Fewer than P are loaded one by one.
-template <int P, class T>
+template <bool kOnce, int P, class T>
 struct Raw {
   Chunk<T, P> v[2];
   __device__ __forceinline__ void load(const void *head, const Slot &s) {
@@ -152,7 +152,7 @@ struct Raw {
  private:
   static __device__ __forceinline__ void load_one(const T *p, int n, Chunk<T, P> &t) {
     if (n == P) {
-      t = *(const Chunk<T, P> *)p;
+      t = load_chunk<kOnce, P>(p);
     } else {
 #pragma unroll
       for (int e = 0; e < P; ++e) t[e] = e < n ? p[e] : (T)0.0f;
@@ -164,7 +164,7 @@ struct Raw {
 // A wave takes up to S steps of one row's queries or keys, a step being 64 / kLanes heads of kLanes lanes
 // each: all of its loads are on their way before the first value is used, and the angles and gamma serve
 // all steps.  blockIdx.y counts the queries' steps of a row by S, then the keys'.
-template <class T, int P, int kLanes, bool kNeighbours, int S>
+template <class T, int P, int kLanes, bool kNeighbours, bool kOnce, int S>
 __global__ __launch_bounds__(256) void k_heads(HeadArgs a) {
   constexpr uint32_t kGroups = 64 / kLanes;
   const uint32_t group = (threadIdx.x & 63) / kLanes;
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadArgs a) {
     float g[2 * P];
     load_gamma<P, T>(a, side.gamma, slot, g);
     for (uint64_t row = first; row < a.rows; row += gridDim.x * 4ull) {
-      Raw<P, T> x[S];
+      Raw<kOnce, P, T> x[S];
       Angles<P> angles;
 #pragma unroll
       for (int s = 0; s < S; ++s)
@@ -220,7 +220,7 @@ constexpr int kBackWaves = 16;
 // in registers over all its rows; at the end a work-group's sums go to the workspace as one line for each.
 // A wave's unit is `steps` steps of one row, or all of them where there are rows enough; the next step's
 // elements are loaded before the present one's are used.
-template <class T, int P, int kLanes, bool kNeighbours>
+template <class T, int P, int kLanes, bool kNeighbours, bool kOnce>
 __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
   constexpr uint32_t kGroups = 64 / kLanes;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), group = (threadIdx.x & 63) / kLanes;
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
   const uint32_t units = (uint32_t)a.rows * side.units;
   uint64_t row = side.by_units.of(unit);
   uint32_t step = (unit - (uint32_t)row * side.units) * side.steps, end = step + side.steps;
-  Raw<P, T> next_x, next_d;
+  Raw<kOnce, P, T> next_x, next_d;
   Angles<P> next_angles, angles;
   const auto load = [&] {  // the head of this lane's group at (row, step), if there is one
     const uint32_t h = step * kGroups + group;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
   }
   bool turn_page = true;  // the step is a unit's first
   while (more) {
-    const Raw<P, T> in_x = next_x, in_d = next_d;
+    const Raw<kOnce, P, T> in_x = next_x, in_d = next_d;
     if (turn_page) angles = next_angles;
     const uint64_t at_row = row;
     const uint32_t h = step * kGroups + group;
@@ -314,15 +314,16 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
 
 // ---- launches ----
 constexpr int kSteps = 4, kForwardP = 8;
+constexpr uint64_t kRowsEach = 8;
 constexpr uint64_t kMostDim = 512;  // 64 lanes of 8 f32 elements
 
 template <class T>
 struct Heads {
-  template <int P, int kLanes, bool kNeighbours, int S>
+  template <int P, int kLanes, bool kNeighbours, bool kOnce, int S>
   static void forward(HeadArgs a, hipStream_t s) {
     for (Side &side : a.side) side.units = (side.heads + S * (64 / kLanes) - 1) / (S * (64 / kLanes));
     const uint64_t x = (a.rows + 3) / 4, y = (uint64_t)a.side[0].units + a.side[1].units;
-    hipLaunchKernelGGL((k_heads<T, P, kLanes, kNeighbours, S>),
+    hipLaunchKernelGGL((k_heads<T, P, kLanes, kNeighbours, kOnce, S>),
                        dim3((uint32_t)(x < 1u << 20 ? x : 1u << 20), (uint32_t)(y < 4096 ? y : 4096)), dim3(256), 0, s, a);
   }
   template <int P, int kLanes, bool kNeighbours>
@@ -341,14 +342,16 @@ struct Heads {
       // a whole row to a wave where that leaves none without work
       const uint64_t waves = k ? kBackWaves - q : q;
       Side &side = a.side[k];
-      side.steps = a.rows >= 256 * waves ? (uint32_t)steps[k] : 1;
+      side.steps = a.rows >= kRowsEach * 256 * waves ? (uint32_t)steps[k] : 1;
       side.units = (uint32_t)((steps[k] + side.steps - 1) / side.steps);
       side.by_units = Divisor(side.units);
       const uint64_t sets = (a.rows * side.units + waves - 1) / waves;
       grid = sets > grid ? sets : grid;
     }
     if (grid > kMaxLines) grid = kMaxLines;
-    hipLaunchKernelGGL((k_heads_bwd<T, P, kLanes, kNeighbours>), dim3((uint32_t)grid), dim3(64 * kBackWaves), 0, s, a);
+    const dim3 g((uint32_t)grid), b(64 * kBackWaves);
+    if (a.once) hipLaunchKernelGGL((k_heads_bwd<T, P, kLanes, kNeighbours, true>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((k_heads_bwd<T, P, kLanes, kNeighbours, false>), g, b, 0, s, a);
     return (uint32_t)grid;
   }
   // Four steps to a wave where that leaves enough waves.
@@ -356,8 +359,9 @@ struct Heads {
   static void forward_by(const HeadArgs &a, hipStream_t s) {
     constexpr uint64_t kGroups = 64 / kLanes;
     const uint64_t steps = (a.side[0].heads + kGroups - 1) / kGroups + (a.side[1].heads + kGroups - 1) / kGroups;
-    if (a.rows * steps >= 8192) forward<P, kLanes, kNeighbours, kSteps>(a, s);
-    else forward<P, kLanes, kNeighbours, 1>(a, s);
+    if (a.once) forward<P, kLanes, kNeighbours, true, kSteps>(a, s);
+    else if (a.rows * steps >= 8192) forward<P, kLanes, kNeighbours, false, kSteps>(a, s);
+    else forward<P, kLanes, kNeighbours, false, 1>(a, s);
   }
   static void set_slots(HeadArgs &a, uint32_t P) {
     a.pair_slots = (a.half + P - 1) / P;
@@ -443,6 +447,7 @@ static tk_status head_forward(HeadCall h, const void *q, uint64_t ldq, const voi
     h.a.side[i] = Side{x[i], nullptr, gamma[i], y[i], ldx[i], 0, ldy[i], 0, 0, 0, {}};
   }
   if ((st = h.angles(c, positions, table_rows, cosines, sines)) != TK_OK || (st = c.done()) != TK_OK) return st;
+  h.a.once = h.rows * (h.width(0) + h.width(1)) * c.t() > kCachedReads;
   h.run(false, stream);
   return launch_status();
 }
@@ -483,6 +488,7 @@ static tk_status head_backward(HeadCall h, const void *dyq, uint64_t lddyq, cons
   if (need) c.vector(workspace, need / 4, 4, true, true);
   if ((st = h.angles(c, positions, table_rows, cosines, sines)) != TK_OK || (st = c.done()) != TK_OK) return st;
   h.a.partial = sums ? (float *)workspace : nullptr;
+  h.a.once = h.rows * (h.width(0) + h.width(1)) * 2 * c.t() > kCachedReads;
   const uint32_t lines = h.run(true, stream);
   if ((st = launch_status()) != TK_OK || !sums) return st;
   return finish(h.type, h.flags, h.a.partial, lines, h.dim, dgamma_q, dgamma_k, nullptr, stream);

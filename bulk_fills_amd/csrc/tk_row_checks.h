@@ -10,6 +10,7 @@
 namespace tk {
 
 constexpr uint64_t kMaxDim = 1ull << 31, kMaxLd = 1ull << 31;
+constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through the caches (tk_rows.h)
 
 struct Region {
   uintptr_t at;

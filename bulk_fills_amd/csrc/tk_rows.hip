@@ -79,7 +79,6 @@ __global__ __launch_bounds__(64 * kWaves) void k_finish(FinishArgs a) {
 // How a backward call is cut
 // ---------------------------------------------------------------------------------------
 constexpr uint64_t kRowsInRegisters = 8192;      // columns that k_norm_bwd holds
-constexpr uint64_t kCachedReads = 96ull << 20;  // bytes a call may read through the caches (tk_rows.h)
 
 // Up to this many sets of rows one work-group (or one to a strip) takes them all and writes the
 // gradients itself (layer norm backward bf16 128x128 5.1 us, with a second kernel 6.4; four sets
