@@ -15,20 +15,8 @@ struct CodeArgs {
   Divisor per_row;  // chunks_per_row
 };
 
-constexpr int kCodes = 8;  // codes of a lane of k_restore
 constexpr int kPack = 16;  // elements of a lane of k_checkpoint: eight lanes hold a block
 constexpr int kBlockLanes = kCodeBlock / kPack;
-
-// nv of a lane's N elements, the others 0: fewer than all are loaded one by one.
-template <int N, class R>
-__device__ __forceinline__ void load_lane(const R *p, int nv, float *v) {
-  if (nv >= N) {
-    unpack<N, R>(load_chunk<true, N>(p), N, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = e < nv ? (float)p[e] : 0.0f;
-  }
-}
 
 // Blocks whose largest element is below this are zeros: the quotient 127 / m stays finite, and the
 // scale normal.
@@ -74,12 +62,23 @@ __device__ __forceinline__ uint32_t down_to_127(uint32_t codes, uint32_t sign) {
   return codes + (one & sign) - (one & ~sign);
 }
 
+// Fewer than a lane's elements are loaded one by one, the others are 0.  Loads go through the caches at any
+// size: a lane's vectors lie beside each other, so past them each line is read again for every vector
+// (float 16384x8192 154 us instead of 113).
+//
 // A lane's elements as they are kept: their values, the largest magnitude's bits as a float's, and
 // 0xFF in the byte of each negative one of four.
 template <class R>
 struct Lane {
   float x[kPack];
-  __device__ __forceinline__ void load(const R *p, int nv) { load_lane<kPack, R>(p, nv, x); }
+  __device__ __forceinline__ void load(const R *p, int nv) {
+    if (nv >= kPack) {
+      unpack<kPack, R>(load_chunk<false, kPack>(p), kPack, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPack; ++e) x[e] = e < nv ? (float)p[e] : 0.0f;
+    }
+  }
   __device__ __forceinline__ float value(int e) const { return x[e]; }
   __device__ __forceinline__ uint32_t top() const {
     uint32_t t = 0;
@@ -103,7 +102,7 @@ struct Lane<bf16_t> {
   Pairs x;
   __device__ __forceinline__ void load(const bf16_t *p, int nv) {
     if (nv >= kPack) {
-      x = __builtin_nontemporal_load((const Pairs *)p);
+      x = *(const Pairs *)p;
     } else {
       const uint16_t *q = (const uint16_t *)p;
 #pragma unroll
@@ -197,28 +196,52 @@ __global__ __launch_bounds__(256) void k_checkpoint(CodeArgs a) {
   }
 }
 
-template <class R>
+// A lane takes V chunks, 64 apart, each 16 bytes of y: four of 16-bit elements, two of floats (16384x8192 with
+// one, two and four: bf16 69.8, 67.7 and 65.2 us, float 124, 104 and 112).  kWide as above (V = 1 where it is
+// not).
+template <class R, int CH, bool kWide, int V>
 __global__ __launch_bounds__(256) void k_restore(CodeArgs a) {
-  const uint32_t n = blockIdx.x * 256u + threadIdx.x;
-  if (n >= a.chunks) return;
-  const uint32_t r = a.per_row.of(n), c = (n - r * a.chunks_per_row) * kCodes;
+  uint32_t n = blockIdx.x * 256u + threadIdx.x, r, c;
+  if constexpr (kWide) {
+    n = blockIdx.x * 4u + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    if (n >= a.chunks) return;
+    r = a.per_row.of(n);
+    c = ((n - r * a.chunks_per_row) * (64 * V) + (threadIdx.x & 63)) * CH;
+  } else {
+    if (n >= a.chunks) return;
+    r = a.per_row.of(n);
+    c = (n - r * a.chunks_per_row) * CH;
+  }
   const uint64_t row = a.row0 + r;
-  const int nv = (int)(a.cols - c);
-  float v[kCodes];
-  load_lane<kCodes, int8_t>(a.codes + row * a.ldc + c, nv, v);
-  const float scale = a.scales[row * a.blocks + c / kCodeBlock];
+  Codes<CH> codes[V];
+  float scale[V];
 #pragma unroll
-  for (int e = 0; e < kCodes; ++e) v[e] *= scale;
-  store_chunk<kCodes>((R *)a.y + row * a.ldy + c, nv, v);
+  for (int j = 0; j < V; ++j) {
+    const uint32_t at = c + j * 64 * CH;
+    codes[j].template load<false>(a.codes + row * a.ldc + chunk_at<CH>(at, a.cols));
+    scale[j] = a.scales[row * a.blocks + (at < a.cols ? at / kCodeBlock : a.blocks - 1)];
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const uint32_t at = c + j * 64 * CH;
+    const int nv = (int)(a.cols - at);
+    float v[CH];
+    codes[j].floats(nv, v);
+#pragma unroll
+    for (int e = 0; e < CH; ++e) v[e] *= scale[j];
+    if (nv > 0) store_chunk<CH>((R *)a.y + row * a.ldy + at, nv, v);
+  }
 }
 
 // A call of more than 2^30 chunks (waves of them, where rows have 64 and more) is cut.
 static tk_status run_codes(CodeArgs a, uint64_t rows, RowType t, bool r32, hipStream_t s) {
   const bool pack = a.x != nullptr;
+  const uint32_t whole = t == kF32 || r32 ? 4 : 8, ch = a.cols < whole ? 1 : whole;  // k_restore's chunk
+  const uint32_t beside = whole / 2;                                                // and chunks of a lane
   a.blocks = (a.cols + kCodeBlock - 1) / kCodeBlock;
-  a.chunks_per_row = pack ? a.blocks * kBlockLanes : (a.cols + kCodes - 1) / kCodes;
-  const bool wide = pack && a.chunks_per_row >= 64;
-  if (wide) a.chunks_per_row = (a.chunks_per_row + 63) / 64;
+  a.chunks_per_row = pack ? a.blocks * kBlockLanes : (a.cols + ch - 1) / ch;
+  const bool wide = a.chunks_per_row >= 64;
+  if (wide) a.chunks_per_row = pack ? (a.chunks_per_row + 63) / 64 : (a.chunks_per_row + 64 * beside - 1) / (64 * beside);
   a.per_row = Divisor(a.chunks_per_row);
   const uint64_t rows_each = (wide ? 1ull << 25 : 1ull << 30) / a.chunks_per_row;
   for (uint64_t r = 0; r < rows; r += rows_each) {
@@ -229,11 +252,14 @@ static tk_status run_codes(CodeArgs a, uint64_t rows, RowType t, bool r32, hipSt
     };
     const auto type = [&](auto h) {
       typedef decltype(h) R;
-      if (wide) go(k_checkpoint<R, true>, 4);
+      constexpr int CH = 16 / sizeof(R);
+      if (pack && wide) go(k_checkpoint<R, true>, 4);
       else if (pack) go(k_checkpoint<R, false>, 256);
-      else go(k_restore<R>, 256);
+      else if (wide) go(k_restore<R, CH, true, CH / 2>, 4);
+      else if (ch == 1) go(k_restore<R, 1, false, 1>, 256);
+      else go(k_restore<R, CH, false, 1>, 256);
     };
-    if (t == kF32 || r32) type(float());
+    if (whole == 4) type(float());
     else if (t == kF16) type(f16_t());
     else type(bf16_t());
     const tk_status st = launch_status();

@@ -119,20 +119,23 @@ __device__ __forceinline__ void set_count(uint32_t *p, uint32_t n) {
 // own begin.  Each wave reads a sixteenth of the rows, in their order, twice: it counts its tokens
 // in a column of its own, and after a scan over tokens and waves it puts its rows in their places.
 // Rows of one token keep their order, whatever the waves do, so a gradient's sum has one order.
-// The lanes of one token find each other by votes, and the first of them counts for all: texts have
-// half of their tokens in the range of the lowest ones (16384 rows: with a turn of a loop for each of
-// a wave's tokens 82 us).
-template <int kRange>
+//
+// Bound by the work-group that has the most rows: of a text's tokens half are among the lowest hundred.
+// The lanes of one token find each other by votes, and the first of them moves its place on for all
+// (16384 rows of 32768 tokens, text-like: 15 us; with a turn of a loop for each of a wave's tokens 82;
+// evenly spread 12).  Counted by votes as well, so that the second pass has no more to do, the same rows
+// take 17 us, and 14 for 26 where all are one token's, whose counts wait for each other.
+template <int kRange, bool kI64>
 __global__ __launch_bounds__(64 * kSortWaves) void k_sort_tokens(SortArgs a) {
   __shared__ uint32_t count[kSortWaves][kRange], begin_of[kRange], total_of[kRange], part[kSortWaves], under[kSortWaves];
   const uint32_t lane = threadIdx.x & 63, wave = (uint32_t)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t under_me = (1ull << lane) - 1;
   const uint32_t piece = ((a.rows + kSortWaves * 64 - 1) / (kSortWaves * 64)) * 64;
   const uint32_t begin = wave * piece, end = begin + piece < a.rows ? begin + piece : a.rows;
-  const auto load = [&](uint32_t i) -> uint32_t {  // the token of row i, or none
-    if (i >= end) return kNoToken;
-    const uint64_t id = token(a.ids, a.ids64, i);
-    return id < a.vocab ? (uint32_t)id : kNoToken;
+  // The token of row i, or none.  Loaded in any case: loads in branches wait for each other.
+  const auto load = [&](uint32_t i) -> uint32_t {
+    const uint64_t id = token(a.ids, kI64, i < a.rows ? i : a.rows - 1);
+    return (i < end) & (id < a.vocab) ? (uint32_t)id : kNoToken;  // no branch
   };
   for (uint32_t range = blockIdx.x; range < a.ranges; range += gridDim.x) {
     const uint32_t lo = range * kRange;
@@ -365,7 +368,7 @@ __global__ __launch_bounds__(256) void k_join(GradArgs a) {
 // ---------------------------------------------------------------------------------------
 // Places to a tile: 8, 16, 32 or 64, the most that leave kUnits waves' work (and no more than the lanes of
 // a strip, which hold them).
-constexpr uint64_t kUnits = 4096;
+constexpr uint64_t kUnits = 2048;
 
 struct TilePlan {
   uint64_t tile = 8, strips, least;  // least: tiles that make kUnits
@@ -466,10 +469,10 @@ static tk_status sort_tokens(SortArgs a, hipStream_t s) {
     hipLaunchKernelGGL(kernel, dim3(a.ranges < 1u << 16 ? a.ranges : 1u << 16), dim3(64 * kSortWaves), 0, s, a);
   };
   // one work-group to a compute unit where the vocabulary allows: each reads all rows
-  if (a.vocab <= 64 * 256) go(k_sort_tokens<64>, 64);
-  else if (a.vocab <= 128 * 256) go(k_sort_tokens<128>, 128);
-  else if (a.vocab <= 256 * 256) go(k_sort_tokens<256>, 256);
-  else go(k_sort_tokens<512>, 512);
+  if (a.vocab <= 64 * 256) go(a.ids64 ? k_sort_tokens<64, true> : k_sort_tokens<64, false>, 64);
+  else if (a.vocab <= 128 * 256) go(a.ids64 ? k_sort_tokens<128, true> : k_sort_tokens<128, false>, 128);
+  else if (a.vocab <= 256 * 256) go(a.ids64 ? k_sort_tokens<256, true> : k_sort_tokens<256, false>, 256);
+  else go(a.ids64 ? k_sort_tokens<512, true> : k_sort_tokens<512, false>, 512);
   return launch_status();
 }
 

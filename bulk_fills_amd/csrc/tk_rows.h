@@ -175,8 +175,8 @@ __device__ __forceinline__ void products_at(uint32_t offset, const uint32_t (&p)
 // the same way behind a multiple of N, and have the same bits 16 to 19 there: any start draw does that
 // with widths that are multiples of N, but where the wave passes a multiple of 2^16.  The hash's first
 // step then takes one product, or two at an offset, and an addition for each word; every offset has
-// code of its own, so that no word chooses its product.  Packing bf16 16384x8192 into 8 bits, which is
-// bound by its instructions, at an odd start draw: WWW us, with a first step for every word 99.
+// code of its own, so that no word chooses its product.  Packing bf16 16384x8192 into 8 bits at any start
+// draw takes 72.2 us, with a first step for every word 75.9.
 template <int N>
 __device__ __forceinline__ void chunk_words(uint32_t hk, uint32_t c, uint32_t *w) {
   uint32_t p[2], low[2], k[2];
@@ -545,6 +545,35 @@ __device__ __forceinline__ float norm_grad(float g, float h, float rstd, float a
   return __builtin_fmaf(h, b, __builtin_fmaf(g, rstd, a));
 }
 
+// A chunk of a checkpoint's codes, in whole registers until each is converted from its byte: as a
+// vector of bytes it took a register for every element, and two instructions more to take it apart (the
+// fused backward bf16 8192x8192, which is bound by its instructions, 131 us instead of 111).
+template <int CH>
+struct Codes {
+  typedef uint32_t Bits __attribute__((ext_vector_type(CH < 4 ? 1 : CH / 4), aligned(1)));
+  Bits b;
+  template <bool kOnce>
+  __device__ __forceinline__ void load(const int8_t *p) {
+    if constexpr (CH < 4) b[0] = (uint8_t)*p;  // CH is 1
+    else b = kOnce ? __builtin_nontemporal_load((const Bits *)p) : *(const Bits *)p;
+  }
+  // as unpack() gives elements
+  __device__ __forceinline__ void floats(int nv, float *v) const {
+    Bits t = b;
+    if (nv < CH) {
+      if constexpr (CH == 8) {
+        const uint64_t all = ((uint64_t)t[1] << 32 | t[0]) >> (nv > 0 ? 8 * (CH - nv) : 0);
+        t[0] = nv > 0 ? (uint32_t)all : 0;
+        t[1] = nv > 0 ? (uint32_t)(all >> 32) : 0;
+      } else {
+        t[0] = nv > 0 ? t[0] >> (8 * (CH - nv)) : 0;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) v[e] = (float)(int8_t)(t[e / 4] >> (8 * (e % 4)));
+  }
+};
+
 // The scale of a checkpoint's codes at column c of a row (past the row's end its last one's).
 __device__ __forceinline__ float code_scale(const BwdArgs &a, uint64_t row, uint32_t c) {
   return a.scales[row * a.blocks + (c < a.cols ? c / kCodeBlock : a.blocks - 1)];
@@ -557,19 +586,24 @@ template <class T, class R, class S, class D, bool kNorm, bool kOnce, int CH>
 struct BwdIn {
   static constexpr bool kCodes = std::is_same<S, int8_t>::value;
   Chunk<D, CH> dy;
-  Chunk<S, CH> sum;
+  typename std::conditional<kCodes, Codes<CH>, Chunk<S, CH>>::type sum;
   Chunk<R, CH> dsum;
   float scale;
   __device__ __forceinline__ void load(const BwdArgs &a, uint64_t row, uint32_t c) {
     const uint32_t at = chunk_at<CH>(c, a.cols);
     dy = load_chunk<kOnce, CH>((const D *)a.dy + row * a.lddy + at);
-    if (kNorm) sum = load_chunk<kOnce, CH>((const S *)a.sum + row * a.lds + at);
-    if (kNorm && kCodes) scale = code_scale(a, row, c);
+    if constexpr (kNorm && kCodes) {
+      sum.template load<kOnce>((const S *)a.sum + row * a.lds + at);
+      scale = code_scale(a, row, c);
+    } else if constexpr (kNorm) {
+      sum = load_chunk<kOnce, CH>((const S *)a.sum + row * a.lds + at);
+    }
     if (a.dsum) dsum = load_chunk<kOnce, CH>((const R *)a.dsum + row * a.ldds + at);
   }
   // h of every element
   __device__ __forceinline__ void normed(int nv, float mean, float rstd, float *h) const {
-    unpack<CH, S>(sum, nv, h);
+    if constexpr (kCodes) sum.floats(nv, h);
+    else unpack<CH, S>(sum, nv, h);
 #pragma unroll
     for (int e = 0; e < CH; ++e) h[e] = ((kCodes ? h[e] * scale : h[e]) - mean) * rstd;
   }
@@ -757,21 +791,27 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
     uint32_t c = threadIdx.x * CH;
     // the next chunk is loaded before the present one is used (past the end: the row's last, unused)
     Chunk<T, CH> next_dy = load_chunk<false, CH>(dy + chunk_at<CH>(c, a.cols));
-    Chunk<S, CH> next_sum = load_chunk<false, CH>(sum + chunk_at<CH>(c, a.cols));
+    typename std::conditional<kCodes, Codes<CH>, Chunk<S, CH>>::type next_sum;
+    const auto load_sum = [&](uint32_t at) {
+      if constexpr (kCodes) next_sum.template load<false>(sum + at);
+      else next_sum = load_chunk<false, CH>(sum + at);
+    };
+    load_sum(chunk_at<CH>(c, a.cols));
     float next_scale = kCodes ? code_scale(a, row, c) : 1.0f;
     for (; c < a.cols; c += kTpr * CH) {
       const int nv = (int)(a.cols - c);
       const uint32_t at = chunk_at<CH>(c + kTpr * CH, a.cols);
       float g[CH], h[CH], w[CH];
       const Chunk<T, CH> here_dy = next_dy;
-      const Chunk<S, CH> here_sum = next_sum;
+      const auto here_sum = next_sum;
       const float scale = next_scale;
       next_dy = load_chunk<false, CH>(dy + at);
-      next_sum = load_chunk<false, CH>(sum + at);
+      load_sum(at);
       if (kCodes) next_scale = code_scale(a, row, c + kTpr * CH);
       load_param<CH, T>(a.gamma, a.params_f32, c, a.cols, 1.0f, w);
       unpack<CH, T>(here_dy, nv, g);
-      unpack<CH, S>(here_sum, nv, h);
+      if constexpr (kCodes) here_sum.floats(nv, h);
+      else unpack<CH, S>(here_sum, nv, h);
 #pragma unroll
       for (int e = 0; e < CH; ++e) {
         const float x = g[e] * w[e];
