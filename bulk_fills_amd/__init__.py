@@ -333,9 +333,10 @@ def _matrix(where, dev, x, ld, rows, cols, dtype):
         if x.is_contiguous():
             if x.numel() == rows * cols and (ld is None or ld == cols or rows <= 1):
                 return x.data_ptr(), cols if ld is None else ld
-        elif tuple(x.shape) == (rows, cols) and (cols == 1 or x.stride(1) == 1):
-            own = cols if rows <= 1 else x.stride(0)  # one row has no distance to a next
-            if own >= cols and (ld is None or ld == own or rows <= 1):
+        elif x.shape == (rows, cols):
+            to_next, within = x.stride()
+            own = cols if rows <= 1 else to_next  # one row has no distance to a next
+            if (within == 1 or cols == 1) and own >= cols and (ld is None or ld == own or rows <= 1):
                 return x.data_ptr(), own if ld is None else ld
     _refuse(where, x, dtype, dev, f"a {rows} x {cols} matrix with contiguous rows that do not overlap (and its own row "
                                   f"distance as ld, or None; here {ld})")
@@ -375,7 +376,7 @@ def _workspace(where, dev, x, stream, needed, size, *sizes):
             return None, 0, None
         if stream is not None and _on(where, stream, dev) != _raw_stream(dev):
             raise ValueError(f"{where}: a call on a stream that is not the current one needs a workspace")
-        x = torch.empty(n, dtype=torch.uint8, device="cuda")
+        x = torch.empty(n, dtype=torch.uint8, device=dev)
         return x.data_ptr(), n, x
     if x.get_device() != dev or not x.is_contiguous():
         _refuse(where, x, x.dtype, dev, "a contiguous workspace")
@@ -481,10 +482,11 @@ def _named(suffix, *functions):
 
 def _heads(where, dev, x, ld, rows, heads, dim, dtype):
     """(address, ld) of a matrix of heads: as _matrix takes it, or a view of rows x heads x dim."""
-    if not (x is None or isinstance(x, int)) and x.dim() == 3 and not x.is_contiguous():
-        if tuple(x.shape) != (rows, heads, dim) or (heads > 1 and x.stride(1) != dim) or (dim > 1 and x.stride(2) != 1):
+    if x is not None and not isinstance(x, int) and x.dim() == 3 and not x.is_contiguous():
+        to_next, apart, within = x.stride()
+        if x.shape != (rows, heads, dim) or (heads > 1 and apart != dim) or (dim > 1 and within != 1):
             _refuse(where, x, dtype, dev, f"{rows} x {heads} x {dim} with a row's heads one after the other")
-        x = x.as_strided((rows, heads * dim), (x.stride(0), 1))
+        x = x.as_strided((rows, heads * dim), (to_next, 1))
     return _matrix(where, dev, x, ld, rows, heads * dim, dtype)
 
 
