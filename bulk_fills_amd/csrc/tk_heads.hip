@@ -12,7 +12,7 @@ struct Side {
   const void *x, *dy, *gamma;
   void *out;  // y, or dx
   uint64_t ldx, lddy, ldo;
-  uint32_t heads, units, steps;  // a row's units of work, and the steps of one
+  uint32_t heads, units;  // units of work of a row
   Divisor by_units;
 };
 
@@ -104,15 +104,18 @@ __device__ __forceinline__ void load_gamma(const HeadArgs &a, const void *gamma,
   }
 }
 
-// The angles of a row for a slot.  A row whose position is none of the tables' does not turn.
+// The position of a row; beyond any table where it is negative.
+__device__ __forceinline__ uint64_t position(const HeadArgs &a, uint64_t row) {
+  if (!a.positions) return row;
+  return a.i64 ? (uint64_t)((const int64_t *)a.positions)[row] : (uint64_t)(int64_t)((const int32_t *)a.positions)[row];
+}
+
+// The angles of a position for a slot.  A row whose position is none of the tables' does not turn.
 template <int P>
 struct Angles {
   float c[P], s[P];
   bool turns;
-  __device__ __forceinline__ void load(const HeadArgs &a, uint64_t row, const Slot &t) {
-    uint64_t at = row;
-    if (a.positions)
-      at = a.i64 ? (uint64_t)((const int64_t *)a.positions)[row] : (uint64_t)(int64_t)((const int32_t *)a.positions)[row];
+  __device__ __forceinline__ void load(const HeadArgs &a, uint64_t at, const Slot &t) {
     turns = t.pairs > 0 && at < a.table_rows;
     const uint64_t from = turns ? at * a.half + t.angle : 0;
     const int n = turns ? t.pairs : 0;
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(256) void k_heads(HeadArgs a) {
 #pragma unroll
       for (int s = 0; s < S; ++s)
         if (h0 + s * kGroups < side.heads) x[s].load((const T *)side.x + row * side.ldx + (h0 + s * kGroups) * a.dim, slot);
-      angles.load(a, row, slot);
+      angles.load(a, position(a, row), slot);
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         if (h0 + s * kGroups >= side.heads) break;
@@ -213,80 +216,76 @@ __device__ __forceinline__ float slots_sum(float x) {
   return x;
 }
 
-constexpr int kBackWaves = 16;
+constexpr int kBackWaves = 16, kFlight = 2;
 
 // The gradient: one pass over x and dy, the statistics made anew.  The waves of a work-group are shared
 // out between queries and keys, a.waves_q for those, so that each keeps one gamma and its gradient's sums
 // in registers over all its rows; at the end a work-group's sums go to the workspace as one line for each.
-// A wave's unit is `steps` steps of one row, or all of them where there are rows enough; the next step's
-// elements are loaded before the present one's are used.
+// A wave goes from step to step through all rows.  Bound by the time that its loads take: two steps are on
+// their way, and the next one's position (bf16 8192x(32+8)x128 53.8 us; one step, and all of a row's to
+// a wave, 64; three and four steps 55.6).  Four elements to a vector rather than eight leave the
+// registers for that.
 template <class T, int P, int kLanes, bool kNeighbours, bool kOnce>
 __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
   constexpr uint32_t kGroups = 64 / kLanes;
+  constexpr int kAhead = P > 4 ? 1 : kFlight;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), group = (threadIdx.x & 63) / kLanes;
   const Slot slot = slot_of<P, kNeighbours>(a, threadIdx.x % kLanes);
   const float inv = 1.0f / (float)a.dim;
   const bool key = wave >= a.waves_q;
   const Side &side = a.side[key];
   const uint32_t waves = key ? kBackWaves - a.waves_q : a.waves_q, stride = gridDim.x * waves;
+  const uint32_t units = (uint32_t)a.rows * side.units;  // steps of all rows
   float acc[2 * P], g[2 * P];
 #pragma unroll
   for (int e = 0; e < 2 * P; ++e) acc[e] = 0.0f;
   load_gamma<P, T>(a, side.gamma, slot, g);
-  uint32_t unit = blockIdx.x * waves + (key ? wave - a.waves_q : wave);
-  const uint32_t units = (uint32_t)a.rows * side.units;
-  uint64_t row = side.by_units.of(unit);
-  uint32_t step = (unit - (uint32_t)row * side.units) * side.steps, end = step + side.steps;
-  Raw<kOnce, P, T> next_x, next_d;
-  Angles<P> next_angles, angles;
-  const auto load = [&] {  // the head of this lane's group at (row, step), if there is one
-    const uint32_t h = step * kGroups + group;
-    if (h >= side.heads) return;
-    next_x.load((const T *)side.x + row * side.ldx + h * a.dim, slot);
-    next_d.load((const T *)side.dy + row * side.lddy + h * a.dim, slot);
+  Raw<kOnce, P, T> in_x[kAhead], in_d[kAhead];
+  Angles<P> angles[kAhead];
+  uint32_t unit = blockIdx.x * waves + (key ? wave - a.waves_q : wave), loaded = unit;
+  uint64_t pos = loaded < units ? position(a, side.by_units.of(loaded)) : 0;
+  // The head of this lane's group in a step: the row, and the head's first element.  Groups behind the
+  // last head load it too.
+  const auto load = [&](int k) {
+    if (loaded < units) {
+      const uint32_t row = side.by_units.of(loaded), h = (loaded - row * side.units) * kGroups + group;
+      const uint32_t at = (h < side.heads ? h : side.heads - 1) * a.dim;
+      in_x[k].load((const T *)side.x + row * side.ldx + at, slot);
+      in_d[k].load((const T *)side.dy + row * side.lddy + at, slot);
+      angles[k].load(a, pos, slot);
+    }
+    loaded += stride;
+    if (loaded < units) pos = position(a, side.by_units.of(loaded));
   };
-  bool more = unit < units;
-  if (more) {
-    load();
-    next_angles.load(a, row, slot);
-  }
-  bool turn_page = true;  // the step is a unit's first
-  while (more) {
-    const Raw<kOnce, P, T> in_x = next_x, in_d = next_d;
-    if (turn_page) angles = next_angles;
-    const uint64_t at_row = row;
-    const uint32_t h = step * kGroups + group;
-    turn_page = ++step == end || step * kGroups >= side.heads;
-    if (turn_page) {
-      unit += stride;
-      more = unit < units;
-      row = side.by_units.of(unit);
-      step = (unit - (uint32_t)row * side.units) * side.steps;
-      end = step + side.steps;
-    }
-    if (more) {
-      load();
-      if (turn_page) next_angles.load(a, row, slot);
-    }
-    if (h < side.heads) {
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) load(k);
+  while (unit < units) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (unit >= units) break;
+      const uint32_t row = side.by_units.of(unit), h = (unit - row * side.units) * kGroups + group;
       float x[2 * P], d[2 * P], s[2] = {0.0f, 0.0f};
-      in_x.floats(x);
-      in_d.floats(d);
-      angles.template turn<kNeighbours, true>(d);
+      in_x[k].floats(x);
+      in_d[k].floats(d);
+      angles[k].template turn<kNeighbours, true>(d);
+      load(k);
+      unit += stride;
+      const bool here = h < side.heads;
 #pragma unroll
       for (int e = 0; e < 2 * P; ++e) s[0] = __builtin_fmaf(x[e], x[e], s[0]);
       const float rstd = rsqrt_any(__builtin_fmaf(lanes_sum<kLanes>(s[0]), inv, a.eps));
 #pragma unroll
       for (int e = 0; e < 2 * P; ++e) {
         x[e] *= rstd;  // h
-        acc[e] = __builtin_fmaf(d[e], x[e], acc[e]);
+        const float to = __builtin_fmaf(d[e], x[e], acc[e]);
+        acc[e] = here ? to : acc[e];
         d[e] *= g[e];
         s[1] = __builtin_fmaf(d[e], x[e], s[1]);
       }
       const float m = lanes_sum<kLanes>(s[1]) * inv;
 #pragma unroll
       for (int e = 0; e < 2 * P; ++e) d[e] = rstd * __builtin_fmaf(-x[e], m, d[e]);
-      store_slot<P, T>((T *)side.out + at_row * side.ldo + h * a.dim, slot, d);
+      if (here) store_slot<P, T>((T *)side.out + row * side.ldo + h * a.dim, slot, d);
     }
   }
   if (!a.partial) return;
@@ -314,7 +313,6 @@ __global__ __launch_bounds__(64 * kBackWaves) void k_heads_bwd(HeadArgs a) {
 
 // ---- launches ----
 constexpr int kSteps = 4, kForwardP = 8;
-constexpr uint64_t kRowsEach = 8;
 constexpr uint64_t kMostDim = 512;  // 64 lanes of 8 f32 elements
 
 template <class T>
@@ -339,13 +337,10 @@ struct Heads {
     uint64_t grid = 1;
     for (int k = 0; k < 2; ++k) {
       if (!steps[k]) continue;
-      // a whole row to a wave where that leaves none without work
       const uint64_t waves = k ? kBackWaves - q : q;
-      Side &side = a.side[k];
-      side.steps = a.rows >= kRowsEach * 256 * waves ? (uint32_t)steps[k] : 1;
-      side.units = (uint32_t)((steps[k] + side.steps - 1) / side.steps);
-      side.by_units = Divisor(side.units);
-      const uint64_t sets = (a.rows * side.units + waves - 1) / waves;
+      a.side[k].units = (uint32_t)steps[k];
+      a.side[k].by_units = Divisor(steps[k]);
+      const uint64_t sets = (a.rows * steps[k] + waves - 1) / waves;
       grid = sets > grid ? sets : grid;
     }
     if (grid > kMaxLines) grid = kMaxLines;
@@ -402,7 +397,7 @@ struct HeadCall {
   tk_status check_numbers() const {
     if (!(eps >= 0.0f && eps < INFINITY) || (flags & ~kHeadFlags) || rotary % 2 || rotary > dim) return TK_EINVAL;
     if (rows >= kMaxDim || dim > kMostDim || heads_q >= kMaxDim || heads_k >= kMaxDim) return TK_ERANGE;
-    if ((heads_q + heads_k) * dim >= kMaxDim) return TK_ERANGE;
+    if ((heads_q + heads_k) * dim >= kMaxDim || rows * (heads_q + heads_k) >= kMaxDim) return TK_ERANGE;
     return TK_OK;
   }
   bool empty() const { return rows == 0 || dim == 0 || heads_q + heads_k == 0; }
@@ -444,7 +439,7 @@ static tk_status head_forward(HeadCall h, const void *q, uint64_t ldq, const voi
     c.matrix_of(x[i], h.rows, h.width(i), ldx[i], c.t(), false, true, i ? kKeys : kQueries);
     c.matrix_of(y[i], h.rows, h.width(i), ldy[i], c.t(), true, true, i ? kKeys : kQueries);
     c.vector(gamma[i], h.dim, c.par(), false, false);
-    h.a.side[i] = Side{x[i], nullptr, gamma[i], y[i], ldx[i], 0, ldy[i], 0, 0, 0, {}};
+    h.a.side[i] = Side{x[i], nullptr, gamma[i], y[i], ldx[i], 0, ldy[i], 0, 0, {}};
   }
   if ((st = h.angles(c, positions, table_rows, cosines, sines)) != TK_OK || (st = c.done()) != TK_OK) return st;
   h.a.once = h.rows * (h.width(0) + h.width(1)) * c.t() > kCachedReads;
@@ -481,7 +476,7 @@ static tk_status head_backward(HeadCall h, const void *dyq, uint64_t lddyq, cons
     c.matrix_of(dy[i], h.rows, h.width(i), lddy[i], c.t(), false, true, kind);
     c.matrix_of(dx[i], h.rows, h.width(i), lddx[i], c.t(), true, true, kind);
     c.vector(gamma[i], h.dim, c.par(), false, false);
-    h.a.side[i] = Side{x[i], dy[i], gamma[i], dx[i], ldx[i], lddy[i], lddx[i], 0, 0, 0, {}};
+    h.a.side[i] = Side{x[i], dy[i], gamma[i], dx[i], ldx[i], lddy[i], lddx[i], 0, 0, {}};
   }
   const uint64_t need = sums ? head_bytes(h.rows, h.heads_q, h.heads_k, h.dim) : 0;
   if (!serves(workspace, bytes, need)) return TK_EINVAL;
@@ -501,7 +496,7 @@ extern "C" {
 tk_status tk_head_norm_workspace_bytes(uint64_t rows, uint64_t heads_q, uint64_t heads_k, uint64_t dim, uint64_t *bytes) {
   if (!bytes) return TK_EINVAL;
   if (rows >= tk::kMaxDim || heads_q >= tk::kMaxDim || heads_k >= tk::kMaxDim || dim > tk::kMostDim ||
-      (heads_q + heads_k) * dim >= tk::kMaxDim)
+      (heads_q + heads_k) * dim >= tk::kMaxDim || rows * (heads_q + heads_k) >= tk::kMaxDim)
     return TK_ERANGE;
   *bytes = tk::head_bytes(rows, heads_q, heads_k, dim);
   return TK_OK;

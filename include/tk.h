@@ -358,7 +358,7 @@ tk_status tk_embedding_backward_bf16(uint32_t key, uint64_t start_draw, uint64_t
  *   In place: yq may be q and yk k; dq may be q or dyq, dk k or dyk (same address and ld).  No other
  *          output may share bytes with any other argument.
  *   rotary must be even and at most dim, else TK_EINVAL; dim is at most 512, and rows, a row's
- *   elements, table_rows and the lds are below 2^31, else TK_ERANGE.  rows == 0, dim == 0 or no head at
+ *   elements, the heads of all rows, table_rows and the lds are below 2^31, else TK_ERANGE.  rows == 0, dim == 0 or no head at
  *   all is TK_OK with nothing to write but gradients of gammas, which are zeros.
  *   workspace (backward with dgamma_q or dgamma_k): at least the bytes that
  *   tk_head_norm_workspace_bytes names, 4-byte aligned; rules as above.                        */

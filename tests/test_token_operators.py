@@ -172,7 +172,7 @@ def test_embedding_beyond_32_bits():
 # ---- heads ----
 # dim, rotary: one element, no pairs, all and parts of a head, odd widths, every number of lanes
 DIMS = [(1, 0), (2, 2), (8, 8), (16, 16), (17, 6), (32, 32), (33, 32), (64, 64), (65, 16), (80, 40), (96, 96), (100, 10),
-        (128, 128), (128, 64), (130, 130), (192, 64), (256, 256), (300, 100), (500, 2), (512, 512), (511, 510)]
+        (128, 128), (128, 64), (130, 130), (192, 64), (256, 256), (300, 100), (500, 2), (512, 512), (511, 510), (512, 2)]
 HEADS = [(1, 0), (0, 3), (5, 2), (32, 8), (7, 7), (1, 1)]
 
 
@@ -404,6 +404,20 @@ def test_checkpoint_is_cut_at_any_row_and_right_on_average():
     tk.tk_checkpoint_f32(4, 0, 4096, 128, 0, x, None, codes, None, scales)
     mean = (codes.double() * scales.double()[:, None]).mean(0)
     assert bool(((mean - x[0].double()).abs() <= 6 * 0.5 / 64 * float(scales[0])).all())
+
+
+def test_checkpoint_of_very_many_rows():
+    """More chunks than one launch takes (2^30): rows of one column, each a block."""
+    rows, n = (1 << 27) + 5, 1000
+    log("checkpoint of very many rows")
+    x = torch.ones(rows, 1, dtype=torch.bfloat16, device="cuda")
+    x[-n:, 0] = torch.randn(n, device="cuda").bfloat16()
+    codes, scales = torch.full((rows, 1), 99, dtype=torch.int8, device="cuda"), torch.full((rows,), FILL, device="cuda")
+    tk.tk_checkpoint_bf16(4, 9, rows, 1, 0, x, None, codes, None, scales)
+    assert bool((codes[:-n] == 127).all())
+    c, s = tok.checkpoint(x[-n:].float().cpu().numpy(), 4, 9 + rows - n)
+    assert np.array_equal(codes[-n:].cpu().numpy(), c) and np.array_equal(scales[-n:].cpu().numpy(), s[:, 0])
+    assert bool((scales[:-n] == scales[0]).all())
 
 
 def test_checkpoint_at_the_counters_end():

@@ -105,6 +105,7 @@ def test_bad_numbers(t):
         assert f(t, hq=1 << 31) == ERANGE and f(t, hk=1 << 31) == ERANGE
         assert f(t, hq=1 << 28, ldq=(1 << 31) - 1) == ERANGE  # a row's elements
         assert f(t, tab=1 << 31) == ERANGE
+        assert f(t, rows=1 << 30, hq=1, hk=1, ldq=8, ldk=8) == ERANGE  # the heads of all rows
     for f in (pack, unpack):
         for bad in (tk.TK_PARAMS_F32, tk.TK_INDEX_I64, tk.TK_ACCUMULATE):
             assert f(t, flags=bad) == EINVAL
@@ -203,7 +204,7 @@ def test_workspace_sizes():
     assert tk.tk_embedding_workspace_bytes(8, 8, 0) == 0
     assert tk.tk_head_norm_workspace_bytes(0, 4, 2, 8) == tk.tk_head_norm_workspace_bytes(4, 0, 0, 8) == 0
     for dim in (1, 64, 65, 512):
-        sizes = [tk.tk_head_norm_workspace_bytes(r, 4, 2, dim) for r in (1, 2, 100, 1 << 20, (1 << 31) - 1)]
+        sizes = [tk.tk_head_norm_workspace_bytes(r, 4, 2, dim) for r in (1, 2, 100, 1 << 20, (1 << 28) - 1)]
         assert sizes == sorted(sizes)
     v = C.c_uint64()
     assert L.tk_embedding_workspace_bytes(4, 8, 8, None) == EINVAL
