@@ -468,11 +468,14 @@ static tk_status sort_tokens(SortArgs a, hipStream_t s) {
     a.ranges = (a.vocab + range - 1) / range;
     hipLaunchKernelGGL(kernel, dim3(a.ranges < 1u << 16 ? a.ranges : 1u << 16), dim3(64 * kSortWaves), 0, s, a);
   };
-  // one work-group to a compute unit where the vocabulary allows: each reads all rows
-  if (a.vocab <= 64 * 256) go(a.ids64 ? k_sort_tokens<64, true> : k_sort_tokens<64, false>, 64);
-  else if (a.vocab <= 128 * 256) go(a.ids64 ? k_sort_tokens<128, true> : k_sort_tokens<128, false>, 128);
-  else if (a.vocab <= 256 * 256) go(a.ids64 ? k_sort_tokens<256, true> : k_sort_tokens<256, false>, 256);
-  else go(a.ids64 ? k_sort_tokens<512, true> : k_sort_tokens<512, false>, 512);
+  // The smallest range that makes one work-group to a compute unit, as each reads all rows: the fewer
+  // tokens it has, the fewer of the rows are its own (23233 rows of 1533 tokens, text-like, with a range
+  // of 8 and of 64: 16.1 and 19.4 us).
+  const bool wide = a.ids64;
+  if (a.vocab <= 8 * 256) go(wide ? k_sort_tokens<8, true> : k_sort_tokens<8, false>, 8);
+  else if (a.vocab <= 32 * 256) go(wide ? k_sort_tokens<32, true> : k_sort_tokens<32, false>, 32);
+  else if (a.vocab <= 128 * 256) go(wide ? k_sort_tokens<128, true> : k_sort_tokens<128, false>, 128);
+  else go(wide ? k_sort_tokens<512, true> : k_sort_tokens<512, false>, 512);
   return launch_status();
 }
 

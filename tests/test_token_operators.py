@@ -15,10 +15,10 @@ from test_row_operators import FILL, IDS, KINDS, Maker, flags, fn, types
 pytestmark = pytest.mark.gpu
 
 # rows, cols, vocab: single ones, both sides of a tile of 64 rows, of a strip's and a lane's columns, of the
-# sort's ranges of 64, 128, 256 and 512 tokens, and of more than 1024 tiles
+# sort's ranges of 8, 32, 128 and 512 tokens, and many tiles
 LOOKUPS = [(1, 1, 1), (3, 7, 5), (64, 16, 1), (65, 8, 4), (130, 65, 3), (1000, 129, 50), (5000, 40, 17), (2047, 513, 700),
-           (300, 2049, 4000), (1500, 264, 16384), (1500, 130, 16385), (700, 33, 32769), (500, 100, 65537), (66000, 5, 900),
-           (4099, 1032, 200), (40, 8200, 30)]
+           (300, 2049, 4000), (1500, 264, 16384), (1500, 130, 32768), (700, 33, 32769), (500, 100, 65537), (66000, 5, 900),
+           (4099, 1032, 200), (40, 8200, 30), (200, 12, 2048), (200, 12, 2049), (300, 20, 8192), (300, 20, 8193)]
 SPREADS = ("even", "skewed", "one", "outside")
 
 
