@@ -130,8 +130,9 @@ struct Lane<bf16_t> {
 // below ceil(t 2^24) - 2^24 floor(t), so below t's fraction, and -floor(t) elsewhere.
 // The largest magnitude is taken among the bit patterns, where NaN is above infinity.
 //
-// Bound by its instructions: 3 bytes move for every element.  Sixteen elements to a lane share what
-// a lane does once.
+// Bound by memory and by its instructions alike, as only 3 bytes move for an element: bf16 16384x8192 72 us,
+// 5.6 TB/s, of which 57 are the time of its 273 vector instructions a wave (17 an element).  Sixteen elements to
+// a lane share what a lane does once: with eight, and each code's sign and rounding apart, 99 us.
 //
 // kWide: a wave takes 64 chunks of one row, so that rows and their addresses are the scalar unit's;
 // else the chunks of all rows follow each other.

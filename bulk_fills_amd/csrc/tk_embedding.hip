@@ -24,6 +24,9 @@ __device__ __forceinline__ uint64_t token(const void *ids, bool ids64, uint64_t 
   return ids64 ? (uint64_t)((const int64_t *)ids)[row] : (uint64_t)(int64_t)((const int32_t *)ids)[row];
 }
 
+// Bound by memory: bf16 16384x4096 from a table of 131072 rows, with dropout, 47 us, 5.5 TB/s (one chunk to a
+// lane 50, four 49; a row's address made by every lane for itself 58).
+//
 // A lane takes V chunks, 64 apart.  Rows come from anywhere in the table, so nothing is gained by going
 // on from one to the next: many waves hide the two loads that wait for each other (the token, then its
 // row).  kWide: a wave takes 64 V chunks of one row, whose token and address are the scalar unit's; else
@@ -225,6 +228,9 @@ struct GradArgs {
 // gradient.  Of a token that goes past an end of the tile it writes the sum so far, to a line of the
 // workspace: the tile's first line if the token begins before the tile, else its second.  k_join adds
 // those lines up in the order of the tiles.
+//
+// Bound by memory: bf16 16384x4096 into a table of 32768 rows, text-like tokens, 68 us with the rows that are
+// cleared, 5.9 TB/s (with eight rows ahead, at fewer waves, 72; with a wave to each token and strip 128).
 template <class W, class R, bool kDivide, bool kAdd, int CH, int kLanes>
 struct Tile {
   static constexpr int kDeep = 4;
@@ -366,8 +372,9 @@ __global__ __launch_bounds__(256) void k_join(GradArgs a) {
 // ---------------------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------------------
-// Places to a tile: 8, 16, 32 or 64, the most that leave kUnits waves' work (and no more than the lanes of
-// a strip, which hold them).
+// Places to a tile: 8, 16, 32 or 64, the most that leave kUnits waves' work, eight to a compute unit (and no
+// more than the lanes of a strip, which hold them).  The gradient bf16 16384x4096 takes 96.0, 96.1, 97.4 and
+// 112 us with 1024, 2048, 4096 and 8192, which leave more partial lines.
 constexpr uint64_t kUnits = 2048;
 
 struct TilePlan {

@@ -166,7 +166,11 @@ struct Raw {
 // ---- kernels ----
 // A wave takes up to S steps of one row's queries or keys, a step being 64 / kLanes heads of kLanes lanes
 // each: all of its loads are on their way before the first value is used, and the angles and gamma serve
-// all steps.  blockIdx.y counts the queries' steps of a row by S, then the keys'.
+// all steps.  blockIdx.y counts the queries' steps of a row by S, then the keys' (a row's units beside each
+// other take 74 us for 64).
+//
+// Bound by memory: bf16 16384x(32+8)x128 from a projection's rows 63.6 us, 5.3 TB/s (through the caches 68, with
+// two steps 69, with heads one after the other 79).
 template <class T, int P, int kLanes, bool kNeighbours, bool kOnce, int S>
 __global__ __launch_bounds__(256) void k_heads(HeadArgs a) {
   constexpr uint32_t kGroups = 64 / kLanes;
