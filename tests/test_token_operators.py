@@ -133,6 +133,37 @@ def test_embedding_gradients_have_one_order(spread):
     assert all(torch.equal(outs[0], d) for d in outs[1:])
 
 
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[2], KINDS[3]], ids=["f32", "f16-r32-p32", "bf16"])
+@pytest.mark.parametrize("rows,cols", [(2900, 4096), (5000, 4096), (9000, 4096), (17000, 4096), (140000, 100), (140000, 200)])
+def test_embedding_gradients_of_every_tile(kind, rows, cols):
+    """Tiles of 8 to 64 rows, and of 8 to 32 rows of fewer lanes, against sums in float64 on the device."""
+    T, R, W = types(kind)
+    vocab, p = 3000, 0.25
+    g = torch.Generator("cuda").manual_seed(rows)
+    dy = torch.empty(rows, cols, dtype=R, device="cuda").normal_(generator=g)
+    u = torch.empty(rows * cols, device="cuda")
+    tk.tk_fill_f32(8, 5, rows * cols, u)
+    v = torch.where(u.view(rows, cols) >= p, dy.double() / ref.quotient(p), 0.0)
+    for spread in ("even", "skewed", "one"):
+        log(f"tiles {kind} {rows}x{cols} {spread}")
+        ids = tokens(rows, vocab, spread, True, rows)
+        ids[::7] = -1
+        there = (ids >= 0).cuda()
+        at = ids.cuda()[there]
+        want = torch.zeros(vocab, cols, dtype=torch.float64, device="cuda").index_add_(0, at, v[there])
+        size = torch.zeros_like(want).index_add_(0, at, v[there].abs())
+        many = torch.bincount(at, minlength=vocab)[:, None]
+        # each term's quotient (2 u), additions of no more than a token's rows, and the product with the scale
+        bound = 3.0 * size * (many + 3) * ref.U + ref.U * 3 * want.abs()
+        d = torch.full((vocab, cols), FILL, dtype=W, device="cuda")
+        fn("embedding_backward", kind)(8, 5, rows, cols, p, 3.0, flags(kind) | tk.TK_INDEX_I64, vocab, ids.cuda(), dy, None, d,
+                                       None)
+        want = want * 3.0
+        limit = 1.01 * bound + (want.abs() + 1.01 * bound) * torch.finfo(W).eps / 2 + ref.TINY[W]
+        assert not bool(((d.double() - want).abs() > limit).any())
+        assert not bool(d[many[:, 0] == 0].any())
+
+
 def test_embedding_sums_of_one_token_are_float_sums():
     """Whole numbers below 2^24 add up exactly in any order, and only in floats: no 16-bit partial sums."""
     rows, cols = 40000, 24
@@ -275,6 +306,32 @@ def test_heads_of_many_rows(kind):
         # the terms are independent of each other: their roundings too, so the sum's error is far within that
         # bound, and a row left out is not
         assert float((dg.cpu().double() - dgamma[0]).norm() / dgamma[0].norm()) < 1e-5 + torch.finfo(c.W).eps
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[3]], ids=["f32", "bf16"])
+def test_heads_of_large_calls(kind, interleaved):
+    """Calls whose reads pass the caches (over 96 MB of them) against calls on parts of their rows, which do
+    not: bit for bit by rows."""
+    rows, dim = (24000, 256) if kind[0] == "bf16" else (12000, 250)
+    log(f"large heads {kind} {rows}")
+    c = HeadCase(kind, rows, 8, 2, dim, 96, interleaved, 4)
+    g = torch.Generator("cuda").manual_seed(1)
+    mat = lambda n: torch.empty(rows, n * dim, dtype=c.T, device="cuda").normal_(generator=g)  # noqa: E731
+    q, k, dyq, dyk = mat(8), mat(2), mat(8), mat(2)
+    dg = [torch.empty(dim, dtype=c.W, device="cuda") for _ in range(2)]
+    outs = []
+    for parts in (1, 5):
+        o = [torch.full((rows, n * dim), FILL, dtype=c.T, device="cuda") for n in (8, 2, 8, 2)]
+        for i in range(parts):
+            sl = slice(rows * i // parts, rows * (i + 1) // parts)
+            d = HeadCase(kind, 1, 8, 2, dim, 96, interleaved, 4)
+            d.rows, d.positions, d.cu, d.flags = sl.stop - sl.start, c.positions[sl], c.cu, c.flags
+            d.forward(q[sl], k[sl], o[0][sl], o[1][sl])
+            d.backward(dyq[sl], dyk[sl], q[sl], k[sl], o[2][sl], o[3][sl], *dg)
+        outs.append(o)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("kind", [KINDS[0], KINDS[3]], ids=["f32", "bf16"])
