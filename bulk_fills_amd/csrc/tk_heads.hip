@@ -167,7 +167,7 @@ struct Raw {
 // A wave takes up to S steps of one row's queries or keys, a step being 64 / kLanes heads of kLanes lanes
 // each: all of its loads are on their way before the first value is used, and the angles and gamma serve
 // all steps.  blockIdx.y counts the queries' steps of a row by S, then the keys' (a row's units beside each
-// other take 74 us for 64).
+// other take 73 us for 64).
 //
 // Bound by memory: bf16 16384x(32+8)x128 from a projection's rows 63.6 us, 5.3 TB/s (through the caches 68, with
 // two steps 69, with heads one after the other 79).

@@ -164,6 +164,27 @@ def test_embedding_gradients_of_every_tile(kind, rows, cols):
         assert not bool(d[many[:, 0] == 0].any())
 
 
+@pytest.mark.parametrize("cols,gap", [(1, 0), (3, 0), (37, 0), (100, 0), (1001, 0), (4100, 0), (20000, 0), (37, 2), (1001, 7)])
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_embedding_gradient_clears_absent_tokens(kind, cols, gap):
+    """Runs of absent tokens of every length, from a base off the 16-byte lines; nothing beside the table changes."""
+    T, R, W = types(kind)
+    ld, off = cols + gap, 3
+    for vocab, ids in ((1, []), (1, [0]), (64, []), (65, [64]), (131, [0, 63, 64, 130]), (200, [1, 7, 66, 128, 199]), (131, [-1, 131])):
+        log(f"absent {kind} {vocab} of {cols}+{gap} {ids}")
+        buf = torch.full((off + vocab * ld + 5,), FILL, dtype=W, device="cuda")
+        d = buf[off : off + vocab * ld].view(vocab, ld)[:, :cols]
+        at = torch.tensor(ids, dtype=torch.int64, device="cuda")
+        dy = torch.ones(len(ids), cols, dtype=R, device="cuda")
+        want = buf.clone()
+        rows = want[off : off + vocab * ld].view(vocab, ld)[:, :cols]
+        rows.zero_()
+        rows[[i for i in ids if 0 <= i < vocab]] = 1
+        fn("embedding_backward", kind)(1, 0, len(ids), cols, 0.0, 1.0, flags(kind) | tk.TK_INDEX_I64, vocab, at, dy, None, d, ld,
+                                       None)
+        assert torch.equal(buf, want)
+
+
 def test_embedding_sums_of_one_token_are_float_sums():
     """Whole numbers below 2^24 add up exactly in any order, and only in floats: no 16-bit partial sums."""
     rows, cols = 40000, 24
