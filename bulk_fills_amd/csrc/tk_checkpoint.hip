@@ -226,10 +226,11 @@ __global__ __launch_bounds__(256) void k_restore(CodeArgs a) {
   for (int j = 0; j < V; ++j) {
     const uint32_t at = c + j * 64 * CH;
     const int nv = (int)(a.cols - at);
+    const float by = held_scale(scale[j]);
     float v[CH];
     codes[j].floats(nv, v);
 #pragma unroll
-    for (int e = 0; e < CH; ++e) v[e] *= scale[j];
+    for (int e = 0; e < CH; ++e) v[e] *= by;
     if (nv > 0) store_chunk<CH>((R *)a.y + row * a.ldy + at, nv, v);
   }
 }

@@ -574,6 +574,11 @@ struct Codes {
   }
 };
 
+// What a checkpoint's codes are multiplied with: their scale, but at most float's largest over 127,
+// rounded down.  Rounded up, as it is kept for a block that holds that largest, 127 times it would be
+// infinite.  A NaN stays.  (One instruction, where the scale is used: where it is loaded it would wait.)
+__device__ __forceinline__ float held_scale(float s) { return __builtin_elementwise_minimum(s, 0x810203p98f); }
+
 // The scale of a checkpoint's codes at column c of a row (past the row's end its last one's).
 __device__ __forceinline__ float code_scale(const BwdArgs &a, uint64_t row, uint32_t c) {
   return a.scales[row * a.blocks + (c < a.cols ? c / kCodeBlock : a.blocks - 1)];
@@ -604,8 +609,9 @@ struct BwdIn {
   __device__ __forceinline__ void normed(int nv, float mean, float rstd, float *h) const {
     if constexpr (kCodes) sum.floats(nv, h);
     else unpack<CH, S>(sum, nv, h);
+    const float by = kCodes ? held_scale(scale) : 1.0f;
 #pragma unroll
-    for (int e = 0; e < CH; ++e) h[e] = ((kCodes ? h[e] * scale : h[e]) - mean) * rstd;
+    for (int e = 0; e < CH; ++e) h[e] = ((kCodes ? h[e] * by : h[e]) - mean) * rstd;
   }
   // Outputs: dresidual = v + dsum and dx = drop(dresidual), which comes back in v.
   template <bool kX>
@@ -804,7 +810,7 @@ __global__ __launch_bounds__(1024) void k_row_stats(BwdArgs a) {
       float g[CH], h[CH], w[CH];
       const Chunk<T, CH> here_dy = next_dy;
       const auto here_sum = next_sum;
-      const float scale = next_scale;
+      const float scale = kCodes ? held_scale(next_scale) : 1.0f;
       next_dy = load_chunk<false, CH>(dy + at);
       load_sum(at);
       if (kCodes) next_scale = code_scale(a, row, c + kTpr * CH);

@@ -407,7 +407,9 @@ tk_status tk_head_norm_rotate_backward_bf16(uint64_t rows, uint64_t heads_q, uin
  *   code * scale is x on average.  The comparison is exact: equal arguments give equal codes on
  *   any device.
  * A block whose m is below 2^-100 is kept as zeros (scale 0); one that holds an infinity or a NaN comes
- * back as NaN throughout (scale NaN, codes 0).
+ * back as NaN throughout (scale NaN, codes 0).  Where values are made from codes, a scale counts as at most
+ * float's largest / 127 rounded down: that of a block that holds float's largest is one unit of its last
+ * place above, and 127 times it would be infinite.
  *   tk_checkpoint          x (float with TK_RESIDUAL_F32, the only flag) to codes, rows x cols bytes
  *                          `ldc` apart, and scales, rows x ceil(cols / 128) contiguous floats
  *   tk_checkpoint_restore  y = code * scale, rounded once

@@ -466,6 +466,46 @@ def test_checkpoint_of_special_blocks(kind):
     assert not bool(bad.any()) and not bool(y[[0, 8]].any())
 
 
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[2], KINDS[4]], ids=["f32", "f16-r32-p32", "bf16-r32"])
+@pytest.mark.parametrize("cols", [3, 300, 9001])
+def test_checkpoint_of_floats_largest(kind, cols):
+    """A block that holds float's largest, either sign, comes back finite, and the backward passes from its codes
+    see those values.  Its scale, m / 127 rounded, is a step too high: 127 times it is infinite."""
+    T, R, W = types(kind)
+    rows, most = 5, np.finfo(np.float32).max
+    log(f"float's largest {kind} {cols}")
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g)
+    x[0], x[1], x[2, 1], x[3, cols - 1] = float(most), -float(most), float(most), -float(most)
+    codes, scales = torch.empty(rows, cols, dtype=torch.int8, device="cuda"), torch.empty(rows, -(-cols // 128), device="cuda")
+    fl = flags(kind)
+    fn("checkpoint", kind)(8, 3, rows, cols, fl & tk.TK_RESIDUAL_F32, x.cuda(), None, codes, None, scales)
+    c, s = tok.checkpoint(x.numpy(), 8, 3)
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    high = most / np.float32(127)
+    assert int((s == high).sum()) >= 4
+    with np.errstate(over="ignore"):
+        assert np.isinf(high * np.float32(127))
+    held = np.minimum(s, np.nextafter(high, np.float32(0)))  # most / 127 rounded down
+    v = tok.restored(torch.from_numpy(c), torch.from_numpy(held))
+    assert bool(torch.isfinite(v.float()).all())
+    y = torch.empty(rows, cols, dtype=R, device="cuda")
+    fn("checkpoint_restore", kind)(rows, cols, fl & tk.TK_RESIDUAL_F32, codes, None, scales, y, None)
+    assert torch.equal(y.cpu(), v.to(R))
+    # a norm of such rows: as the forward's statistics are inputs, any in range serve
+    mean, rstd = torch.zeros(rows), torch.full((rows,), 2.0 ** -120)
+    m = Maker(rows, cols, 0, 1)
+    (dy, dyr), (ds, dsr), (gamma, gr) = m.mat(T), m.mat(R), m.vec(W, 1.0)
+    dx, dr, dg, db, dbias = m.out(T), m.out(R), m.flat(cols, W), m.flat(cols, W), m.flat(cols, W)
+    fn("dropout_add_layer_norm_backward_checkpoint", kind)(8, 5, rows, cols, 0.25, fl, dy, None, ds, None, codes, None, scales,
+                                                           gamma, mean.cuda(), rstd.cuda(), dx, None, dr, None, dg, db, dbias)
+    want = ref.dropout_add_layer_norm_backward(dyr, dsr, v, gr, mean.double(), rstd.double(), ref.keep_mask(8, 5, rows, cols, 0.25),
+                                               0.25)
+    for name, t in (("dx", dx), ("dresidual", dr), ("dgamma", dg), ("dbeta", db), ("dbias", dbias)):
+        ref.check(t, want[name], f"{kind} {cols} {name}")
+    m.untouched(f"{kind} {cols}")
+
+
 def test_checkpoint_is_cut_at_any_row_and_right_on_average():
     rows, cols = 300, 1111
     x = torch.randn(rows, cols, device="cuda").bfloat16()
