@@ -164,6 +164,40 @@ def test_embedding_gradients_of_every_tile(kind, rows, cols):
         assert not bool(d[many[:, 0] == 0].any())
 
 
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("rows,cols", [(1500, 4096), (2900, 4096), (5000, 4096), (9000, 4096), (17000, 4096), (140000, 3),
+                                       (140000, 20), (140000, 40), (140000, 100), (140000, 200), (20, 300000)])
+def test_embedding_gradients_are_whole(kind, rows, cols):
+    """No row or tile left out or taken twice, also where one token has them all: small whole numbers, whose sums
+    below 2^24 are exact in floats in any order, so the result is the exact sum rounded to the table's type.
+    With p 1/2 an element counts twice or not at all.  Tiles of 8, 16, 32 and 64 rows at each number of lanes
+    that has them, more tiles and more columns than a launch of the join takes at once."""
+    T, R, W = types(kind)
+    vocab, fl = 300, flags(kind) | tk.TK_INDEX_I64
+    g = torch.Generator("cuda").manual_seed(rows + cols)
+    dy = torch.randint(-3, 4, (rows, cols), generator=g, device="cuda").to(R)
+    u = torch.empty(rows * cols, device="cuda")
+    tk.tk_fill_f32(8, 5, rows * cols, u)
+    for i, spread in enumerate(("even", "skewed", "one")):
+        p = (0.0, 0.5, 0.5)[i] if rows % 2000 else (0.5, 0.0, 0.0)[i]
+        log(f"whole {kind} {rows}x{cols} {spread} p {p}")
+        ids = tokens(rows, vocab, spread, True, rows)
+        ids[::11] = -1
+        there = (ids >= 0).cuda()
+        at = ids.cuda()[there]
+        v = dy.double() if p == 0 else torch.where(u.view(rows, cols) >= p, dy.double() * 2, 0.0)
+        want = torch.zeros(vocab, cols, dtype=torch.float64, device="cuda").index_add_(0, at, v[there]) * 2
+        assert 2 * 6 * rows < 1 << 24
+        d = torch.full((vocab, cols), FILL, dtype=W, device="cuda")
+        run = lambda f: fn("embedding_backward", kind)(8, 5, rows, cols, p, 2.0, f, vocab, ids.cuda(), dy, None, d, None)  # noqa: E731
+        run(fl)
+        assert torch.equal(d, want.to(W)), (kind, rows, cols, spread)
+        d.copy_(torch.randint(-100, 101, (vocab, cols), generator=g, device="cuda"))
+        want += d.double()
+        run(fl | tk.TK_ACCUMULATE)
+        assert torch.equal(d, want.to(W)), (kind, rows, cols, spread, "accumulate")
+
+
 @pytest.mark.parametrize("cols,gap", [(1, 0), (3, 0), (37, 0), (100, 0), (1001, 0), (4100, 0), (20000, 0), (37, 2), (1001, 7)])
 @pytest.mark.parametrize("kind", KINDS, ids=IDS)
 def test_embedding_gradient_clears_absent_tokens(kind, cols, gap):
