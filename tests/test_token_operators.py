@@ -255,6 +255,51 @@ def test_embedding_beyond_32_bits():
         assert bool((buf.as_strided((vocab - 1, ld - cols), (ld, 1), cols) == (0 if fl else FILL)).all())
 
 
+@pytest.mark.parametrize("vocab", [(1 << 25) + 700, (1 << 28) + 900], ids=["2^25", "2^28"])
+def test_embedding_gradient_of_more_tokens_than_a_grid(vocab):
+    """The sort's work-groups take further ranges of tokens, and those that clear further rows."""
+    log(f"gradient of {vocab} tokens")
+    edges = [k for r in range(0, vocab, 1 << 25) for k in (r, r + 1, r + 511, r + 512, r + 699)] + [(1 << 28) - 1, 1 << 28, vocab - 1]
+    edges = torch.tensor([k for k in edges if k < vocab])
+    g = torch.Generator().manual_seed(3)
+    ids = edges[torch.randint(0, len(edges), (3000,), generator=g)]
+    ids[:len(edges)] = edges  # each of them, and many rows of some
+    ids[700:1400] = vocab - 1
+    ids[5::50] = -1
+    ids[6::50] = vocab
+    dy = torch.randint(1, 4, (3000, 1), generator=g).bfloat16().cuda()
+    there = (ids >= 0) & (ids < vocab)
+    want = torch.zeros(vocab, dtype=torch.float32, device="cuda").index_add_(0, ids[there].cuda(), dy[there.cuda(), 0].float())
+    buf = torch.full((vocab + 8,), FILL, dtype=torch.bfloat16, device="cuda")
+    d = buf[3:3 + vocab].view(vocab, 1)
+    tk.tk_embedding_backward_bf16(1, 0, 3000, 1, 0.0, 1.0, tk.TK_INDEX_I64, vocab, ids.cuda(), dy, None, d, None)
+    assert torch.equal(d[:, 0], want.bfloat16()) and bool((buf[:3] == FILL).all()) and bool((buf[-5:] == FILL).all())
+    d.fill_(1.0)
+    tk.tk_embedding_backward_bf16(1, 0, 3000, 1, 0.0, 1.0, tk.TK_INDEX_I64 | tk.TK_ACCUMULATE, vocab, ids.cuda(), dy, None, d, None)
+    assert torch.equal(d[:, 0], (want + 1.0).bfloat16())
+
+
+def test_embedding_of_more_rows_than_a_launch():
+    """2^30 chunks are a launch's: rows of one column beyond it, also with the counters' range nearly used up."""
+    rows, n, vocab = (1 << 30) + 1000, 3000, 97
+    log("embedding of more rows than a launch")
+    table = torch.arange(1, vocab + 1, device="cuda").bfloat16().view(vocab, 1)
+    ids = torch.full((rows,), 41, dtype=torch.int32, device="cuda")
+    ids[-n:] = torch.randint(-5, vocab + 5, (n,), device="cuda", dtype=torch.int32)
+    y = torch.full((rows, 1), FILL, dtype=torch.bfloat16, device="cuda")
+    tk.tk_embedding_bf16(4, 9, rows, 1, 0.0, 2.0, 0, vocab, ids, table, None, y, None)
+    tail = ids[-n:].long()
+    there = (tail >= 0) & (tail < vocab)
+    assert torch.equal(y[-n:, 0], torch.where(there, 2 * table[tail.clamp(0, vocab - 1), 0], 0.0))
+    assert bool((y[:-n] == 84.0).all())
+    tk.tk_embedding_bf16(4, 9, rows, 1, 0.5, 2.0, 0, vocab, ids, table, None, y, None)
+    for lo in (0, (1 << 30) - 1500):  # both sides of the cut
+        hi = min(lo + 2500, rows)
+        part = torch.empty(hi - lo, 1, dtype=torch.bfloat16, device="cuda")
+        tk.tk_embedding_bf16(4, 9 + lo, hi - lo, 1, 0.5, 2.0, 0, vocab, ids[lo:hi], table, None, part, None)
+        assert torch.equal(y[lo:hi], part)
+
+
 # ---- heads ----
 # dim, rotary: one element, no pairs, all and parts of a head, odd widths, every number of lanes
 DIMS = [(1, 0), (2, 2), (8, 8), (16, 16), (17, 6), (32, 32), (33, 32), (64, 64), (65, 16), (80, 40), (96, 96), (100, 10),
@@ -387,6 +432,63 @@ def test_heads_of_large_calls(kind, interleaved):
         outs.append(o)
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+def test_heads_of_more_rows_than_a_grid():
+    """Past 2^22 rows a wave goes on to further ones."""
+    rows = (1 << 22) + 9
+    log("heads of more rows than a grid")
+    g = torch.Generator("cuda").manual_seed(1)
+    q, dy = (torch.empty(rows, 2, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(2))
+    pos = torch.randint(-1, 51, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    angle = torch.rand(50, 1, generator=g, device="cuda") * 7
+    cos, sin = angle.cos(), angle.sin()
+    outs = []
+    for cuts in ((0, rows), (0, 5, 1 << 21, (1 << 22) - 3, rows)):
+        y, d = (torch.full((rows, 2), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        for lo, hi in zip(cuts, cuts[1:]):
+            at = slice(lo, hi)
+            tk.tk_head_norm_rotate_bf16(hi - lo, 1, 0, 2, 2, 1e-5, 0, q[at], None, None, None, None, None, pos[at], 50, cos, sin, y[at],
+                                        None, None, None)
+            tk.tk_head_norm_rotate_backward_bf16(hi - lo, 1, 0, 2, 2, 1e-5, 0, dy[at], None, None, None, q[at], None, None, None, None,
+                                                 None, pos[at], 50, cos, sin, d[at], None, None, None, None, None)
+        outs.append((y, d))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    n = 2000  # and against the definition at both ends
+    for at in (slice(0, n), slice(rows - n, rows)):
+        p = pos[at].long().cpu()
+        there = ((p >= 0) & (p < 50))[:, None]
+        c = torch.where(there, cos.cpu()[p.clamp(0, 49)].double(), 1.0)
+        s = torch.where(there, sin.cpu()[p.clamp(0, 49)].double(), 0.0)
+        x, e = tok.head_norm_rotate(q[at].cpu().double().view(n, 1, 2), None, c, s, False, 1e-5)
+        ref.check(outs[0][0][at], (x.view(n, 2), e.view(n, 2)), "far rows")
+        x, e = tok.head_norm_rotate_backward(dy[at].cpu().double().view(n, 1, 2), q[at].cpu().double().view(n, 1, 2), None, c, s, False,
+                                             1e-5)["dx"]
+        ref.check(outs[0][1][at], (x.view(n, 2), e.view(n, 2)), "far rows' gradient")
+
+
+@pytest.mark.parametrize("hq,hk", [(140000, 9), (600000, 1000)])
+def test_heads_of_more_heads_than_a_grid(hq, hk):
+    """Past 4096 units a row's work-groups go on to further heads: the bits of as many rows of one head."""
+    log(f"{hq}+{hk} heads")
+    g = torch.Generator("cuda").manual_seed(hq)
+    q, k, dyq, dyk = (torch.empty(1, n * 2, device="cuda").normal_(generator=g) for n in (hq, hk, hq, hk))
+    gamma = [1 + 0.3 * torch.randn(2, generator=g, device="cuda") for _ in range(2)]
+    angle = torch.rand(9, 1, generator=g, device="cuda") * 7
+    cos, sin = angle.cos(), angle.sin()
+    yq, yk, dq, dk = (torch.full_like(t, FILL) for t in (q, k, q, k))
+    pos = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    tail = (*gamma, pos, 9, cos, sin)
+    tk.tk_head_norm_rotate_f32(1, hq, hk, 2, 2, 1e-5, 0, q, None, k, None, *tail, yq, None, yk, None)
+    tk.tk_head_norm_rotate_backward_f32(1, hq, hk, 2, 2, 1e-5, 0, dyq, None, dyk, None, q, None, k, None, *tail, dq, None, dk, None,
+                                        None, None)
+    for x, dy, y, d, ga, n in ((q, dyq, yq, dq, gamma[0], hq), (k, dyk, yk, dk, gamma[1], hk)):
+        at, y1, d1 = pos.expand(n).contiguous(), torch.empty(n, 2, device="cuda"), torch.empty(n, 2, device="cuda")
+        one = lambda t: t.view(n, 2)  # noqa: E731
+        tk.tk_head_norm_rotate_f32(n, 1, 0, 2, 2, 1e-5, 0, one(x), None, None, None, ga, None, at, 9, cos, sin, y1, None, None, None)
+        tk.tk_head_norm_rotate_backward_f32(n, 1, 0, 2, 2, 1e-5, 0, one(dy), None, None, None, one(x), None, None, None, ga, None, at, 9,
+                                            cos, sin, d1, None, None, None, None, None)
+        assert torch.equal(one(y), y1) and torch.equal(one(d), d1)
 
 
 @pytest.mark.parametrize("kind", [KINDS[0], KINDS[3]], ids=["f32", "bf16"])
@@ -570,6 +672,20 @@ def test_checkpoint_of_very_many_rows():
     c, s = tok.checkpoint(x[-n:].float().cpu().numpy(), 4, 9 + rows - n)
     assert np.array_equal(codes[-n:].cpu().numpy(), c) and np.array_equal(scales[-n:].cpu().numpy(), s[:, 0])
     assert bool((scales[:-n] == scales[0]).all())
+
+
+def test_restore_of_very_many_rows():
+    """More chunks than one launch of the restore takes (2^30): rows of one column."""
+    rows, n = (1 << 30) + 700, 2000
+    log("restore of very many rows")
+    codes = torch.full((rows, 1), 3, dtype=torch.int8, device="cuda")
+    scales = torch.full((rows,), 0.5, device="cuda")
+    codes[-n:, 0] = torch.randint(-127, 128, (n,), device="cuda", dtype=torch.int8)
+    scales[-n:] = torch.rand(n, device="cuda")
+    y = torch.full((rows, 1), FILL, dtype=torch.bfloat16, device="cuda")
+    tk.tk_checkpoint_restore_bf16(rows, 1, 0, codes, None, scales, y, None)
+    assert torch.equal(y[-n:, 0], (codes[-n:, 0].float() * scales[-n:]).bfloat16())
+    assert bool((y[:-n] == 1.5).all())
 
 
 def test_checkpoint_at_the_counters_end():
