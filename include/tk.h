@@ -300,9 +300,10 @@ tk_status tk_dropout_add_layer_norm_backward_bf16(uint32_t key, uint64_t start_d
  * +0.0 and goes into no gradient; its dy is not read.
  *   flags: TK_RESIDUAL_F32  y and dy are float       TK_PARAMS_F32  table and dtable are float
  *          TK_INDEX_I64     ids are int64
- *          TK_ACCUMULATE    (backward) the sums are added to what dtable holds, rounded once; rows of
- *                           it whose token does not occur are neither read nor written.  Without it
- *                           every row is written, with zeros where its token does not occur.
+ *          TK_ACCUMULATE    (backward) scale * sum, rounded to a float, is added to what dtable holds, as
+ *                           floats, and that rounded to dtable's type; rows of it whose token does not
+ *                           occur are neither read nor written.  Without it every row is written, with
+ *                           zeros where its token does not occur.
  * The gradient's sums are float, over the rows in their order: equal arguments give equal bits.
  * Nothing is updated concurrently, so a token of every row costs no more than others.
  *   scale must be finite, else TK_EINVAL; rows, cols, vocab and the lds are below 2^31, else TK_ERANGE.
@@ -412,7 +413,7 @@ tk_status tk_head_norm_rotate_backward_bf16(uint64_t rows, uint64_t heads_q, uin
  * place above, and 127 times it would be infinite.
  *   tk_checkpoint          x (float with TK_RESIDUAL_F32, the only flag) to codes, rows x cols bytes
  *                          `ldc` apart, and scales, rows x ceil(cols / 128) contiguous floats
- *   tk_checkpoint_restore  y = code * scale, rounded once
+ *   tk_checkpoint_restore  y = code * scale, a float's product, rounded to y's type
  *   tk_layer_norm_backward_checkpoint, tk_dropout_add_layer_norm_backward_checkpoint
  *                          the backward passes of the row operators with the checkpoint in place of x or
  *                          sum, its values float; mean and rstd are the forward's

@@ -255,6 +255,25 @@ def test_embedding_beyond_32_bits():
         assert bool((buf.as_strided((vocab - 1, ld - cols), (ld, 1), cols) == (0 if fl else FILL)).all())
 
 
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+def test_embedding_gradients_are_added_as_floats(kind):
+    """scale * sum is a float, and so is what it makes with the old value before the table's type: bit for
+    bit, of tokens within a tile and across tiles.  The sums themselves are whole numbers, so exact."""
+    T, R, W = types(kind)
+    rows, cols, vocab, scale = 700, 130, 40, 1.1
+    g = torch.Generator("cuda").manual_seed(2)
+    ids = tokens(rows, vocab, "skewed", False, 2)
+    dy = torch.randint(-3, 4, (rows, cols), generator=g, device="cuda").to(R)
+    sums = torch.zeros(vocab, cols, device="cuda").index_add_(0, ids.cuda(), dy.float())
+    old = torch.randn(vocab, cols, generator=g, device="cuda").to(W)
+    d = old.clone()
+    fn("embedding_backward", kind)(1, 0, rows, cols, 0.0, scale, flags(kind) | tk.TK_ACCUMULATE, vocab, on_device(ids, False), dy,
+                                   None, d, None)
+    product = sums * torch.full((), scale, device="cuda")
+    here = torch.bincount(ids, minlength=vocab).cuda()[:, None] > 0
+    assert torch.equal(d, torch.where(here, (product + old.float()).to(W), old))
+
+
 @pytest.mark.parametrize("vocab", [(1 << 25) + 700, (1 << 28) + 900], ids=["2^25", "2^28"])
 def test_embedding_gradient_of_more_tokens_than_a_grid(vocab):
     """The sort's work-groups take further ranges of tokens, and those that clear further rows."""
