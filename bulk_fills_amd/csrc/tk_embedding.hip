@@ -339,7 +339,10 @@ __global__ __launch_bounds__(256) void k_token_sums(GradArgs a) {
   }
 }
 
-// The tokens that go past the end of the tile where they begin, blockIdx.y: their lines, in order.
+// The tokens that go past the end of the tile where they begin, blockIdx.y: their lines, in order.  A thread
+// adds all of a token's lines at its column, eight loads ahead: 6 us where text-like tokens have 16384 rows of
+// 4096 bf16 columns, but about 50 ns a line where one token has very many (f32, 64 columns, tiles of 8: 26 us
+// for its 4096 rows, 418 for 65536).
 template <class W, bool kAdd>
 __global__ __launch_bounds__(256) void k_join(GradArgs a) {
   const uint64_t pitch = line_pitch(a.cols);

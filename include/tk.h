@@ -304,8 +304,12 @@ tk_status tk_dropout_add_layer_norm_backward_bf16(uint32_t key, uint64_t start_d
  *                           floats, and that rounded to dtable's type; rows of it whose token does not
  *                           occur are neither read nor written.  Without it every row is written, with
  *                           zeros where its token does not occur.
- * The gradient's sums are float, over the rows in their order: equal arguments give equal bits.
- * Nothing is updated concurrently, so a token of every row costs no more than others.
+ * The gradient's sums are float, in an order that the arguments fix: equal arguments give equal bits.
+ * Nothing is updated concurrently: the rows, sorted by token, are summed in pieces of 8 to 64, and the pieces of
+ * one token are then added one after the other.  So a token that has most of a call's rows makes it longer,
+ * the more rows and the narrower they are: bf16, vocabulary 32768, all rows one token's 250 us for 32768 x 64
+ * (evenly spread 29), 177 for 32768 x 512 (36), 111 for 16384 x 4096 (98).  A row of padding is best given
+ * an id that is no row of the table.
  *   scale must be finite, else TK_EINVAL; rows, cols, vocab and the lds are below 2^31, else TK_ERANGE.
  *   rows == 0 or cols == 0 is TK_OK, as is vocab == 0 (y is then zeros; the table may be NULL);
  *   a gradient over rows == 0 is zeros, or with TK_ACCUMULATE stays as it is.
