@@ -123,11 +123,15 @@ __device__ __forceinline__ void set_count(uint32_t *p, uint32_t n) {
 // in a column of its own, and after a scan over tokens and waves it puts its rows in their places.
 // Rows of one token keep their order, whatever the waves do, so a gradient's sum has one order.
 //
-// Bound by the work-group that has the most rows: of a text's tokens half are among the lowest hundred.
-// The lanes of one token find each other by votes, and the first of them moves its place on for all
-// (16384 rows of 32768 tokens, text-like: 15 us; with a turn of a loop for each of a wave's tokens 82;
-// evenly spread 12).  Counted by votes as well, so that the second pass has no more to do, the same rows
-// take 17 us, and 14 for 26 where all are one token's, whose counts wait for each other.
+// Bound by two passes over all rows' tokens in every work-group, whatever the tokens are, and beyond that by
+// the work-group that has the most rows of its own: of a text's tokens half are among the lowest hundred.
+// us, rows evenly spread, text-like, and all one token's:
+//                       4096 rows        16384 rows         65536 rows
+//      32768 tokens   7.3  7.7  9.9    12.0 15.2 26.1    27.4 48.2 93.1
+//     131072 tokens                    12.4 16.6 27.7    29.5 54.5 98.6
+// The lanes of one token find each other by votes, and the first of them moves its place on for all (with a
+// turn of a loop for each of a wave's tokens the 15.2 us are 82).  Counted by votes as well, so that the second
+// pass has no more to do, they are 17, and the 26 are 14, where the counts wait for each other.
 template <int kRange, bool kI64>
 __global__ __launch_bounds__(64 * kSortWaves) void k_sort_tokens(SortArgs a) {
   __shared__ uint32_t count[kSortWaves][kRange], begin_of[kRange], total_of[kRange], part[kSortWaves], under[kSortWaves];
@@ -230,7 +234,8 @@ struct GradArgs {
 // those lines up in the order of the tiles.
 //
 // Bound by memory: bf16 16384x4096 into a table of 32768 rows, text-like tokens, 68 us with the rows that are
-// cleared, 5.9 TB/s (with eight rows ahead, at fewer waves, 72; with a wave to each token and strip 128).
+// cleared, 6.0 TB/s of the 409 MB that the counters show (with eight rows ahead, at fewer waves, 72; with a wave
+// to each token and strip 128).
 template <class W, class R, bool kDivide, bool kAdd, int CH, int kLanes>
 struct Tile {
   static constexpr int kDeep = 4;
