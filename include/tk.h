@@ -357,6 +357,10 @@ tk_status tk_embedding_backward_bf16(uint32_t key, uint64_t start_draw, uint64_t
  *   _backward: g = dy turned back, h = x rstd: dgamma = sums of g h over rows and heads,
  *              dx = rstd (g gamma - h mean(g gamma h)); the statistics are made anew from x.
  * All matrices are of the operator's type; sums and angles are float, outputs are rounded once.
+ * The sum of a head's squares is a float as well: a head where it passes float's range (2^128: elements of
+ * 2^60 and more, as the lowest value of float or bfloat16 is) comes out as zeros, and so do its gradients; an
+ * element below 2^-75 adds nothing to it, so that a head of such alone gives infinities or NaN where eps is 0.
+ * NaN and infinity follow the formulas and stay in their head.
  *   flags: TK_PARAMS_F32 (gammas and their gradients are float), TK_INDEX_I64, TK_INTERLEAVED.
  *   Nullable: gammas (1), positions, dgammas, q's or k's arguments where their number of heads is 0,
  *          and the tables where rotary or table_rows is 0.

@@ -563,6 +563,45 @@ def test_heads_of_non_finite_values_and_zeros():
     assert not bool(yq[3, 80:].any())  # zeros give zeros: eps keeps the root away from them
 
 
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("kind", [KINDS[0], KINDS[3]], ids=["f32", "bf16"])
+def test_heads_beyond_floats_range(kind, interleaved):
+    """A head whose squares pass float's range is zeros, as are its gradients, and the other heads and the sums of
+    the gammas are as without it; with eps 0 a head whose squares vanish is infinite or NaN, alone."""
+    T, _, W = types(kind)
+    rows, hq, hk, dim = 5, 3, 2, 40
+    log(f"heads beyond float's range {kind} {interleaved}")
+    c = HeadCase(kind, rows, hq, hk, dim, 16, interleaved, 2)
+    g = torch.Generator("cuda").manual_seed(3)
+    q, k, dyq, dyk = (torch.randn(rows, n * dim, generator=g, device="cuda").to(T) for n in (hq, hk, hq, hk))
+    big = [(q, 1, 2, torch.finfo(T).min), (q, 3, 0, 2.0 ** 100), (k, 0, 1, torch.finfo(T).max)]  # matrix, row, head, value
+    at = lambda t, r, h: t[r, h * dim:(h + 1) * dim]  # noqa: E731
+    outs = []
+    for with_big in (False, True):
+        for x, r, h, v in big:
+            at(x, r, h).fill_(0)  # a head of zeros: its h is 0 too, so nothing of it in the gammas' gradients
+            if with_big:
+                at(x, r, h)[torch.arange(h, dim, 7)] = v
+        o = [torch.full_like(t, FILL) for t in (q, k, q, k)] + [torch.empty(dim, dtype=W, device="cuda") for _ in range(2)]
+        c.forward(q, k, *o[:2])
+        c.backward(dyq, dyk, q, k, *o[2:])
+        outs.append(o)
+    for x, r, h, _ in big:
+        i = 0 if x is q else 1
+        assert not bool(at(outs[1][i], r, h).any()) and not bool(at(outs[1][i + 2], r, h).any())
+        assert not bool(at(outs[0][i], r, h).any())
+        at(outs[0][i + 2], r, h).fill_(0)  # zeros have a gradient, at 1 / sqrt(eps)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    q = torch.randn(rows, hq * dim, generator=g, device="cuda").to(T)
+    at(q, 2, 1).fill_(2.0 ** -80)
+    y = torch.full_like(q, FILL)
+    fn("head_norm_rotate", kind)(rows, hq, 0, dim, 0, 0.0, 0, q, None, None, None, None, None, None, 0, None, None, y, None, None, None)
+    assert not bool(at(y, 2, 1).isfinite().any())
+    at(y, 2, 1).fill_(0)
+    assert bool(y.isfinite().all())
+
+
 # ---- checkpoints ----
 CODED = [(1, 1), (3, 7), (2, 8), (5, 9), (4, 127), (9, 128), (3, 129), (33, 200), (2, 1000), (70, 256), (5, 2049), (130, 513),
          (1, 70001)]
