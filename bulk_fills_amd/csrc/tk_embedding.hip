@@ -30,7 +30,12 @@ __device__ __forceinline__ uint64_t token(const void *ids, bool ids64, uint64_t 
 // A lane takes V chunks, 64 apart.  Rows come from anywhere in the table, so nothing is gained by going
 // on from one to the next: many waves hide the two loads that wait for each other (the token, then its
 // row).  kWide: a wave takes 64 V chunks of one row, whose token and address are the scalar unit's; else
-// (V = 1) the chunks of all rows follow each other.
+// (V = 1) the chunks of all rows follow each other.  From 64 chunks on, which gains on long rows and loses where
+// the row's last wave has many lanes idle.  us, wide and chunk by chunk, 2^25 elements from a table of 32768 rows:
+//      columns              512       1024       1152       1536       2048       4096
+//      bf16              22.9 20.6  21.0 20.7  23.8 20.9  22.3 20.9  21.3 21.0  21.4 21.0 (16384x4096 of 131072: 47.5 55.9)
+//      bf16, dropout     31.3 22.6  22.2 22.1  28.3 22.5  23.7 22.3  22.2 22.3  22.5 22.2
+//      f32               39.2 38.7  39.4 38.8  40.2 39.2  39.6 39.1  39.8 39.0  40.8 44.4
 template <class W, class R, bool kDivide, int CH, bool kWide, int V>
 __global__ __launch_bounds__(256) void k_embedding(LookupArgs a) {
   uint32_t n, r, c;
