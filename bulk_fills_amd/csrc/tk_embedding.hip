@@ -386,8 +386,13 @@ __global__ __launch_bounds__(256) void k_join(GradArgs a) {
 // Launches
 // ---------------------------------------------------------------------------------------
 // Places to a tile: 8, 16, 32 or 64, the most that leave kUnits waves' work, eight to a compute unit (and no
-// more than the lanes of a strip, which hold them).  The gradient bf16 16384x4096 takes 96.0, 96.1, 97.4 and
-// 112 us with 1024, 2048, 4096 and 8192, which leave more partial lines.
+// more than the lanes of a strip, which hold them).  More units leave more partial lines, fewer leave compute
+// units without work.  The gradient's us, bf16, rows evenly spread and text-like, with 1024, 2048 and 4096 units:
+//     65536x256  of 32768 tokens  48.4 45.8 50.2    74.3 77.1 90.7
+//     16384x1024                  31.5 34.6 37.8    35.9 38.8 43.7
+//     65536x1024                  80.4 80.0 85.9     101  101  105
+//     16384x4096                  98.3 98.2  101    93.4 93.9 95.8
+//     4096x1024, 65536x4096, 2047x1001 of 50001: within 1 %
 constexpr uint64_t kUnits = 2048;
 
 struct TilePlan {
