@@ -836,6 +836,55 @@ def test_backward_from_codes_is_that_of_their_values(kind, cols):
             assert torch.equal(a, b)
 
 
+def test_rows_beyond_32_bits():
+    """Heads and checkpoints whose last rows begin past 2^32 elements, at the largest row distance: the bits of
+    dense rows, and nothing written beside the rows."""
+    rows, ld, hq, hk, dim = 4, (1 << 31) - 1, 3, 2, 64
+    cols = (hq + hk) * dim
+    log("rows beyond 32 bits")
+    g = torch.Generator("cuda").manual_seed(6)
+    x, dy = (torch.randn(rows, cols, generator=g, device="cuda").bfloat16() for _ in range(2))
+    far = torch.full((3 * ld + cols + 9,), FILL, dtype=torch.bfloat16, device="cuda")
+    at = far.as_strided((rows, cols), (ld, 1))
+    beside = lambda b: all(bool((b[r * ld + cols:r * ld + cols + 9] == FILL).all()) for r in range(rows))  # noqa: E731
+    angle = torch.rand(rows, 32, generator=g, device="cuda") * 7
+    shape = (rows, hq, hk, dim, dim, 1e-5, 0)
+    tail = (None, None, None, rows, angle.cos(), angle.sin())
+    q, k = slice(0, hq * dim), slice(hq * dim, cols)
+    y, d = (torch.full((rows, cols), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tk.tk_head_norm_rotate_bf16(*shape, x[:, q], None, x[:, k], None, *tail, y[:, q], None, y[:, k], None)
+    at.copy_(x)
+    tk.tk_head_norm_rotate_bf16(*shape, at[:, q], None, at[:, k], None, *tail, at[:, q], None, at[:, k], None)
+    assert torch.equal(at, y) and beside(far)
+    tk.tk_head_norm_rotate_backward_bf16(*shape, dy[:, q], None, dy[:, k], None, x[:, q], None, x[:, k], None, *tail, d[:, q], None,
+                                         d[:, k], None, None, None)
+    at.copy_(x)
+    tk.tk_head_norm_rotate_backward_bf16(*shape, dy[:, q], None, dy[:, k], None, at[:, q], None, at[:, k], None, *tail, at[:, q], None,
+                                         at[:, k], None, None, None)
+    assert torch.equal(at, d) and beside(far)
+    at.copy_(x)
+    codes, scales = torch.empty(rows, cols, dtype=torch.int8, device="cuda"), torch.empty(rows, 3, device="cuda")
+    tk.tk_checkpoint_bf16(1, 2, rows, cols, 0, x, None, codes, None, scales)
+    far_codes, far_scales = torch.full((3 * ld + cols + 9,), int(FILL), dtype=torch.int8, device="cuda"), torch.empty(rows, 3, device="cuda")
+    at_codes = far_codes.as_strided((rows, cols), (ld, 1))
+    tk.tk_checkpoint_bf16(1, 2, rows, cols, 0, at, None, at_codes, None, far_scales)
+    assert torch.equal(at_codes, codes) and torch.equal(far_scales, scales) and beside(far_codes)
+    tk.tk_checkpoint_restore_bf16(rows, cols, 0, codes, None, scales, y, None)
+    tk.tk_checkpoint_restore_bf16(rows, cols, 0, at_codes, None, scales, at, None)
+    assert torch.equal(at, y) and beside(far)
+    mean, rstd = x.float().mean(1), x.float().var(1).rsqrt()
+    dx, dr = (torch.full((rows, cols), FILL, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    sums = [torch.empty(cols, dtype=torch.bfloat16, device="cuda") for _ in range(6)]
+    tk.tk_dropout_add_layer_norm_backward_checkpoint_bf16(1, 2, rows, cols, 0.1, 0, dy, None, None, None, codes, None, scales, None, mean,
+                                                          rstd, dx, None, dr, None, *sums[:3])
+    at.copy_(dy)
+    tk.tk_dropout_add_layer_norm_backward_checkpoint_bf16(1, 2, rows, cols, 0.1, 0, at, None, None, None, at_codes, None, scales, None,
+                                                          mean, rstd, at, None, d, None, *sums[3:])
+    assert torch.equal(at, dx) and torch.equal(d, dr) and beside(far)
+    for a, b in zip(sums[:3], sums[3:]):
+        assert torch.equal(a, b)
+
+
 # ---- together ----
 class Step:
     """A training step's run: tokens -> embedding -> checkpoint -> layer norm -> head norms of slices of the norm's
